@@ -276,6 +276,68 @@ int ttt_layer_host(ttt_weights W, const void* hQ, const void* hK, const void* hV
                    int grid_w, ttt_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* dbuf, size_t dbuf_bytes,
                    void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: a linear fast weight S in R^{dv x dk} per value head,
+ * written and read token by token,
+ *     S~_t = exp(g_t) S_{t-1},   u_t = beta_t (v_t - S~_t k^_t),
+ *     S_t = S~_t + u_t k^_t^T,   o_t = scale S_t q^_t,
+ * with q^, k^ the L2-normalised q, k (io->qk_l2norm = 1, as in ttt_apply) or q, k
+ * themselves.  It is the per-token counterpart of the chunk-wise Muon update
+ * above (no counterpart in the pages, which update per chunk).
+ *  - Heads: value head h reads query/key head h / (heads_v / heads_qk); heads_v
+ *    is a multiple of heads_qk.  Q, K: [T][ld] with head h in columns [h*dk,
+ *    (h+1)*dk); V, O: head h in columns [h*dv, (h+1)*dv); the ld_* of
+ *    ttt_io_cfg, 0 meaning heads*d.
+ *  - g (log decay, usually <= 0; g > 0 grows the state and is allowed while
+ *    exp of its sums stays finite), beta: float [T][heads_v], contiguous.
+ *  - States are float [..][heads_v][dv][dk], contiguous; they are never rounded
+ *    to fewer bits.
+ *  - dk, dv multiples of 8, dk <= 256, dv <= 1024; heads_v <= 4096; other
+ *    shapes return TTT_ERR_UNSUPPORTED.  Token rows and pointers are 16-byte
+ *    aligned (TTT_ERR_ALIGN), g and beta 4-byte.
+ *  - A non-finite token, gate or state makes undefined the outputs of its chunk
+ *    of 64 tokens (earlier tokens of that chunk too) and of all later tokens of
+ *    its sequence and head; other sequences are not touched by it.
+ *  - Outputs may not overlap inputs or each other, except S with S0. */
+typedef struct { int heads_qk, heads_v, dk, dv; } ttt_delta_dims;
+
+/* Workspace bytes for ttt_delta_chunked (backward = 0) or both it and
+ * ttt_delta_chunked_backward (backward = 1) over at most T tokens in at most
+ * n_seq sequences; 256-byte aligned, its status word cleared once
+ * (ttt_reset_status) before the first call and read with ttt_poll_status.
+ * Calls that can overlap, and captured graphs that can replay at the same
+ * time, need a workspace each.  Returns 0 for invalid dims. */
+size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_dtype dtype, int backward);
+
+/* The rule over n_seq packed sequences, in chunks of 64 tokens.
+ *  - cu_seqlens: device int32 [n_seq + 1], sequence i being tokens
+ *    [cu[i], cu[i+1]); lengths of 0 are allowed, and tokens before cu[0] or from
+ *    cu[n_seq] on are neither read nor written.  NULL: n_seq sequences of T /
+ *    n_seq tokens (T a multiple of n_seq).  Offsets that decrease or leave
+ *    [0, T] are found on the device: ttt_poll_status then reports
+ *    TTT_ERR_INVALID, and while an error is recorded these calls write nothing.
+ *  - S0: state before each sequence [n_seq][heads_v][dv][dk], NULL for zeros.
+ *    S: state after each (a sequence of length 0 keeps S0), may be S0 itself
+ *    or NULL.  Passing S as the next call's S0 resumes the sequences.
+ *  - TTT_BF16: bf16 Q, K, V, O on the tensor cores, with fp32-precise products
+ *    (operands split in two fp16 parts); TTT_FP32: float Q, K, V, O, token by
+ *    token on the CUDA cores (the precision check, and short sequences).
+ *  - T up to 2^31 - 1. */
+int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
+                      float* S, void* O, const int32_t* cu_seqlens, int n_seq, int64_t T, float scale,
+                      ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* One token for each of B sequences whose states live in a pool (decoding):
+ * S: float [n_slots][heads_v][dv][dk], updated in place.  slots: device int32
+ * [B], row b's place in the pool; a slot outside [0, n_slots) marks a padding
+ * row, whose O is left as it was.  Rows of the same slot are consecutive tokens
+ * of that sequence, in row order.  slots NULL: row b uses slot b (B <= n_slots).
+ * One launch, no workspace; both dtypes. */
+int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, const float* beta, float* S,
+                   int n_slots, const int32_t* slots, void* O, int64_t B, float scale, ttt_delta_dims dims,
+                   const ttt_io_cfg* io, ttt_dtype dtype, void* stream);
+
 /* Diagnostic for the timeout path: launches one single-warp kernel that waits on
  * a barrier nothing ever signals, with a wait limit of `timeout_us`
  * microseconds.  The wait gives up, records TTT_ERR_TIMEOUT in the workspace
@@ -314,7 +376,9 @@ typedef enum {
   TTT_PROF_CONV = 4,    /* ShortConv2D */
   TTT_PROF_REDUCE = 5,  /* split-K reduction of the gradient partials */
   TTT_PROF_SHADOW = 6,  /* bf16 copies of the fast weights */
-  TTT_PROF_KINDS = 7
+  TTT_PROF_DELTA = 7,   /* gated delta rule (all its kernels) */
+  TTT_PROF_BNORM = 8,   /* block norms, forward and backward */
+  TTT_PROF_KINDS = 9
 } ttt_prof_kind;
 
 int ttt_profile_enable(int on);

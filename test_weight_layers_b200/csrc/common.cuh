@@ -18,8 +18,8 @@
 
 namespace ttt {
 
-// device status codes (positive; the host maps them to TTT_ERR_TIMEOUT and TTT_ERR_RANGE)
-enum : unsigned int { DEV_OK = 0, DEV_TIMEOUT = 5, DEV_RANGE = 6 };
+// device status codes (positive; the host maps them to TTT_ERR_INVALID, TTT_ERR_TIMEOUT and TTT_ERR_RANGE)
+enum : unsigned int { DEV_OK = 0, DEV_INVALID = 1, DEV_TIMEOUT = 5, DEV_RANGE = 6 };
 
 constexpr int ETA_PARTS = 128;    // partial maxima of |eta| (k_eta_absmax) that fix the value scale
 
@@ -126,7 +126,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // Wait until the phase with the given parity has completed.  Returns false
 // (after recording DEV_TIMEOUT) if it does not within g.timeout ns, or early
 // if another thread of the grid already recorded an error.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, const Guard& g) {
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, const Guard& g) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -376,7 +376,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 
 // bounded wait with cluster-scope acquire (for barriers that receive arrivals from the peer CTA)
-__device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t* bar, uint32_t parity, const Guard& g) {
+static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t* bar, uint32_t parity, const Guard& g) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;

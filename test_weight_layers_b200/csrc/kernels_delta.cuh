@@ -1,0 +1,664 @@
+// Gated delta rule, chunked form (bf16 tokens): chunk table, chunk preparation
+// and the state pass.  The formulas and the operand scheme are in
+// delta_common.cuh.
+#pragma once
+
+#include "delta_common.cuh"
+
+namespace ttt {
+
+// ---------------------------------------------------------------------------
+// Chunk table.  One block: checks the offsets (0 <= cu[i] <= cu[i+1] <= T),
+// writes each sequence's first chunk and each chunk's first token and length.
+// Refused offsets, or an error already recorded in the status word, mark every
+// sequence with length -1: the kernels after it then write nothing.
+__global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu, int n_seq, int T, int max_chunks,
+                                                     DrSeq* __restrict__ seqs, DrChunk* __restrict__ chunks,
+                                                     unsigned int* status) {
+  __shared__ int warp_sum[32];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = *(volatile unsigned int*)status != DEV_OK;
+  const int even = n_seq > 0 ? T / n_seq : 0;  // without offsets: sequences of equal length
+  if (cu)
+    for (int i = tid; i < n_seq; i += 1024) {
+      const int a = cu[i], b = cu[i + 1];
+      if (a < 0 || b < a || b > T) {
+        bad = true;
+        atomicCAS(status, (unsigned int)DEV_OK, (unsigned int)DEV_INVALID);
+      }
+    }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int i0 = 0; i0 < n_seq; i0 += 1024) {
+    const int i = i0 + tid;
+    int tok = 0, len = 0;
+    if (i < n_seq) {
+      tok = cu ? cu[i] : i * even;
+      len = bad ? -1 : (cu ? cu[i + 1] - tok : even);
+    }
+    const int n = len > 0 ? (len + DR_C - 1) / DR_C : 0;
+    int sum = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      int w = warp_sum[lane];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += v;
+      }
+      warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const int first = carry + sum - n + (warp ? warp_sum[warp - 1] : 0);
+    if (i < n_seq) seqs[i] = DrSeq{tok, len, first, 0};
+    __syncthreads();
+    if (tid == 1023) carry = first + n;
+    __syncthreads();
+  }
+  const int total = carry;
+  __threadfence_block();
+  __syncthreads();
+  for (int c = tid; c < max_chunks; c += 1024) {
+    DrChunk e{0, -1};
+    if (c < total) {
+      int lo = 0, hi = n_seq - 1;  // the last sequence whose first chunk is <= c (empty ones before it share it)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seqs[mid].chunk0 <= c) lo = mid;
+        else hi = mid - 1;
+      }
+      const DrSeq s = seqs[lo];
+      const int at = (c - s.chunk0) * DR_C;
+      e.tok = s.tok + at;
+      e.len = min(DR_C, s.len - at);
+    }
+    chunks[c] = e;
+  }
+  pdl_trigger();
+}
+
+// ---------------------------------------------------------------------------
+// Chunk preparation: one block per (chunk, query/key head), for all value heads
+// that share it.  Writes K16 and Q16 (the token rows, exact in fp16, as
+// shared-memory images for the next kernels' bulk copies) and per value head
+// Y (hi, lo), P and the chunk vectors.
+struct PrepArgs {
+  const __nv_bfloat16 *Q, *K;
+  const float *g, *beta;  // [T][heads_v]
+  int64_t ldq, ldk;
+  int hk, hv, dk, l2norm;
+  float scale;
+  const DrChunk* chunks;
+  uint8_t* kq;   // [chunk][hk][K16 | Q16]
+  uint8_t* blk;  // [chunk][hv][blk_bytes]
+  int blk_bytes;
+  float* fkq;    // [chunk][hk][2][64] factors f_k, f_q (backward only, else null)
+};
+
+constexpr int PREP_LD = 68;  // floats per row of the fp32 64 x 64 tiles
+
+template <int DK>
+constexpr int prep_smem() {
+  return 2 * DR_C * DK * 2 + 4 * DR_C * PREP_LD * 4 + DR_C * 8 + 8 * DR_C * 4;
+}
+
+// Row scale (a power of two) of row `i`'s 64 floats at `p`, over both half-row threads.
+__device__ __forceinline__ int half_row_exp(const float* p, int half) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + half * 32 + j);
+    m = max_abs2(max_abs2(m, v.x, v.y), v.z, v.w);
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return row_exp(m, DR_ROW_EXP);
+}
+
+// Writes row i (this thread's half) of a 64 x 64 fp32 tile as fp16 hi and lo images.
+__device__ __forceinline__ void store_half_row(const float* p, int i, int half, float s, uint8_t* hi, uint8_t* lo) {
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    const float4 a = *reinterpret_cast<const float4*>(p + half * 32 + ch * 8);
+    const float4 b = *reinterpret_cast<const float4*>(p + half * 32 + ch * 8 + 4);
+    uint4 h, l;
+    split2(a.x * s, a.y * s, h.x, l.x);
+    split2(a.z * s, a.w * s, h.y, l.y);
+    split2(b.x * s, b.y * s, h.z, l.z);
+    split2(b.z * s, b.w * s, h.w, l.w);
+    const uint32_t off = img_off(i, half * 4 + ch, 128);
+    *reinterpret_cast<uint4*>(hi + off) = h;
+    if (lo) *reinterpret_cast<uint4*>(lo + off) = l;
+  }
+}
+
+template <int DK, bool BACK>
+__global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* k16 = smem;
+  uint8_t* q16 = k16 + DR_C * DK * 2;
+  float* KK = reinterpret_cast<float*>(q16 + DR_C * DK * 2);  // raw products of the scaled rows
+  float* QK = KK + DR_C * PREP_LD;
+  float* Lm = QK + DR_C * PREP_LD;
+  float* Ym = Lm + DR_C * PREP_LD;
+  double* c = reinterpret_cast<double*>(Ym + DR_C * PREP_LD);
+  float* fk = reinterpret_cast<float*>(c + DR_C);
+  float* fq = fk + DR_C;
+  float* bet = fq + DR_C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ci = blockIdx.x, hq = blockIdx.y;
+  pdl_wait();
+  const DrChunk ch = a.chunks[ci];
+  if (ch.len < 0) return;
+
+  // token rows -> scaled fp16 images and their factors
+  uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
+#pragma unroll 1
+  for (int r = warp; r < 2 * DR_C; r += 4) {
+    const int row = r & (DR_C - 1);
+    const bool isq = r >= DR_C;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (row < ch.len && lane * 8 < a.dk) {
+      const __nv_bfloat16* p = isq ? a.Q + (int64_t)(ch.tok + row) * a.ldq : a.K + (int64_t)(ch.tok + row) * a.ldk;
+      raw = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)hq * a.dk + lane * 8));
+    }
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = (&raw.x)[j];
+      x[2 * j] = __uint_as_float(w << 16);
+      x[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = row_exp(m, DR_TOK_EXP);
+    const float s = pow2i(e);
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] *= s;
+      ss += x[j] * x[j];
+    }
+    if (lane * 8 < DK) {
+      uint4 h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) (&h.x)[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
+      const uint32_t off = img_off(row, lane, DK * 2);
+      *reinterpret_cast<uint4*>((isq ? q16 : k16) + off) = h;
+      *reinterpret_cast<uint4*>(kq + (isq ? DR_C * DK * 2 : 0) + off) = h;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) {
+      // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
+      const float inv = pow2i(-e), norm = sqrtf(ss);
+      float f = row < ch.len ? inv : 0.f;
+      if (a.l2norm && row < ch.len) f = norm * inv > 1e-12f ? 1.f / norm : inv * 1e12f;
+      if (isq) f *= a.scale;
+      (isq ? fq : fk)[row] = f;
+    }
+  }
+  __syncthreads();
+  if (BACK && tid < DR_C) {
+    float* f = a.fkq + ((int64_t)ci * a.hk + hq) * 2 * DR_C;
+    f[tid] = fk[tid];
+    f[DR_C + tid] = fq[tid];
+  }
+
+  // K16 K16^T and Q16 K16^T on and below the diagonal; warp w has rows [16 w, 16 w + 16)
+  {
+    const uint32_t kb = smem_u32(k16), qb = smem_u32(q16);
+    float ak[8][4], aq[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ak[n][j] = aq[n][j] = 0.f;
+#pragma unroll 2
+    for (int kt = 0; kt < DK / 16; ++kt) {
+      uint32_t fa[4], fb[4];
+      ldsm4(fa, addr_bk(kb, lane, warp * 16, kt * 2, DK * 2));
+      ldsm4(fb, addr_bk(qb, lane, warp * 16, kt * 2, DK * 2));
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        if (np > warp) break;
+        uint32_t b[4];
+        ldsm4(b, addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
+        mma_f16(ak[2 * np], fa, b[0], b[1]);
+        mma_f16(ak[2 * np + 1], fa, b[2], b[3]);
+        mma_f16(aq[2 * np], fb, b[0], b[1]);
+        mma_f16(aq[2 * np + 1], fb, b[2], b[3]);
+      }
+    }
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const int col = n * 8 + 2 * t, r0 = warp * 16 + g;
+      *reinterpret_cast<float2*>(KK + r0 * PREP_LD + col) = make_float2(ak[n][0], ak[n][1]);
+      *reinterpret_cast<float2*>(KK + (r0 + 8) * PREP_LD + col) = make_float2(ak[n][2], ak[n][3]);
+      *reinterpret_cast<float2*>(QK + r0 * PREP_LD + col) = make_float2(aq[n][0], aq[n][1]);
+      *reinterpret_cast<float2*>(QK + (r0 + 8) * PREP_LD + col) = make_float2(aq[n][2], aq[n][3]);
+    }
+  }
+
+  const int rep = a.hv / a.hk;
+#pragma unroll 1
+  for (int hr = 0; hr < rep; ++hr) {
+    const int h = hq * rep + hr;
+    uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * a.blk_bytes;
+    float* vec = reinterpret_cast<float*>(blk + 3 * DR_TILE);
+    __syncthreads();  // the tiles of the value head before are read
+    // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
+    if (tid < DR_C) {
+      const bool live = tid < ch.len;
+      const int64_t at = (int64_t)(ch.tok + tid) * a.hv + h;
+      double s = live ? (double)a.g[at] : 0.0;
+      bet[tid] = live ? a.beta[at] : 0.f;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += v;
+      }
+      c[tid] = s;
+    }
+    __syncthreads();
+    if (tid >= 32 && tid < DR_C) c[tid] += c[31];  // (c[31] itself is not written here)
+    __syncthreads();
+    // L and P, two threads to a row
+    const int i = tid >> 1, half = tid & 1;
+    {
+      const double cii = c[i];
+      const float fki = fk[i], fqi = fq[i];
+      float* L = Lm + i * PREP_LD;
+      float* P = Ym + i * PREP_LD;
+#pragma unroll 4
+      for (int j = half * 32; j < half * 32 + 32; ++j) {
+        float l = 0.f, p = 0.f;
+        if (j <= i) {
+          const float d = expf((float)(cii - c[j])) * fk[j];
+          p = d * fqi * QK[i * PREP_LD + j];
+          if (j < i) l = d * fki * KK[i * PREP_LD + j];
+        }
+        L[j] = l;
+        P[j] = p;
+      }
+      __syncwarp();
+      const int e = half_row_exp(P, half);
+      store_half_row(P, i, half, pow2i(e), blk + 2 * DR_TILE, BACK ? blk + DR_HBLK : nullptr);
+      if (!half) {
+        const double G = c[DR_C - 1];
+        const float ec = expf((float)cii), el = expf((float)(G - cii));
+        vec[DV_PS * DR_C + i] = pow2i(-e);
+        vec[DV_AR * DR_C + i] = ec * fki;
+        vec[DV_BETA * DR_C + i] = bet[i];
+        vec[DV_AO * DR_C + i] = ec * fqi;
+        vec[DV_AK * DR_C + i] = el * fki;
+        vec[DV_EG * DR_C + i] = expf((float)G);
+      }
+    }
+    __syncthreads();
+    // (I + L beta) Y = -L by forward substitution, one column to a thread
+    if (tid < DR_C) {
+      float w[DR_C];  // beta_j Y_j of this column
+#pragma unroll
+      for (int r = 0; r < DR_C; ++r) {
+        const float* L = Lm + r * PREP_LD;
+        float s0 = -L[tid], s1 = 0.f, s2 = 0.f, s3 = 0.f;  // L is zero on and above the diagonal
+#pragma unroll
+        for (int j = 0; j + 3 < r; j += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(L + j);
+          s0 -= l.x * w[j];
+          s1 -= l.y * w[j + 1];
+          s2 -= l.z * w[j + 2];
+          s3 -= l.w * w[j + 3];
+        }
+#pragma unroll
+        for (int j = r & ~3; j < r; ++j) s1 -= L[j] * w[j];
+        const float y = tid < r ? (s0 + s1) + (s2 + s3) : 0.f;
+        w[r] = bet[r] * y;
+        Ym[r * PREP_LD + tid] = y;
+      }
+    }
+    __syncthreads();
+    const int e = half_row_exp(Ym + i * PREP_LD, half);
+    store_half_row(Ym + i * PREP_LD, i, half, pow2i(e), blk, blk + DR_TILE);
+    if (!half) vec[DV_YS * DR_C + i] = pow2i(-e);
+  }
+  pdl_trigger();
+}
+
+// ---------------------------------------------------------------------------
+// State pass: the recurrence over the chunks of a sequence.  The rows of S
+// (value channels) do not meet, so a warp owns 16 of them and keeps them in
+// registers for the whole sequence, S^T-free: S [16][dk] as accumulators is at
+// once the A operand of S K^T, the errors R^T [16][64] that of (beta R)^T Y^T,
+// the writes U^T that of U^T K and U^T P^T.  No warp waits for another inside
+// a chunk; shared memory holds only what all warps read (K16, Q16, Y, P),
+// brought by bulk copies one chunk ahead.
+struct StateArgs {
+  const __nv_bfloat16* V;
+  __nv_bfloat16* O;
+  int64_t ldv, ldo;
+  const float* S0;
+  float* S;
+  int hk, hv, dk, dv;
+  const DrSeq* seqs;
+  const uint8_t* kq;
+  const uint8_t* blk;
+  int blk_bytes;
+  Guard guard;
+};
+
+constexpr int DR_VROW = 48;                  // bytes per row of a warp's V / O tile (32 used): conflict-free 8x8 tiles
+constexpr int DR_VTILE = DR_C * DR_VROW;
+
+template <int DK>
+constexpr int state_stage() {
+  return 2 * DR_C * DK * 2 + DR_HBLK;
+}
+template <int DK>
+constexpr int state_smem(int warps) {
+  return 2 * state_stage<DK>() + warps * 2 * DR_VTILE + 64;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int STAGE = state_stage<DK>();
+  constexpr int KQ = 2 * DR_C * DK * 2;
+  constexpr int NT = DK / 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* vbuf = smem + 2 * STAGE + warp * 2 * DR_VTILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * 2 * DR_VTILE);
+  const int h = blockIdx.z, hq = h / (a.hv / a.hk);
+  const int v0 = (blockIdx.y * nwarp + warp) * 16;  // first value channel of this warp (may lie past dv)
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const DrSeq sq = a.seqs[blockIdx.x];
+  __syncthreads();
+  if (sq.len < 0) return;
+  const int nchunk = (sq.len + DR_C - 1) / DR_C;
+
+  auto load_stage = [&](int n) {  // one thread
+    const int64_t ci = sq.chunk0 + n;
+    uint8_t* st = smem + (n & 1) * STAGE;
+    mbar_expect_tx(&full[n & 1], KQ + DR_HBLK);
+    bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, &full[n & 1]);
+    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, DR_HBLK, &full[n & 1]);
+  };
+  auto load_v = [&](int n) {  // this warp's 64 x 16 tile of V, zero outside the sequence and the head
+    const uint32_t dst = smem_u32(vbuf + (n & 1) * DR_VTILE);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int row = it * 16 + (lane >> 1), half = lane & 1;
+      const int at = n * DR_C + row;
+      const bool live = at < sq.len && v0 + half * 8 < a.dv;
+      const __nv_bfloat16* p = live ? a.V + (int64_t)(sq.tok + at) * a.ldv + (int64_t)h * a.dv + v0 + half * 8 : a.V;
+      cp_async16(dst + row * DR_VROW + half * 16, p, live);
+    }
+    cp_commit();
+  };
+
+  float s[NT][4];
+  const int64_t srow = ((int64_t)blockIdx.x * a.hv + h) * a.dv;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+      float2 x = make_float2(0.f, 0.f);
+      if (a.S0 && r < a.dv && col < a.dk) x = *reinterpret_cast<const float2*>(a.S0 + (srow + r) * a.dk + col);
+      s[n][2 * p] = x.x;
+      s[n][2 * p + 1] = x.y;
+    }
+  float inv0 = 1.f, inv1 = 1.f;  // S = s * inv: rows g and g + 8 carry a power of two
+
+  if (nchunk > 0) {
+    if (tid == 0) load_stage(0);
+    load_v(0);
+  }
+#pragma unroll 1
+  for (int n = 0; n < nchunk; ++n) {
+    if (n + 1 < nchunk) {
+      if (tid == 0) load_stage(n + 1);
+      load_v(n + 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncwarp();
+    // a wait that gives up records the error; the pass then runs on (bounded) with what the stage holds
+    mbar_wait(&full[n & 1], (n >> 1) & 1, a.guard);
+    const uint32_t st = smem_u32(smem + (n & 1) * STAGE);
+    const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, pb = yl + DR_TILE;
+    const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + KQ + 3 * DR_TILE);
+    const uint32_t vb = smem_u32(vbuf + (n & 1) * DR_VTILE);
+
+    // S K^T and S Q^T
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      m0 = max_abs2(m0, s[k][0], s[k][1]);
+      m1 = max_abs2(m1, s[k][2], s[k][3]);
+    }
+    const int e0 = row_exp(quad_max(m0), DR_ROW_EXP), e1 = row_exp(quad_max(m1), DR_ROW_EXP);
+    const float sc0 = pow2i(e0), sc1 = pow2i(e1);
+    float r[8][4], o[8][4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[k][j] = o[k][j] = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt) {
+      uint32_t hi[4], lo[4];
+      split_a(s[2 * kt], s[2 * kt + 1], sc0, sc1, hi, lo);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b[4];
+        ldsm4(b, addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
+        mma_f16(r[2 * np], hi, b[0], b[1]);
+        mma_f16(r[2 * np + 1], hi, b[2], b[3]);
+        mma_f16(r[2 * np], lo, b[0], b[1]);
+        mma_f16(r[2 * np + 1], lo, b[2], b[3]);
+        // the outputs are rounded to bf16: S's hi part alone (2^-12) is enough for them
+        ldsm4(b, addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
+        mma_f16(o[2 * np], hi, b[0], b[1]);
+        mma_f16(o[2 * np + 1], hi, b[2], b[3]);
+      }
+    }
+    // R = V - e^c K S^T, then the scale of beta R
+    const float is0 = inv0 * pow2i(-e0), is1 = inv1 * pow2i(-e1);
+    m0 = m1 = 0.f;
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t v[4];
+      ldsm4t(v, vb + (np * 16 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k = 2 * np + q, col = k * 8 + 2 * t;
+        const float2 ar = *reinterpret_cast<const float2*>(vec + DV_AR * DR_C + col);
+        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+        const uint32_t x0 = v[2 * q], x1 = v[2 * q + 1];
+        r[k][0] = __uint_as_float(x0 << 16) - ar.x * (r[k][0] * is0);
+        r[k][1] = __uint_as_float(x0 & 0xffff0000u) - ar.y * (r[k][1] * is0);
+        r[k][2] = __uint_as_float(x1 << 16) - ar.x * (r[k][2] * is1);
+        r[k][3] = __uint_as_float(x1 & 0xffff0000u) - ar.y * (r[k][3] * is1);
+        m0 = max_abs2(m0, be.x * r[k][0], be.y * r[k][1]);
+        m1 = max_abs2(m1, be.x * r[k][2], be.y * r[k][3]);
+      }
+    }
+    // E = R + Y (beta R); the diagonal is not part of Y, so only tiles with i >= j
+    {
+      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+      const float w0 = pow2i(f0), w1 = pow2i(f1);
+      float x[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        float b0[4], b1[4];
+        const float2 ba = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + kt * 16 + 2 * t);
+        const float2 bb = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + kt * 16 + 8 + 2 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          b0[j] = r[2 * kt][j] * (j & 1 ? ba.y : ba.x);
+          b1[j] = r[2 * kt + 1][j] * (j & 1 ? bb.y : bb.x);
+        }
+        uint32_t hi[4], lo[4];
+        split_a(b0, b1, w0, w1, hi, lo);
+#pragma unroll
+        for (int np = kt; np < 4; ++np) {
+          uint32_t y[4];
+          ldsm4(y, addr_bn(yh, lane, np * 16, kt * 2, 128));
+          mma_f16(x[2 * np], hi, y[0], y[1]);
+          mma_f16(x[2 * np + 1], hi, y[2], y[3]);
+          mma_f16(x[2 * np], lo, y[0], y[1]);
+          mma_f16(x[2 * np + 1], lo, y[2], y[3]);
+          ldsm4(y, addr_bn(yl, lane, np * 16, kt * 2, 128));
+          mma_f16(x[2 * np], hi, y[0], y[1]);
+          mma_f16(x[2 * np + 1], hi, y[2], y[3]);
+        }
+      }
+      const float i0 = pow2i(-f0), i1 = pow2i(-f1);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = k * 8 + 2 * t;
+        const float2 ys = *reinterpret_cast<const float2*>(vec + DV_YS * DR_C + col);
+        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+        r[k][0] = be.x * (r[k][0] + ys.x * (x[k][0] * i0));  // r becomes U
+        r[k][1] = be.y * (r[k][1] + ys.y * (x[k][1] * i0));
+        r[k][2] = be.x * (r[k][2] + ys.x * (x[k][2] * i1));
+        r[k][3] = be.y * (r[k][3] + ys.y * (x[k][3] * i1));
+      }
+    }
+    // O = e^c Q S^T + P U, accumulated in U's scale over P's row scales
+    {
+      m0 = m1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m0 = max_abs2(m0, r[k][0], r[k][1]);
+        m1 = max_abs2(m1, r[k][2], r[k][3]);
+      }
+      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+      const float w0 = pow2i(f0), w1 = pow2i(f1), i0 = pow2i(-f0), i1 = pow2i(-f1);
+      float x[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        uint32_t hi[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          hi[2 * q] = pack_f16x2(r[2 * kt + q][0] * w0, r[2 * kt + q][1] * w0);
+          hi[2 * q + 1] = pack_f16x2(r[2 * kt + q][2] * w1, r[2 * kt + q][3] * w1);
+        }
+#pragma unroll
+        for (int np = kt; np < 4; ++np) {
+          uint32_t p[4];
+          ldsm4(p, addr_bn(pb, lane, np * 16, kt * 2, 128));
+          mma_f16(x[2 * np], hi, p[0], p[1]);
+          mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+        }
+      }
+      __syncwarp();  // every lane has read its V tile; O takes its place
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t y[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int k = 2 * np + q, col = k * 8 + 2 * t;
+          const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
+          const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
+          y[2 * q] = pack_bf16x2(ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * i0),
+                                 ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * i0));
+          y[2 * q + 1] = pack_bf16x2(ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * i1),
+                                     ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * i1));
+        }
+        stsm4t(vb + (np * 16 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4), y[0], y[1], y[2],
+               y[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int row = it * 16 + (lane >> 1), half = lane & 1;
+        const int at = n * DR_C + row;
+        if (at < sq.len && v0 + half * 8 < a.dv)
+          *reinterpret_cast<uint4*>(a.O + (int64_t)(sq.tok + at) * a.ldo + (int64_t)h * a.dv + v0 + half * 8) =
+              *reinterpret_cast<const uint4*>(vbuf + (n & 1) * DR_VTILE + row * DR_VROW + half * 16);
+      }
+    }
+    // S' = e^{c_C} S + (e^{c_C - c} U)^T K, with S brought to the scale of the added term
+    {
+      m0 = m1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 ak = *reinterpret_cast<const float2*>(vec + DV_AK * DR_C + k * 8 + 2 * t);
+        r[k][0] *= ak.x;
+        r[k][1] *= ak.y;
+        r[k][2] *= ak.x;
+        r[k][3] *= ak.y;
+        m0 = max_abs2(m0, r[k][0], r[k][1]);
+        m1 = max_abs2(m1, r[k][2], r[k][3]);
+      }
+      // (a state far larger than what is added bounds the scale, so that it cannot overflow)
+      const int f0 = min(row_exp(quad_max(m0), DR_ROW_EXP), 87 - exp_of(is0));
+      const int f1 = min(row_exp(quad_max(m1), DR_ROW_EXP), 87 - exp_of(is1));
+      const float w0 = pow2i(f0), w1 = pow2i(f1);
+      const float eg = vec[DV_EG * DR_C];
+      const float d0 = eg * inv0 * w0, d1 = eg * inv1 * w1;
+      inv0 = pow2i(-f0);
+      inv1 = pow2i(-f1);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        s[k][0] *= d0;
+        s[k][1] *= d0;
+        s[k][2] *= d1;
+        s[k][3] *= d1;
+      }
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        uint32_t hi[4], lo[4];
+        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np) {
+          uint32_t b[4];
+          ldsm4t(b, addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
+          mma_f16(s[2 * np], hi, b[0], b[1]);
+          mma_f16(s[2 * np + 1], hi, b[2], b[3]);
+          mma_f16(s[2 * np], lo, b[0], b[1]);
+          mma_f16(s[2 * np + 1], lo, b[2], b[3]);
+        }
+      }
+    }
+    __syncthreads();  // the stage is read; the next copy into it may start
+  }
+  if (a.S) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+        const float i = p ? inv1 : inv0;
+        if (r < a.dv && col < a.dk)
+          *reinterpret_cast<float2*>(a.S + (srow + r) * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
+      }
+  }
+}
+
+}  // namespace ttt

@@ -1,0 +1,262 @@
+// C ABI of the gated delta rule (see include/ttt.h for the contract): argument
+// checks, workspace carving and the launch sequences.
+#include <algorithm>
+
+#include "host.cuh"
+#include "kernels_delta.cuh"
+#include "kernels_delta_seq.cuh"
+#include "ttt.h"
+
+using namespace ttt;
+
+namespace {
+
+struct DeltaWs {
+  unsigned int* status;
+  DrSeq* seqs;
+  DrChunk* chunks;
+  uint8_t* kq;
+  uint8_t* blk;
+  int blk_bytes;
+  int64_t max_chunks;
+  size_t total;
+};
+
+int dk_pad(int dk) { return (dk + 63) / 64 * 64; }
+
+bool delta_dims_ok(const ttt_delta_dims& d) {
+  return d.heads_qk >= 1 && d.heads_v >= 1 && d.dk >= 1 && d.dv >= 1 && d.heads_v % d.heads_qk == 0;
+}
+
+bool delta_dims_supported(const ttt_delta_dims& d) {
+  return d.dk % 8 == 0 && d.dv % 8 == 0 && d.dk <= 256 && d.dv <= 1024 && d.heads_v <= 4096;
+}
+
+DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward) {
+  DeltaWs w{};
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = b + off;
+    off = up256(off + bytes);
+    return p;
+  };
+  w.max_chunks = T / DR_C + n_seq;
+  w.blk_bytes = DR_HBLK;
+  w.status = reinterpret_cast<unsigned int*>(take(256));
+  w.seqs = reinterpret_cast<DrSeq*>(take((size_t)std::max(n_seq, 1) * sizeof(DrSeq)));
+  w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
+  if (dt == TTT_BF16) {
+    w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
+    w.blk = take((size_t)w.max_chunks * d.heads_v * w.blk_bytes);
+  }
+  w.total = off;
+  return w;
+}
+
+struct DeltaIo {
+  int64_t ldq, ldk, ldv, ldo;
+  int l2norm;
+};
+
+int check_rows(const void* p, int64_t ld, int64_t width, ttt_dtype dt) {
+  if (!p || ld < width) return TTT_ERR_INVALID;
+  if (!aligned16(p) || (ld * (int64_t)esize(dt)) % 16) return TTT_ERR_ALIGN;
+  return TTT_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks shared by the entry points; fills the row strides.
+int delta_check(const void* Q, const void* K, const void* V, const float* g, const float* beta, const void* O,
+                const ttt_delta_dims& d, const ttt_io_cfg* io, ttt_dtype dt, bool any_tokens, DeltaIo& out) {
+  const int64_t nq = (int64_t)d.heads_qk * d.dk, nv = (int64_t)d.heads_v * d.dv;
+  out.ldq = io->ld_q ? io->ld_q : nq;
+  out.ldk = io->ld_k ? io->ld_k : nq;
+  out.ldv = io->ld_v ? io->ld_v : nv;
+  out.ldo = io->ld_o ? io->ld_o : nv;
+  out.l2norm = io->qk_l2norm;
+  if (out.ldq < nq || out.ldk < nq || out.ldv < nv || out.ldo < nv) return TTT_ERR_INVALID;
+  if (!any_tokens) return TTT_OK;
+  TTT_TRY(check_rows(Q, out.ldq, nq, dt));
+  TTT_TRY(check_rows(K, out.ldk, nq, dt));
+  TTT_TRY(check_rows(V, out.ldv, nv, dt));
+  TTT_TRY(check_rows(O, out.ldo, nv, dt));
+  if (!g || !beta || O == Q || O == K || O == V) return TTT_ERR_INVALID;
+  return aligned4(g) && aligned4(beta) ? TTT_OK : TTT_ERR_ALIGN;
+}
+
+int smem_opt_in(const void* fn, int bytes) {
+  TTT_CHECK(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  return TTT_OK;
+}
+
+int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaStream_t s) {
+  k_delta_plan<<<1, 1024, 0, s>>>(cu, n_seq, (int)T, (int)w.max_chunks, w.seqs, w.chunks, w.status);
+  TTT_LAUNCHED();
+  return TTT_OK;
+}
+
+// Warps of a state-pass block (16 value channels each).  Fewer warps spread few heads over more SMs; more
+// share one staged copy of the chunk's operands.
+int state_warps(int64_t chains, int n16, int most) {
+  int w = std::min(most, 8);
+  while (w > 1 && chains * ((n16 + w - 1) / w) < sm_count()) w >>= 1;
+  while (w > 1 && (n16 + w - 1) / w == (n16 + w / 2 - 1) / (w / 2)) w >>= 1;  // no warps without channels
+  return w;
+}
+
+template <int DK>
+int run_delta_fwd(const PrepArgs& pa, StateArgs sa, int n_seq, const DeltaWs& w, cudaStream_t s) {
+  const int psm = prep_smem<DK>();
+  TTT_TRY(smem_opt_in((const void*)k_delta_prep<DK, false>, psm));
+  TTT_TRY(launch_pdl(k_delta_prep<DK, false>, dim3((unsigned)w.max_chunks, pa.hk), dim3(128), psm, s, pa));
+  TTT_LAUNCHED();
+  const int n16 = (sa.dv + 15) / 16;
+  const int warps = state_warps((int64_t)n_seq * sa.hv, n16, DK >= 256 ? 4 : 8);
+  const int ssm = state_smem<DK>(warps);
+  TTT_TRY(smem_opt_in((const void*)k_delta_state<DK>, ssm));
+  TTT_TRY(launch_pdl(k_delta_state<DK>, dim3(n_seq, (n16 + warps - 1) / warps, sa.hv), dim3(warps * 32), ssm, s, sa));
+  TTT_LAUNCHED();
+  return TTT_OK;
+}
+
+template <typename T, int VEC, int NV>
+int launch_tokens(const SeqArgs<T>& a, unsigned blocks, cudaStream_t s) {
+  constexpr int ROWS = NV * VEC > 4 ? 4 : 8;
+  const dim3 grid(blocks, a.hv, (a.dv + 4 * ROWS - 1) / (4 * ROWS));
+  if (a.seqs) {
+    TTT_TRY(launch_pdl(k_delta_tokens<T, VEC, NV, ROWS>, grid, dim3(128), 0, s, a));
+  } else {
+    k_delta_tokens<T, VEC, NV, ROWS><<<grid, 128, 0, s>>>(a);
+  }
+  TTT_LAUNCHED();
+  return TTT_OK;
+}
+
+template <typename T>
+int run_tokens(const SeqArgs<T>& a, unsigned blocks, cudaStream_t s) {
+  if (a.dk == 128) return launch_tokens<T, 4, 1>(a, blocks, s);
+  if (a.dk == 256) return launch_tokens<T, 4, 2>(a, blocks, s);
+  switch ((a.dk + 63) / 64) {
+    case 1: return launch_tokens<T, 2, 1>(a, blocks, s);
+    case 2: return launch_tokens<T, 2, 2>(a, blocks, s);
+    case 3: return launch_tokens<T, 2, 3>(a, blocks, s);
+    default: return launch_tokens<T, 2, 4>(a, blocks, s);
+  }
+}
+
+template <typename T>
+SeqArgs<T> seq_args(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
+                    float* S, void* O, float scale, const ttt_delta_dims& d, const DeltaIo& io) {
+  SeqArgs<T> a{};
+  a.Q = (const T*)Q;
+  a.K = (const T*)K;
+  a.V = (const T*)V;
+  a.O = (T*)O;
+  a.ldq = io.ldq;
+  a.ldk = io.ldk;
+  a.ldv = io.ldv;
+  a.ldo = io.ldo;
+  a.g = g;
+  a.beta = beta;
+  a.S0 = S0;
+  a.S = S;
+  a.hk = d.heads_qk;
+  a.hv = d.heads_v;
+  a.dk = d.dk;
+  a.dv = d.dv;
+  a.l2norm = io.l2norm;
+  a.scale = scale;
+  return a;
+}
+
+int delta_check_call(const ttt_delta_dims& d, ttt_dtype dt, int64_t T, int n_seq, bool packed, const ttt_io_cfg* io,
+                     bool backward, void* ws, size_t ws_bytes) {
+  if ((dt != TTT_FP32 && dt != TTT_BF16) || !delta_dims_ok(d) || T < 0 || n_seq < 0 || !io) return TTT_ERR_INVALID;
+  if (!delta_dims_supported(d) || T > INT32_MAX - DR_C) return TTT_ERR_UNSUPPORTED;
+  if (n_seq == 0 ? T > 0 && !packed : !packed && T % n_seq) return TTT_ERR_INVALID;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return TTT_ERR_WORKSPACE;
+  return ws_bytes < delta_carve(nullptr, d, T, n_seq, dt, backward).total ? TTT_ERR_WORKSPACE : TTT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_dtype dtype, int backward) {
+  if ((dtype != TTT_FP32 && dtype != TTT_BF16) || !delta_dims_ok(dims) || !delta_dims_supported(dims) || T < 0 ||
+      T > INT32_MAX - DR_C || n_seq < 0)
+    return 0;
+  return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0).total;
+}
+
+int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
+                      float* S, void* O, const int32_t* cu_seqlens, int n_seq, int64_t T, float scale,
+                      ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws, size_t ws_bytes,
+                      void* stream) {
+  TTT_TRY(delta_check_call(dims, dtype, T, n_seq, cu_seqlens != nullptr, io, false, ws, ws_bytes));
+  DeltaIo x;
+  TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, T > 0 && n_seq > 0, x));
+  if ((S0 && !aligned16(S0)) || (S && !aligned16(S)) || !aligned4(cu_seqlens)) return TTT_ERR_ALIGN;
+  if (n_seq == 0) return TTT_OK;
+  cudaStream_t s = (cudaStream_t)stream;
+  const DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, false);
+  ProfScope ps(TTT_PROF_DELTA, s);
+  TTT_TRY(launch_plan(cu_seqlens, n_seq, T, w, s));
+  if (dtype == TTT_FP32) {
+    SeqArgs<float> a = seq_args<float>(Q, K, V, g, beta, S0, S, O, scale, dims, x);
+    a.seqs = w.seqs;
+    return run_tokens<float>(a, (unsigned)n_seq, s);
+  }
+  PrepArgs pa{(const __nv_bfloat16*)Q, (const __nv_bfloat16*)K, g, beta, x.ldq, x.ldk, dims.heads_qk, dims.heads_v,
+              dims.dk, x.l2norm, scale, w.chunks, w.kq, w.blk, w.blk_bytes, nullptr};
+  StateArgs sa{};
+  sa.V = (const __nv_bfloat16*)V;
+  sa.O = (__nv_bfloat16*)O;
+  sa.ldv = x.ldv;
+  sa.ldo = x.ldo;
+  sa.S0 = S0;
+  sa.S = S;
+  sa.hk = dims.heads_qk;
+  sa.hv = dims.heads_v;
+  sa.dk = dims.dk;
+  sa.dv = dims.dv;
+  sa.seqs = w.seqs;
+  sa.kq = w.kq;
+  sa.blk = w.blk;
+  sa.blk_bytes = w.blk_bytes;
+  sa.guard = Guard{w.status, wait_timeout_ns()};
+  switch (dk_pad(dims.dk)) {
+    case 64: return run_delta_fwd<64>(pa, sa, n_seq, w, s);
+    case 128: return run_delta_fwd<128>(pa, sa, n_seq, w, s);
+    case 192: return run_delta_fwd<192>(pa, sa, n_seq, w, s);
+    default: return run_delta_fwd<256>(pa, sa, n_seq, w, s);
+  }
+}
+
+int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, const float* beta, float* S,
+                   int n_slots, const int32_t* slots, void* O, int64_t B, float scale, ttt_delta_dims dims,
+                   const ttt_io_cfg* io, ttt_dtype dtype, void* stream) {
+  if ((dtype != TTT_FP32 && dtype != TTT_BF16) || !delta_dims_ok(dims) || B < 0 || n_slots < 0 || !io)
+    return TTT_ERR_INVALID;
+  if (!delta_dims_supported(dims) || B > INT32_MAX / 2) return TTT_ERR_UNSUPPORTED;
+  if (!slots && B > n_slots) return TTT_ERR_INVALID;
+  DeltaIo x;
+  TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, B > 0, x));
+  if (B == 0) return TTT_OK;
+  if (!S) return TTT_ERR_INVALID;
+  if (!aligned16(S) || !aligned4(slots)) return TTT_ERR_ALIGN;
+  cudaStream_t s = (cudaStream_t)stream;
+  ProfScope ps(TTT_PROF_DELTA, s);
+  auto go = [&](auto a) {
+    a.slots = slots;
+    a.n_slots = n_slots;
+    a.rows = (int)B;
+    return run_tokens(a, (unsigned)B, s);
+  };
+  if (dtype == TTT_FP32) return go(seq_args<float>(Q, K, V, g, beta, S, S, O, scale, dims, x));
+  return go(seq_args<__nv_bfloat16>(Q, K, V, g, beta, S, S, O, scale, dims, x));
+}
+
+}  // extern "C"

@@ -46,6 +46,10 @@ class IOCfg(ctypes.Structure):
                 ("ld_v", ctypes.c_int64), ("ld_o", ctypes.c_int64)]
 
 
+class DeltaDims(ctypes.Structure):
+    _fields_ = [("heads_qk", ctypes.c_int), ("heads_v", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -79,6 +83,10 @@ def lib() -> ctypes.CDLL:
                                    ctypes.POINTER(IOCfg), I, P, SZ, P, SZ, P]),
             "ttt_gate_workspace_bytes": (SZ, [I64, I]),
             "ttt_output_gate": (I, [P, I64, P, P, I64, I64, I, I, P, SZ, P]),
+            "ttt_delta_workspace_bytes": (SZ, [DeltaDims, I64, I, I, I]),
+            "ttt_delta_chunked": (I, [P, P, P, P, P, P, P, P, P, I, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P, SZ,
+                                      P]),
+            "ttt_delta_step": (I, [P, P, P, P, P, P, I, P, P, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P]),
             "ttt_status_string": (ctypes.c_char_p, [I]),
             "ttt_compiled_arch": (I, []),
             "ttt_kernel_binary_version": (I, [ctypes.POINTER(I)]),
@@ -249,6 +257,89 @@ def ttt_layer_host(W: Weights, hQ, hK, hV, hEta, hO, T, chunk, order, steps, ns:
         _stream(stream)))
 
 
+def _same_device(*tensors):
+    """All given tensors on the current CUDA device, whose stream the call is queued on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _rows(name, t, rows, width, ld, dtype):
+    """A token matrix of at least `rows` rows of `width` columns, stored with row stride ld (0: width)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}][{width}] with unit column stride, got {tuple(t.shape)}")
+    if rows > 1 and t.stride(0) != (ld or width):
+        raise ValueError(f"{name} has row stride {t.stride(0)}, the call says {ld or width}")
+
+
+def _dense(name, t, shape, dtype=torch.float32):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def delta_dims(heads_qk: int, heads_v: int, dk: int, dv: int) -> DeltaDims:
+    return DeltaDims(heads_qk, heads_v, dk, dv)
+
+
+def delta_workspace(dm: DeltaDims, T: int, n_seq: int, dtype: int, backward: bool = False, device="cuda"):
+    """A zeroed workspace for ttt_delta_chunked (and its backward pass) over T tokens in n_seq sequences."""
+    n = int(lib().ttt_delta_workspace_bytes(dm, T, n_seq, dtype, 1 if backward else 0))
+    if n == 0:
+        raise TTTError("ttt_delta_workspace_bytes", TTT_ERR_UNSUPPORTED, "invalid or unsupported dims")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _delta_tokens(Q, K, V, g, beta, T, dm, io):
+    nq, nv = dm.heads_qk * dm.dk, dm.heads_v * dm.dv
+    _rows("Q", Q, T, nq, io.ld_q, K.dtype)
+    _rows("K", K, T, nq, io.ld_k, K.dtype)
+    _rows("V", V, T, nv, io.ld_v, K.dtype)
+    _dense("g", g, (T, dm.heads_v))
+    _dense("beta", beta, (T, dm.heads_v))
+
+
+def _delta_states(dm, n, **states):
+    for name, t in states.items():
+        if t is not None:
+            _dense(name, t, (n, dm.heads_v, dm.dv, dm.dk))
+
+
+def _offsets(cu_seqlens, n_seq):
+    if cu_seqlens is not None:
+        _dense("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32)
+
+
+def ttt_delta_chunked(Q, K, V, g, beta, S0, S, O, T, dm: DeltaDims, io: IOCfg, ws, cu_seqlens=None, n_seq=1,
+                      scale=1.0, stream=None):
+    """The gated delta rule over n_seq packed sequences: O, and the states S after them (S0 before; either may be
+    None).  cu_seqlens: int32 CUDA tensor [n_seq + 1], None for sequences of equal length."""
+    _same_device(Q, K, V, g, beta, S0, S, O, cu_seqlens, ws)
+    _delta_tokens(Q, K, V, g, beta, T, dm, io)
+    _rows("O", O, T, dm.heads_v * dm.dv, io.ld_o, K.dtype)
+    _delta_states(dm, n_seq, S0=S0, S=S)
+    _offsets(cu_seqlens, n_seq)
+    _check("ttt_delta_chunked", lib().ttt_delta_chunked(
+        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S0), _ptr(S), _ptr(O), _ptr(cu_seqlens), n_seq, T, scale,
+        dm, ctypes.byref(io), dtype_code(K.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def ttt_delta_step(Q, K, V, g, beta, S, O, B, dm: DeltaDims, io: IOCfg, slots=None, scale=1.0, stream=None):
+    """One token for each of B sequences; S [n_slots][heads_v][dv][dk] is updated in place.  slots: int32 CUDA tensor
+    [B], out-of-range entries marking padding rows; None: row b has slot b."""
+    _same_device(Q, K, V, g, beta, S, O, slots)
+    _delta_tokens(Q, K, V, g, beta, B, dm, io)
+    _rows("O", O, B, dm.heads_v * dm.dv, io.ld_o, K.dtype)
+    _delta_states(dm, S.shape[0], S=S)
+    if slots is not None:
+        _dense("slots", slots, (B,), torch.int32)
+    _check("ttt_delta_step", lib().ttt_delta_step(
+        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S), S.shape[0], _ptr(slots), _ptr(O), B, scale, dm,
+        ctypes.byref(io), dtype_code(K.dtype), _stream(stream)))
+
+
 def ttt_selftest_wait_timeout(ws, timeout_us: int, stream=None):
     _check("ttt_selftest_wait_timeout", lib().ttt_selftest_wait_timeout(_ptr(ws), ws.numel(), timeout_us,
                                                                         _stream(stream)))
@@ -259,7 +350,9 @@ def ttt_launch_count() -> int:
 
 
 TTT_PROF_GRAD, TTT_PROF_APPLY, TTT_PROF_NS, TTT_PROF_NORM, TTT_PROF_CONV, TTT_PROF_REDUCE, TTT_PROF_SHADOW = range(7)
-PROF_NAMES = ["grad", "apply", "newton_schulz_step", "row_norms", "shortconv2d", "split_reduce", "weight_shadow"]
+TTT_PROF_DELTA, TTT_PROF_BNORM = 7, 8
+PROF_NAMES = ["grad", "apply", "newton_schulz_step", "row_norms", "shortconv2d", "split_reduce", "weight_shadow",
+              "delta", "block_norm"]
 
 
 def ttt_profile_enable(on: bool = True):
