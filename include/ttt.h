@@ -338,6 +338,42 @@ int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, 
                    int n_slots, const int32_t* slots, void* O, int64_t B, float scale, ttt_delta_dims dims,
                    const ttt_io_cfg* io, ttt_dtype dtype, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Block norms: the norm after a block with its gate and residual scale, the
+ * residual sum, and the norm before the next block, per row of D columns:
+ *     p  = RMSNorm(y) o w_post o SiLU(z)
+ *     x' = x + res_scale o p,      n = RMSNorm(x') o w_pre
+ * with RMSNorm(y) = y / sqrt(mean(y^2) + eps), the mean of y over all D columns
+ * or over each group of `group` consecutive ones (a head), which then share
+ * w_post (float [group]); res_scale and w_pre are float [D].  ZipMap's gated
+ * output above is the same norm and gate with z = W_g o'.
+ *  - X (residual stream), Z (gate), the weights and one of Xout and N may be
+ *    NULL: no residual, no gate, ones, and that output is not written.  n is
+ *    computed from x' before x' is rounded.
+ *  - Rows of X, Y, Z, Xout, N are bf16 or float (dtype), with the row strides of
+ *    cfg (elements; 0 means D).  Any alignment of the element type works;
+ *    16-byte aligned rows and D, group multiples of 8 run with 16-byte accesses.
+ *  - An output may be one of the inputs (same pointer and stride), else they may
+ *    not overlap.  Arithmetic is fp32, each output rounded once.
+ *  - D <= 8192; group divides D and is D or a multiple of 8. */
+typedef struct { int D, group; float eps; int64_t ld_x, ld_y, ld_z, ld_xout, ld_n; } ttt_norm_cfg;
+
+int ttt_block_norm(const void* X, const void* Y, const void* Z, const float* w_post, const float* res_scale,
+                   const float* w_pre, void* Xout, void* N, int64_t T, const ttt_norm_cfg* cfg, ttt_dtype dtype,
+                   void* stream);
+
+/* Its gradient from dXout and dN (either may be NULL: zeros; dN NULL means that n
+ * was not used): dX, dY, dZ rows with the strides of X, Y, Z, and the weights'
+ * gradients summed over the rows (and over a row's groups for dw_post), float,
+ * overwritten.  Any output may be NULL; a T of 0 writes zero weight gradients.
+ * Everything is recomputed from X, Y, Z; deterministic.  ws (256-byte aligned,
+ * ttt_block_norm_workspace_bytes) is needed for the weights' gradients only. */
+size_t ttt_block_norm_workspace_bytes(const ttt_norm_cfg* cfg, int64_t T);
+int ttt_block_norm_backward(const void* X, const void* Y, const void* Z, const float* w_post, const float* res_scale,
+                            const float* w_pre, const void* dXout, const void* dN, void* dX, void* dY, void* dZ,
+                            float* dw_post, float* dres_scale, float* dw_pre, int64_t T, const ttt_norm_cfg* cfg,
+                            ttt_dtype dtype, void* ws, size_t ws_bytes, void* stream);
+
 /* Diagnostic for the timeout path: launches one single-warp kernel that waits on
  * a barrier nothing ever signals, with a wait limit of `timeout_us`
  * microseconds.  The wait gives up, records TTT_ERR_TIMEOUT in the workspace

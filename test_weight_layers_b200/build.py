@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libttt.so")
-UNITS = ["ttt_capi.cu", "ttt_delta.cu"]
+UNITS = ["ttt_capi.cu", "ttt_delta.cu", "ttt_norm.cu"]
 OBJ = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

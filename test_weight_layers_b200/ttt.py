@@ -50,6 +50,12 @@ class DeltaDims(ctypes.Structure):
     _fields_ = [("heads_qk", ctypes.c_int), ("heads_v", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int)]
 
 
+class NormCfg(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int), ("group", ctypes.c_int), ("eps", ctypes.c_float), ("ld_x", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_z", ctypes.c_int64), ("ld_xout", ctypes.c_int64),
+                ("ld_n", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -87,6 +93,10 @@ def lib() -> ctypes.CDLL:
             "ttt_delta_chunked": (I, [P, P, P, P, P, P, P, P, P, I, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P, SZ,
                                       P]),
             "ttt_delta_step": (I, [P, P, P, P, P, P, I, P, P, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P]),
+            "ttt_block_norm": (I, [P, P, P, P, P, P, P, P, I64, ctypes.POINTER(NormCfg), I, P]),
+            "ttt_block_norm_workspace_bytes": (SZ, [ctypes.POINTER(NormCfg), I64]),
+            "ttt_block_norm_backward": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, I64, ctypes.POINTER(NormCfg), I,
+                                            P, SZ, P]),
             "ttt_status_string": (ctypes.c_char_p, [I]),
             "ttt_compiled_arch": (I, []),
             "ttt_kernel_binary_version": (I, [ctypes.POINTER(I)]),
@@ -338,6 +348,56 @@ def ttt_delta_step(Q, K, V, g, beta, S, O, B, dm: DeltaDims, io: IOCfg, slots=No
     _check("ttt_delta_step", lib().ttt_delta_step(
         _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S), S.shape[0], _ptr(slots), _ptr(O), B, scale, dm,
         ctypes.byref(io), dtype_code(K.dtype), _stream(stream)))
+
+
+def norm_cfg(D: int, group: int = 0, eps: float = 1e-6, ld_x=0, ld_y=0, ld_z=0, ld_xout=0, ld_n=0) -> NormCfg:
+    """group 0: one mean over all D columns."""
+    return NormCfg(D, group or D, eps, ld_x, ld_y, ld_z, ld_xout, ld_n)
+
+
+def norm_workspace(T: int, cfg: NormCfg, device="cuda") -> torch.Tensor:
+    """A workspace for ttt_block_norm_backward over at most T rows."""
+    n = int(lib().ttt_block_norm_workspace_bytes(ctypes.byref(cfg), T))
+    if n == 0:
+        raise TTTError("ttt_block_norm_workspace_bytes", TTT_ERR_UNSUPPORTED, "invalid or unsupported norm shape")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm_check(T, cfg, dtype, rows, weights):
+    for name, t, ld in rows:
+        if t is not None:
+            _rows(name, t, T, cfg.D, ld, dtype)
+    for name, t, n in weights:
+        if t is not None:
+            _dense(name, t, (n,))
+
+
+def ttt_block_norm(Y, Xout, T, cfg: NormCfg, X=None, Z=None, w_post=None, res_scale=None, w_pre=None, N=None,
+                   stream=None):
+    """Xout = X + res_scale * RMSNorm(Y) * w_post * SiLU(Z) and N = RMSNorm(Xout) * w_pre per row (either output may
+    be None)."""
+    _same_device(Y, Xout, X, Z, w_post, res_scale, w_pre, N)
+    _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
+                                  ("Xout", Xout, cfg.ld_xout), ("N", N, cfg.ld_n)),
+                (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D)))
+    _check("ttt_block_norm", lib().ttt_block_norm(
+        _ptr(X), _ptr(Y), _ptr(Z), _ptr(w_post), _ptr(res_scale), _ptr(w_pre), _ptr(Xout), _ptr(N), T,
+        ctypes.byref(cfg), dtype_code(Y.dtype), _stream(stream)))
+
+
+def ttt_block_norm_backward(Y, dXout, dY, T, cfg: NormCfg, ws, X=None, Z=None, w_post=None, res_scale=None, w_pre=None,
+                            dN=None, dX=None, dZ=None, dw_post=None, dres_scale=None, dw_pre=None, stream=None):
+    """The gradient of ttt_block_norm from dXout and dN (None: zero); outputs that are None are not written."""
+    _same_device(Y, dXout, dY, ws, X, Z, w_post, res_scale, w_pre, dN, dX, dZ, dw_post, dres_scale, dw_pre)
+    _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
+                                  ("dXout", dXout, cfg.ld_xout), ("dN", dN, cfg.ld_n), ("dX", dX, cfg.ld_x),
+                                  ("dY", dY, cfg.ld_y), ("dZ", dZ, cfg.ld_z)),
+                (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D),
+                 ("dw_post", dw_post, cfg.group), ("dres_scale", dres_scale, cfg.D), ("dw_pre", dw_pre, cfg.D)))
+    _check("ttt_block_norm_backward", lib().ttt_block_norm_backward(
+        _ptr(X), _ptr(Y), _ptr(Z), _ptr(w_post), _ptr(res_scale), _ptr(w_pre), _ptr(dXout), _ptr(dN), _ptr(dX),
+        _ptr(dY), _ptr(dZ), _ptr(dw_post), _ptr(dres_scale), _ptr(dw_pre), T, ctypes.byref(cfg), dtype_code(Y.dtype),
+        _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
 
 
 def ttt_selftest_wait_timeout(ws, timeout_us: int, stream=None):
