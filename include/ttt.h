@@ -328,6 +328,20 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
                       ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws, size_t ws_bytes,
                       void* stream);
 
+/* The gradient of ttt_delta_chunked from dO (rows of stride ld_o) and dS, the
+ * gradient of the states after the sequences (NULL: zeros): dQ, dK, dV with the
+ * strides of Q, K, V, dg and dbeta float [T][heads_v], and dS0 (NULL: not
+ * wanted) for the states before them.  Gradients of shared query/key heads are
+ * summed over their value heads.  Stateless: the states are recomputed from the
+ * inputs (workspace with backward = 1), nothing of the forward call is needed.
+ * Rows outside the sequences are left as they are.  Deterministic.  TTT_BF16
+ * only (TTT_FP32 returns TTT_ERR_UNSUPPORTED). */
+int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, const float* g, const float* beta,
+                               const float* S0, const void* dO, const float* dS, void* dQ, void* dK, void* dV,
+                               float* dg, float* dbeta, float* dS0, const int32_t* cu_seqlens, int n_seq, int64_t T,
+                               float scale, ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws,
+                               size_t ws_bytes, void* stream);
+
 /* One token for each of B sequences whose states live in a pool (decoding):
  * S: float [n_slots][heads_v][dv][dk], updated in place.  slots: device int32
  * [B], row b's place in the pool; a slot outside [0, n_slots) marks a padding

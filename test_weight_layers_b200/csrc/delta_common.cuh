@@ -36,8 +36,9 @@ enum {
   DV_AO = 3,    // scale e^{c_i} f_q : factor of Q16 S^T in O
   DV_PS = 4,    // inverse row scale of P
   DV_AK = 5,    // e^{c_C - c_j} f_k : factor of U in S'
-  DV_EG = 6,    // [0]: e^{c_C}
-  DR_NVEC = 7
+  DV_EG = 6,    // e^{c_C} (64 times)
+  DV_C = 7,     // c_j
+  DR_NVEC = 8
 };
 // Bytes of a value head's chunk block: Y hi | Y lo | P hi | vectors (| P lo, for the backward pass)
 constexpr int DR_HBLK = 3 * DR_TILE + DR_NVEC * DR_C * 4;

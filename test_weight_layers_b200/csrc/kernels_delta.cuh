@@ -98,8 +98,12 @@ struct PrepArgs {
   uint8_t* kq;   // [chunk][hk][K16 | Q16]
   uint8_t* blk;  // [chunk][hv][blk_bytes]
   int blk_bytes;
-  float* fkq;    // [chunk][hk][2][64] factors f_k, f_q (backward only, else null)
+  float* tok;    // [chunk][hk][6][64] token factors (TF_*), backward pass only
 };
+
+// Token factors for the way back through the norm: k~ = f_k K16 with f_k = scale 2^-e / n, so
+// dk = h_k (dk~ - p_k K16 (K16 . dk~)), h_k = f_k 2^e, p_k = 1 / ||K16||^2 (0 where nothing is normalised).
+enum { TF_FK = 0, TF_FQ = 1, TF_HK = 2, TF_HQ = 3, TF_PK = 4, TF_PQ = 5, TF_N = 6 };
 
 constexpr int PREP_LD = 68;  // floats per row of the fp32 64 x 64 tiles
 
@@ -200,18 +204,20 @@ __global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
     if (lane == 0) {
       // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
       const float inv = pow2i(-e), norm = sqrtf(ss);
+      const bool normed = a.l2norm && norm * inv > 1e-12f;
       float f = row < ch.len ? inv : 0.f;
-      if (a.l2norm && row < ch.len) f = norm * inv > 1e-12f ? 1.f / norm : inv * 1e12f;
+      if (a.l2norm && row < ch.len) f = normed ? 1.f / norm : inv * 1e12f;
       if (isq) f *= a.scale;
       (isq ? fq : fk)[row] = f;
+      if constexpr (BACK) {
+        float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
+        tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
+        tf[(isq ? TF_HQ : TF_HK) * DR_C] = f * s;
+        tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
+      }
     }
   }
   __syncthreads();
-  if (BACK && tid < DR_C) {
-    float* f = a.fkq + ((int64_t)ci * a.hk + hq) * 2 * DR_C;
-    f[tid] = fk[tid];
-    f[DR_C + tid] = fq[tid];
-  }
 
   // K16 K16^T and Q16 K16^T on and below the diagonal; warp w has rows [16 w, 16 w + 16)
   {
@@ -301,6 +307,7 @@ __global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
         vec[DV_AO * DR_C + i] = ec * fqi;
         vec[DV_AK * DR_C + i] = el * fki;
         vec[DV_EG * DR_C + i] = expf((float)G);
+        vec[DV_C * DR_C + i] = (float)cii;
       }
     }
     __syncthreads();
@@ -354,30 +361,71 @@ struct StateArgs {
   const uint8_t* blk;
   int blk_bytes;
   Guard guard;
+  // backward pass: recompute the states, keep them and the errors, and sum dO . O
+  const __nv_bfloat16* dO;  // rows of stride ldo
+  float* keep_s;            // [chunk][hv][dv][dk]
+  float* keep_e;            // [chunk][hv][dv][64] E^T
+  float* w_part;            // [chunk][hv][dv / 16][64]
 };
 
 constexpr int DR_VROW = 48;                  // bytes per row of a warp's V / O tile (32 used): conflict-free 8x8 tiles
 constexpr int DR_VTILE = DR_C * DR_VROW;
 
-template <int DK>
+template <int DK, bool BACK>
 constexpr int state_stage() {
-  return 2 * DR_C * DK * 2 + DR_HBLK;
+  return 2 * DR_C * DK * 2 + DR_HBLK + (BACK ? DR_TILE : 0);
 }
-template <int DK>
+// per warp two V tiles, and two dO tiles for the backward pass
+template <bool BACK>
+constexpr int state_warp_smem() {
+  return (BACK ? 4 : 2) * DR_VTILE;
+}
+template <int DK, bool BACK>
 constexpr int state_smem(int warps) {
-  return 2 * state_stage<DK>() + warps * 2 * DR_VTILE + 64;
+  return 2 * state_stage<DK, BACK>() + warps * state_warp_smem<BACK>() + 64;
 }
 
-template <int DK>
+// A warp's 64 x 16 tile of token rows `p` (first channel v0 of head h), zero outside the sequence and the head.
+__device__ __forceinline__ void load_vtile(uint32_t dst, const __nv_bfloat16* p, int64_t ld, const DrSeq& sq, int n,
+                                           int col0, int v0, int dv, int lane) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int row = it * 16 + (lane >> 1), half = lane & 1;
+    const int at = n * DR_C + row;
+    const bool live = at < sq.len && v0 + half * 8 < dv;
+    cp_async16(dst + row * DR_VROW + half * 16, live ? p + (int64_t)(sq.tok + at) * ld + col0 + v0 + half * 8 : p, live);
+  }
+}
+// ... and its counterpart: a tile in shared memory -> token rows.
+__device__ __forceinline__ void store_vtile(const uint8_t* src, __nv_bfloat16* p, int64_t ld, const DrSeq& sq, int n,
+                                            int64_t col0, int v0, int dv, int lane) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int row = it * 16 + (lane >> 1), half = lane & 1;
+    const int at = n * DR_C + row;
+    if (at < sq.len && v0 + half * 8 < dv)
+      *reinterpret_cast<uint4*>(p + (int64_t)(sq.tok + at) * ld + col0 + v0 + half * 8) =
+          *reinterpret_cast<const uint4*>(src + row * DR_VROW + half * 16);
+  }
+}
+// Address of 8x8 matrix lane/8 of token rows n0..n0+15 of such a tile: (tokens n0 + 8 (m / 2), channels 8 (m % 2));
+// read with .trans it gives the accumulator layout of two neighbouring 8-token tiles (rows = channels).
+__device__ __forceinline__ uint32_t vtile_addr(uint32_t base, int lane, int n0) {
+  return base + (n0 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4);
+}
+
+template <int DK, bool BACK>
 __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int STAGE = state_stage<DK>();
+  constexpr int STAGE = state_stage<DK, BACK>();
   constexpr int KQ = 2 * DR_C * DK * 2;
+  constexpr int HB = STAGE - KQ;
+  constexpr int WSM = state_warp_smem<BACK>();
   constexpr int NT = DK / 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* vbuf = smem + 2 * STAGE + warp * 2 * DR_VTILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * 2 * DR_VTILE);
+  uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
   const int h = blockIdx.z, hq = h / (a.hv / a.hk);
   const int v0 = (blockIdx.y * nwarp + warp) * 16;  // first value channel of this warp (may lie past dv)
   if (tid == 0) {
@@ -394,20 +442,14 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   auto load_stage = [&](int n) {  // one thread
     const int64_t ci = sq.chunk0 + n;
     uint8_t* st = smem + (n & 1) * STAGE;
-    mbar_expect_tx(&full[n & 1], KQ + DR_HBLK);
+    mbar_expect_tx(&full[n & 1], KQ + HB);
     bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, &full[n & 1]);
-    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, DR_HBLK, &full[n & 1]);
+    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, &full[n & 1]);
   };
-  auto load_v = [&](int n) {  // this warp's 64 x 16 tile of V, zero outside the sequence and the head
-    const uint32_t dst = smem_u32(vbuf + (n & 1) * DR_VTILE);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = it * 16 + (lane >> 1), half = lane & 1;
-      const int at = n * DR_C + row;
-      const bool live = at < sq.len && v0 + half * 8 < a.dv;
-      const __nv_bfloat16* p = live ? a.V + (int64_t)(sq.tok + at) * a.ldv + (int64_t)h * a.dv + v0 + half * 8 : a.V;
-      cp_async16(dst + row * DR_VROW + half * 16, p, live);
-    }
+  auto load_v = [&](int n) {
+    load_vtile(smem_u32(vbuf + (n & 1) * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
+    if constexpr (BACK)
+      load_vtile(smem_u32(vbuf + (2 + (n & 1)) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
     cp_commit();
   };
 
@@ -445,7 +487,20 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
     const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, pb = yl + DR_TILE;
     const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + KQ + 3 * DR_TILE);
     const uint32_t vb = smem_u32(vbuf + (n & 1) * DR_VTILE);
+    const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;  // this chunk's block of the kept arrays
 
+    if constexpr (BACK) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int r = v0 + g + 8 * p, col = k * 8 + 2 * t;
+          const float i = p ? inv1 : inv0;
+          if (r < a.dv && col < a.dk)
+            *reinterpret_cast<float2*>(a.keep_s + (blk * a.dv + r) * a.dk + col) =
+                make_float2(s[k][2 * p] * i, s[k][2 * p + 1] * i);
+        }
+    }
     // S K^T and S Q^T
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -476,6 +531,10 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         ldsm4(b, addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
         mma_f16(o[2 * np], hi, b[0], b[1]);
         mma_f16(o[2 * np + 1], hi, b[2], b[3]);
+        if constexpr (BACK) {  // the gates' gradients are sums of dO . O in fp32
+          mma_f16(o[2 * np], lo, b[0], b[1]);
+          mma_f16(o[2 * np + 1], lo, b[2], b[3]);
+        }
       }
     }
     // R = V - e^c K S^T, then the scale of beta R
@@ -484,7 +543,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t v[4];
-      ldsm4t(v, vb + (np * 16 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4));
+      ldsm4t(v, vtile_addr(vb, lane, np * 16));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int k = 2 * np + q, col = k * 8 + 2 * t;
@@ -539,10 +598,21 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         const int col = k * 8 + 2 * t;
         const float2 ys = *reinterpret_cast<const float2*>(vec + DV_YS * DR_C + col);
         const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
-        r[k][0] = be.x * (r[k][0] + ys.x * (x[k][0] * i0));  // r becomes U
-        r[k][1] = be.y * (r[k][1] + ys.y * (x[k][1] * i0));
-        r[k][2] = be.x * (r[k][2] + ys.x * (x[k][2] * i1));
-        r[k][3] = be.y * (r[k][3] + ys.y * (x[k][3] * i1));
+        r[k][0] = r[k][0] + ys.x * (x[k][0] * i0);
+        r[k][1] = r[k][1] + ys.y * (x[k][1] * i0);
+        r[k][2] = r[k][2] + ys.x * (x[k][2] * i1);
+        r[k][3] = r[k][3] + ys.y * (x[k][3] * i1);
+        if constexpr (BACK) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (v0 + g + 8 * p < a.dv)
+              *reinterpret_cast<float2*>(a.keep_e + (blk * a.dv + v0 + g + 8 * p) * DR_C + col) =
+                  make_float2(r[k][2 * p], r[k][2 * p + 1]);
+        }
+        r[k][0] *= be.x;  // r becomes U
+        r[k][1] *= be.y;
+        r[k][2] *= be.x;
+        r[k][3] *= be.y;
       }
     }
     // O = e^c Q S^T + P U, accumulated in U's scale over P's row scales
@@ -562,45 +632,68 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          hi[2 * q] = pack_f16x2(r[2 * kt + q][0] * w0, r[2 * kt + q][1] * w0);
-          hi[2 * q + 1] = pack_f16x2(r[2 * kt + q][2] * w1, r[2 * kt + q][3] * w1);
-        }
+        uint32_t hi[4], lo[4];
+        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
 #pragma unroll
         for (int np = kt; np < 4; ++np) {
           uint32_t p[4];
           ldsm4(p, addr_bn(pb, lane, np * 16, kt * 2, 128));
           mma_f16(x[2 * np], hi, p[0], p[1]);
           mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+          if constexpr (BACK) {
+            mma_f16(x[2 * np], lo, p[0], p[1]);
+            mma_f16(x[2 * np + 1], lo, p[2], p[3]);
+            ldsm4(p, addr_bn(yh + DR_HBLK, lane, np * 16, kt * 2, 128));
+            mma_f16(x[2 * np], hi, p[0], p[1]);
+            mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+          }
         }
       }
-      __syncwarp();  // every lane has read its V tile; O takes its place
+      if constexpr (BACK) {  // this warp's part of dO . O for each token
+        const uint32_t db = smem_u32(vbuf + (2 + (n & 1)) * DR_VTILE);
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t y[4];
+        for (int np = 0; np < 4; ++np) {
+          uint32_t d[4];
+          ldsm4t(d, vtile_addr(db, lane, np * 16));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int k = 2 * np + q, col = k * 8 + 2 * t;
-          const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
-          const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
-          y[2 * q] = pack_bf16x2(ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * i0),
-                                 ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * i0));
-          y[2 * q + 1] = pack_bf16x2(ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * i1),
-                                     ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * i1));
+          for (int q = 0; q < 2; ++q) {
+            const int k = 2 * np + q, col = k * 8 + 2 * t;
+            const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
+            const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
+            const uint32_t d0 = d[2 * q], d1 = d[2 * q + 1];
+            float sx = (ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * i0)) * __uint_as_float(d0 << 16) +
+                       (ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * i1)) * __uint_as_float(d1 << 16);
+            float sy = (ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * i0)) * __uint_as_float(d0 & 0xffff0000u) +
+                       (ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * i1)) * __uint_as_float(d1 & 0xffff0000u);
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) {
+              sx += __shfl_xor_sync(0xffffffffu, sx, m);
+              sy += __shfl_xor_sync(0xffffffffu, sy, m);
+            }
+            if (g == 0 && v0 < a.dv)
+              *reinterpret_cast<float2*>(a.w_part + (blk * ((a.dv + 15) / 16) + v0 / 16) * DR_C + col) =
+                  make_float2(sx, sy);
+          }
         }
-        stsm4t(vb + (np * 16 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4), y[0], y[1], y[2],
-               y[3]);
-      }
-      __syncwarp();
+      } else {
+        __syncwarp();  // every lane has read its V tile; O takes its place
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int row = it * 16 + (lane >> 1), half = lane & 1;
-        const int at = n * DR_C + row;
-        if (at < sq.len && v0 + half * 8 < a.dv)
-          *reinterpret_cast<uint4*>(a.O + (int64_t)(sq.tok + at) * a.ldo + (int64_t)h * a.dv + v0 + half * 8) =
-              *reinterpret_cast<const uint4*>(vbuf + (n & 1) * DR_VTILE + row * DR_VROW + half * 16);
+        for (int np = 0; np < 4; ++np) {
+          uint32_t y[4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int k = 2 * np + q, col = k * 8 + 2 * t;
+            const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
+            const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
+            y[2 * q] = pack_bf16x2(ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * i0),
+                                   ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * i0));
+            y[2 * q + 1] = pack_bf16x2(ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * i1),
+                                       ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * i1));
+          }
+          stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
+        }
+        __syncwarp();
+        store_vtile(vbuf + (n & 1) * DR_VTILE, a.O, a.ldo, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
       }
     }
     // S' = e^{c_C} S + (e^{c_C - c} U)^T K, with S brought to the scale of the added term

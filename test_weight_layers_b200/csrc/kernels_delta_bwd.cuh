@@ -1,0 +1,703 @@
+// Gated delta rule, gradient of the chunked form (bf16 tokens).
+//
+// With the symbols of delta_common.cuh and S' the state after the chunk, from dO and dS':
+//     dU = P^T dO + e^{c_C - c} K dS'^T,     Z = dU + Y^T (beta dU)   (= M^-T dU)
+//     dV = beta Z,   dbeta = E . Z
+//     dS = e^{c_C} dS' + (e^c dO)^T Q - (e^c beta Z)^T K
+//     F_ij = D_ij dO_i.U_j (j <= i),   W_ij = D_ij beta_i Z_i.U_j (j < i)
+//     dQ = e^c dO S + F K
+//     dK = -e^c beta Z S - W K + e^{c_C - c} U dS' + F^T Q - W^T K
+// Scaling S by exp(g_t) at token t scales every later o and read error alike, so
+//     dg_t = <S~_t, dS~_t> = <S, dS> - sum_{i < t} (dO_i.O_i - dV_i.V_i)
+// with <S, dS> taken at each chunk's start: no sum runs over more than a chunk.
+//
+// Passes: the chunk preparation and the state pass again (they keep S, E and
+// dO.O), the reverse pass over the chunks (dS in registers as the state pass
+// has S; it keeps dS' and Z and writes dV), and one block per chunk and
+// query/key head for dQ, dK and the gates.
+#pragma once
+
+#include "kernels_delta.cuh"
+
+namespace ttt {
+
+struct ReverseArgs {
+  const __nv_bfloat16 *V, *dO;
+  __nv_bfloat16* dV;
+  int64_t ldv, ldo;
+  const float* dS;  // gradient of the state after each sequence (null: zeros)
+  float* dS0;       // gradient of the state before it (null: not wanted)
+  int hk, hv, dk, dv;
+  const DrSeq* seqs;
+  const uint8_t* kq;
+  const uint8_t* blk;
+  int blk_bytes;
+  Guard guard;
+  const float *keep_s, *keep_e;
+  float* keep_ds;  // [chunk][hv][dv][dk] dS'
+  float* keep_z;   // [chunk][hv][dv][64] Z^T
+  float* w_part;   // [chunk][hv][dv / 16][64]: dO.O in, dO.O - dV.V out
+  float* b_part;   // [chunk][hv][dv / 16][64] E.Z
+  float* x_part;   // [chunk][hv][dv / 16] <S, dS>
+};
+
+// As the state pass: a warp owns 16 value channels and keeps dS [16][dk] in registers.
+template <int DK>
+__global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int STAGE = state_stage<DK, true>();
+  constexpr int KQ = 2 * DR_C * DK * 2;
+  constexpr int HB = STAGE - KQ;
+  constexpr int WSM = state_warp_smem<true>();
+  constexpr int NT = DK / 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
+  const int h = blockIdx.z, hq = h / (a.hv / a.hk);
+  const int v0 = (blockIdx.y * nwarp + warp) * 16;
+  const int n16 = (a.dv + 15) / 16;
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const DrSeq sq = a.seqs[blockIdx.x];
+  __syncthreads();
+  if (sq.len < 0) return;
+  const int nchunk = (sq.len + DR_C - 1) / DR_C;
+
+  auto load_stage = [&](int n, int buf) {  // one thread
+    const int64_t ci = sq.chunk0 + n;
+    uint8_t* st = smem + buf * STAGE;
+    mbar_expect_tx(&full[buf], KQ + HB);
+    bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, &full[buf]);
+    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, &full[buf]);
+  };
+  auto load_v = [&](int n, int buf) {
+    load_vtile(smem_u32(vbuf + buf * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
+    load_vtile(smem_u32(vbuf + (2 + buf) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
+    cp_commit();
+  };
+
+  float s[NT][4];
+  const int64_t srow = ((int64_t)blockIdx.x * a.hv + h) * a.dv;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+      float2 x = make_float2(0.f, 0.f);
+      if (a.dS && r < a.dv && col < a.dk) x = *reinterpret_cast<const float2*>(a.dS + (srow + r) * a.dk + col);
+      s[n][2 * p] = x.x;
+      s[n][2 * p + 1] = x.y;
+    }
+  float inv0 = 1.f, inv1 = 1.f;  // dS = s * inv
+
+  if (nchunk > 0) {
+    if (tid == 0) load_stage(nchunk - 1, 0);
+    load_v(nchunk - 1, 0);
+  }
+#pragma unroll 1
+  for (int it = 0; it < nchunk; ++it) {
+    const int n = nchunk - 1 - it, buf = it & 1;
+    if (n > 0) {
+      if (tid == 0) load_stage(n - 1, buf ^ 1);
+      load_v(n - 1, buf ^ 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncwarp();
+    mbar_wait(&full[buf], (it >> 1) & 1, a.guard);  // (as in the state pass)
+    const uint32_t st = smem_u32(smem + buf * STAGE);
+    const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, ph = yl + DR_TILE;
+    const uint32_t pl = yh + DR_HBLK;
+    const float* vec = reinterpret_cast<const float*>(smem + buf * STAGE + KQ + 3 * DR_TILE);
+    const uint32_t vb = smem_u32(vbuf + buf * DR_VTILE), db = smem_u32(vbuf + (2 + buf) * DR_VTILE);
+    const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;
+
+    // keep dS'
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = v0 + g + 8 * p, col = k * 8 + 2 * t;
+        const float i = p ? inv1 : inv0;
+        if (r < a.dv && col < a.dk)
+          *reinterpret_cast<float2*>(a.keep_ds + (blk * a.dv + r) * a.dk + col) =
+              make_float2(s[k][2 * p] * i, s[k][2 * p + 1] * i);
+      }
+    // dS' K^T
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      m0 = max_abs2(m0, s[k][0], s[k][1]);
+      m1 = max_abs2(m1, s[k][2], s[k][3]);
+    }
+    const int e0 = row_exp(quad_max(m0), DR_ROW_EXP), e1 = row_exp(quad_max(m1), DR_ROW_EXP);
+    const float sc0 = pow2i(e0), sc1 = pow2i(e1);
+    const float is0 = inv0 * pow2i(-e0), is1 = inv1 * pow2i(-e1);
+    float r[8][4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[k][j] = 0.f;
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt) {
+      uint32_t hi[4], lo[4];
+      split_a(s[2 * kt], s[2 * kt + 1], sc0, sc1, hi, lo);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b[4];
+        ldsm4(b, addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
+        mma_f16(r[2 * np], hi, b[0], b[1]);
+        mma_f16(r[2 * np + 1], hi, b[2], b[3]);
+        mma_f16(r[2 * np], lo, b[0], b[1]);
+        mma_f16(r[2 * np + 1], lo, b[2], b[3]);
+      }
+    }
+    // the dO tile in the accumulator layout (bf16 pairs)
+    uint32_t d[8][2];
+    m0 = m1 = 0.f;
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t v[4];
+      ldsm4t(v, vtile_addr(db, lane, np * 16));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k = 2 * np + q;
+        d[k][0] = v[2 * q];
+        d[k][1] = v[2 * q + 1];
+        const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + k * 8 + 2 * t);
+        m0 = max_abs2(m0, __uint_as_float(d[k][0] << 16) * ps.x, __uint_as_float(d[k][0] & 0xffff0000u) * ps.y);
+        m1 = max_abs2(m1, __uint_as_float(d[k][1] << 16) * ps.x, __uint_as_float(d[k][1] & 0xffff0000u) * ps.y);
+      }
+    }
+    // dU = P^T dO + e^{c_C - c} K dS'^T; dO times P's row scale is exact in fp16
+    {
+      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+      const float w0 = pow2i(f0), w1 = pow2i(f1), i0 = pow2i(-f0), i1 = pow2i(-f1);
+      float x[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        uint32_t hi[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + (2 * kt + q) * 8 + 2 * t);
+          const uint32_t a0 = d[2 * kt + q][0], a1 = d[2 * kt + q][1];
+          hi[2 * q] = pack_f16x2(__uint_as_float(a0 << 16) * ps.x * w0, __uint_as_float(a0 & 0xffff0000u) * ps.y * w0);
+          hi[2 * q + 1] =
+              pack_f16x2(__uint_as_float(a1 << 16) * ps.x * w1, __uint_as_float(a1 & 0xffff0000u) * ps.y * w1);
+        }
+#pragma unroll
+        for (int np = 0; np <= kt; ++np) {
+          uint32_t p[4];
+          ldsm4t(p, addr_bk(ph, lane, kt * 16, np * 2, 128));
+          mma_f16(x[2 * np], hi, p[0], p[1]);
+          mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+          ldsm4t(p, addr_bk(pl, lane, kt * 16, np * 2, 128));
+          mma_f16(x[2 * np], hi, p[0], p[1]);
+          mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 ak = *reinterpret_cast<const float2*>(vec + DV_AK * DR_C + k * 8 + 2 * t);
+        r[k][0] = x[k][0] * i0 + ak.x * (r[k][0] * is0);
+        r[k][1] = x[k][1] * i0 + ak.y * (r[k][1] * is0);
+        r[k][2] = x[k][2] * i1 + ak.x * (r[k][2] * is1);
+        r[k][3] = x[k][3] * i1 + ak.y * (r[k][3] * is1);
+      }
+    }
+    // Z = dU + Y^T (beta dU); Y's row scale goes to the other factor
+    {
+      m0 = m1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + k * 8 + 2 * t);
+        const float2 ys = *reinterpret_cast<const float2*>(vec + DV_YS * DR_C + k * 8 + 2 * t);
+        m0 = max_abs2(m0, r[k][0] * (be.x * ys.x), r[k][1] * (be.y * ys.y));
+        m1 = max_abs2(m1, r[k][2] * (be.x * ys.x), r[k][3] * (be.y * ys.y));
+      }
+      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+      const float w0 = pow2i(f0), w1 = pow2i(f1), i0 = pow2i(-f0), i1 = pow2i(-f1);
+      float x[8][4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        float b[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int k = 2 * kt + q;
+          const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + k * 8 + 2 * t);
+          const float2 ys = *reinterpret_cast<const float2*>(vec + DV_YS * DR_C + k * 8 + 2 * t);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[q][j] = r[k][j] * (j & 1 ? be.y * ys.y : be.x * ys.x);
+        }
+        uint32_t hi[4], lo[4];
+        split_a(b[0], b[1], w0, w1, hi, lo);
+#pragma unroll
+        for (int np = 0; np <= kt; ++np) {
+          uint32_t y[4];
+          ldsm4t(y, addr_bk(yh, lane, kt * 16, np * 2, 128));
+          mma_f16(x[2 * np], hi, y[0], y[1]);
+          mma_f16(x[2 * np + 1], hi, y[2], y[3]);
+          mma_f16(x[2 * np], lo, y[0], y[1]);
+          mma_f16(x[2 * np + 1], lo, y[2], y[3]);
+          ldsm4t(y, addr_bk(yl, lane, kt * 16, np * 2, 128));
+          mma_f16(x[2 * np], hi, y[0], y[1]);
+          mma_f16(x[2 * np + 1], hi, y[2], y[3]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        r[k][0] += x[k][0] * i0;
+        r[k][1] += x[k][1] * i0;
+        r[k][2] += x[k][2] * i1;
+        r[k][3] += x[k][3] * i1;
+      }
+    }
+    // keep Z, the gates' row sums, dV = beta Z
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t v[4], y[4];
+      ldsm4t(v, vtile_addr(vb, lane, np * 16));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int k = 2 * np + q, col = k * 8 + 2 * t;
+        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+        float ex = 0.f, ey = 0.f;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (v0 + g + 8 * p < a.dv) {
+            const int64_t at = (blk * a.dv + v0 + g + 8 * p) * DR_C + col;
+            *reinterpret_cast<float2*>(a.keep_z + at) = make_float2(r[k][2 * p], r[k][2 * p + 1]);
+            const float2 e = *reinterpret_cast<const float2*>(a.keep_e + at);
+            ex += e.x * r[k][2 * p];
+            ey += e.y * r[k][2 * p + 1];
+          }
+        const float d00 = be.x * r[k][0], d01 = be.y * r[k][1], d10 = be.x * r[k][2], d11 = be.y * r[k][3];
+        const uint32_t x0 = v[2 * q], x1 = v[2 * q + 1];
+        float wx = d00 * __uint_as_float(x0 << 16) + d10 * __uint_as_float(x1 << 16);
+        float wy = d01 * __uint_as_float(x0 & 0xffff0000u) + d11 * __uint_as_float(x1 & 0xffff0000u);
+#pragma unroll
+        for (int m = 4; m < 32; m <<= 1) {
+          ex += __shfl_xor_sync(0xffffffffu, ex, m);
+          ey += __shfl_xor_sync(0xffffffffu, ey, m);
+          wx += __shfl_xor_sync(0xffffffffu, wx, m);
+          wy += __shfl_xor_sync(0xffffffffu, wy, m);
+        }
+        if (g == 0 && v0 < a.dv) {
+          const int64_t at = (blk * n16 + v0 / 16) * DR_C + col;
+          const float2 oo = *reinterpret_cast<const float2*>(a.w_part + at);
+          *reinterpret_cast<float2*>(a.w_part + at) = make_float2(oo.x - wx, oo.y - wy);
+          *reinterpret_cast<float2*>(a.b_part + at) = make_float2(ex, ey);
+        }
+        y[2 * q] = pack_bf16x2(d00, d01);
+        y[2 * q + 1] = pack_bf16x2(d10, d11);
+      }
+      __syncwarp();  // every lane has read these tokens of the V tile; dV takes their place
+      stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
+    }
+    __syncwarp();
+    store_vtile(vbuf + buf * DR_VTILE, a.dV, a.ldv, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
+
+    // dS = e^{c_C} dS' + (e^c dO)^T Q - (e^c beta Z)^T K
+    {
+      m0 = m1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = k * 8 + 2 * t;
+        const float2 ar = *reinterpret_cast<const float2*>(vec + DV_AR * DR_C + col);
+        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+        const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
+        r[k][0] *= -ar.x * be.x;
+        r[k][1] *= -ar.y * be.y;
+        r[k][2] *= -ar.x * be.x;
+        r[k][3] *= -ar.y * be.y;
+        m0 = max_abs2(max_abs2(m0, r[k][0], r[k][1]), ao.x * __uint_as_float(d[k][0] << 16),
+                      ao.y * __uint_as_float(d[k][0] & 0xffff0000u));
+        m1 = max_abs2(max_abs2(m1, r[k][2], r[k][3]), ao.x * __uint_as_float(d[k][1] << 16),
+                      ao.y * __uint_as_float(d[k][1] & 0xffff0000u));
+      }
+      const int f0 = min(row_exp(quad_max(m0), DR_ROW_EXP), 87 - exp_of(is0));
+      const int f1 = min(row_exp(quad_max(m1), DR_ROW_EXP), 87 - exp_of(is1));
+      const float w0 = pow2i(f0), w1 = pow2i(f1);
+      const float eg = vec[DV_EG * DR_C];
+      const float d0 = eg * inv0 * w0, d1 = eg * inv1 * w1;
+      inv0 = pow2i(-f0);
+      inv1 = pow2i(-f1);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        s[k][0] *= d0;
+        s[k][1] *= d0;
+        s[k][2] *= d1;
+        s[k][3] *= d1;
+      }
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+        uint32_t hi[4], lo[4], ho[4], lp[4];
+        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
+        float b[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + (2 * kt + q) * 8 + 2 * t);
+          const uint32_t a0 = d[2 * kt + q][0], a1 = d[2 * kt + q][1];
+          b[q][0] = ao.x * __uint_as_float(a0 << 16);
+          b[q][1] = ao.y * __uint_as_float(a0 & 0xffff0000u);
+          b[q][2] = ao.x * __uint_as_float(a1 << 16);
+          b[q][3] = ao.y * __uint_as_float(a1 & 0xffff0000u);
+        }
+        split_a(b[0], b[1], w0, w1, ho, lp);
+#pragma unroll
+        for (int np = 0; np < DK / 16; ++np) {
+          uint32_t b4[4];
+          ldsm4t(b4, addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
+          mma_f16(s[2 * np], hi, b4[0], b4[1]);
+          mma_f16(s[2 * np + 1], hi, b4[2], b4[3]);
+          mma_f16(s[2 * np], lo, b4[0], b4[1]);
+          mma_f16(s[2 * np + 1], lo, b4[2], b4[3]);
+          ldsm4t(b4, addr_bk(qb, lane, kt * 16, np * 2, DK * 2));
+          mma_f16(s[2 * np], ho, b4[0], b4[1]);
+          mma_f16(s[2 * np + 1], ho, b4[2], b4[3]);
+          mma_f16(s[2 * np], lp, b4[0], b4[1]);
+          mma_f16(s[2 * np + 1], lp, b4[2], b4[3]);
+        }
+      }
+    }
+    // <S, dS> of these channels
+    {
+      float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int rr = v0 + g + 8 * p, col = k * 8 + 2 * t;
+          if (rr < a.dv && col < a.dk) {
+            const float2 z = *reinterpret_cast<const float2*>(a.keep_s + (blk * a.dv + rr) * a.dk + col);
+            if (p) x1 += z.x * s[k][2] + z.y * s[k][3];
+            else x0 += z.x * s[k][0] + z.y * s[k][1];
+          }
+        }
+      float xx = x0 * inv0 + x1 * inv1;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) xx += __shfl_xor_sync(0xffffffffu, xx, m);
+      if (lane == 0 && v0 < a.dv) a.x_part[blk * n16 + v0 / 16] = xx;
+    }
+    __syncthreads();  // the stage is read; the next copy into it may start
+  }
+  if (a.dS0) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+        const float i = p ? inv1 : inv0;
+        if (r < a.dv && col < a.dk)
+          *reinterpret_cast<float2*>(a.dS0 + (srow + r) * a.dk + col) =
+              make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dQ, dK and the gates: one block per (chunk, query/key head), over the value
+// heads that share it.  What leaves here is rounded to bf16 (the gates' gradients
+// are sums of what the two passes kept), so the products take fp32 operands as
+// they lie in memory through TF32 (11 significant bits, no scaling), 64 value
+// channels at a time.
+struct GradArgs {
+  const __nv_bfloat16 *dO;
+  int64_t ldo, ldq, ldk;
+  __nv_bfloat16 *dQ, *dK;
+  float *dg, *dbeta;  // [T][hv]
+  int hk, hv, dk, dv;
+  const DrChunk* chunks;
+  const uint8_t* kq;
+  const uint8_t* blk;
+  int blk_bytes;
+  const float* tok;
+  const float *keep_s, *keep_e, *keep_ds, *keep_z, *w_part, *b_part, *x_part;
+};
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// fp32 -> TF32, rounded to nearest
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+
+constexpr int GR_LDT = 72;  // floats per row of [dv][64] tiles: fragment reads k-major (4 rows x 8 columns) hit 32 banks
+constexpr int GR_LDA = 68;  // ... of [64][64] tiles read row-major (8 rows x 4 columns)
+template <int DK>
+constexpr int grad_smem() {
+  return (2 * DR_C * (DK + 8) + 2 * DR_C * GR_LDT + 3 * DR_C * GR_LDA + 5 * DR_C) * 4;
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int LDS = DK + 8;
+  constexpr int NH = DK / 16;  // n-tiles of a warp's half of the dk columns
+  float* Sm = reinterpret_cast<float*>(smem);  // S tile [64][LDS]; later K~
+  float* Dm = Sm + DR_C * LDS;                 // dS' tile; later Q~
+  float* Um = Dm + DR_C * LDS;                 // U^T tile [64 channels][GR_LDT]
+  float* Zm = Um + DR_C * GR_LDT;              // beta Z, the same
+  float* Om = Zm + DR_C * GR_LDT;              // dO tile [64 tokens][GR_LDA]
+  float* Fm = Om + DR_C * GR_LDA;              // F [64][GR_LDA]
+  float* Wm = Fm + DR_C * GR_LDA;              // W
+  float* vc = Wm + DR_C * GR_LDA;              // c, beta, e^c, e^{c_C - c} of the value head
+  float* red = vc + 4 * DR_C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int rg = warp >> 1, ch = warp & 1;  // this warp's 16 token rows and half of the columns
+  const int ci = blockIdx.x, hq = blockIdx.y, rep = a.hv / a.hk, n16 = (a.dv + 15) / 16;
+  pdl_wait();
+  const DrChunk cu = a.chunks[ci];
+  if (cu.len < 0) return;
+
+  float q[NH][4], k[NH][4];  // dQ~ and dK~, rows 16 rg + {g, g + 8}, columns ch DK/2 + 8 n + {2t, 2t + 1}
+#pragma unroll
+  for (int n = 0; n < NH; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[n][j] = k[n][j] = 0.f;
+  const int r0 = rg * 16 + g;
+
+#pragma unroll 1
+  for (int hr = 0; hr < rep; ++hr) {
+    const int h = hq * rep + hr;
+    const int64_t blk = (int64_t)ci * a.hv + h;
+    const float* vec = reinterpret_cast<const float*>(a.blk + blk * a.blk_bytes + 3 * DR_TILE);
+    __syncthreads();  // the head before is done with shared memory
+    if (tid < DR_C) {
+      const float c = vec[DV_C * DR_C + tid], G = vec[DV_C * DR_C + DR_C - 1];
+      vc[tid] = c;
+      vc[DR_C + tid] = vec[DV_BETA * DR_C + tid];
+      vc[2 * DR_C + tid] = expf(c);
+      vc[3 * DR_C + tid] = expf(G - c);
+    }
+    // the gates: dbeta = E.Z, dg_t = <S, dS> - sum_{i < t} w_i
+    if (tid < DR_C) {
+      float w = 0.f, b = 0.f, x = 0.f;
+      for (int p = 0; p < n16; ++p) {
+        w += a.w_part[(blk * n16 + p) * DR_C + tid];
+        b += a.b_part[(blk * n16 + p) * DR_C + tid];
+        x += a.x_part[blk * n16 + p];
+      }
+      float sum = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      if (tid == 31) red[0] = sum;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (tid >= 32) sum += red[0];
+      if (tid < cu.len) {
+        const int64_t at = (int64_t)(cu.tok + tid) * a.hv + h;
+        a.dg[at] = x - (sum - w);
+        a.dbeta[at] = b;
+      }
+    }
+    float f[4][4], wm[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[n][j] = wm[n][j] = 0.f;
+    __syncthreads();
+    const float ec0 = vc[2 * DR_C + r0], ec1 = vc[2 * DR_C + r0 + 8];
+    const float el0 = vc[3 * DR_C + r0], el1 = vc[3 * DR_C + r0 + 8];
+
+#pragma unroll 1
+    for (int d0 = 0; d0 < a.dv; d0 += DR_C) {
+      if (d0) __syncthreads();
+      // tiles of 64 value channels, zero past dv and dk
+      for (int i = tid; i < DR_C * (DK / 4); i += 256) {
+        const int r = i / (DK / 4), c = i % (DK / 4) * 4;
+        float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f), d4 = s4;
+        if (d0 + r < a.dv && c < a.dk) {
+          const int64_t at = (blk * a.dv + d0 + r) * a.dk + c;
+          s4 = *reinterpret_cast<const float4*>(a.keep_s + at);
+          d4 = *reinterpret_cast<const float4*>(a.keep_ds + at);
+        }
+        *reinterpret_cast<float4*>(Sm + r * LDS + c) = s4;
+        *reinterpret_cast<float4*>(Dm + r * LDS + c) = d4;
+      }
+      for (int i = tid; i < DR_C * 16; i += 256) {
+        const int r = i >> 4, c = (i & 15) * 4;
+        float4 e4 = make_float4(0.f, 0.f, 0.f, 0.f), z4 = e4;
+        if (d0 + r < a.dv) {
+          const int64_t at = (blk * a.dv + d0 + r) * DR_C + c;
+          e4 = *reinterpret_cast<const float4*>(a.keep_e + at);
+          z4 = *reinterpret_cast<const float4*>(a.keep_z + at);
+        }
+        const float4 be = *reinterpret_cast<const float4*>(vc + DR_C + c);
+        *reinterpret_cast<float4*>(Um + r * GR_LDT + c) = make_float4(e4.x * be.x, e4.y * be.y, e4.z * be.z, e4.w * be.w);
+        *reinterpret_cast<float4*>(Zm + r * GR_LDT + c) = make_float4(z4.x * be.x, z4.y * be.y, z4.z * be.z, z4.w * be.w);
+      }
+      for (int i = tid; i < DR_C * 8; i += 256) {
+        const int r = i >> 3, c = (i & 7) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < cu.len && d0 + c < a.dv)
+          x = *reinterpret_cast<const uint4*>(a.dO + (int64_t)(cu.tok + r) * a.ldo + (int64_t)h * a.dv + d0 + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = (&x.x)[j];
+          Om[r * GR_LDA + c + 2 * j] = __uint_as_float(w << 16);
+          Om[r * GR_LDA + c + 2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+      }
+      __syncthreads();
+#pragma unroll 2
+      for (int kk = 0; kk < DR_C; kk += 8) {
+        const float o0 = Om[r0 * GR_LDA + kk + t], o1 = Om[(r0 + 8) * GR_LDA + kk + t];
+        const float o2 = Om[r0 * GR_LDA + kk + t + 4], o3 = Om[(r0 + 8) * GR_LDA + kk + t + 4];
+        const float z0 = Zm[(kk + t) * GR_LDT + r0], z1 = Zm[(kk + t) * GR_LDT + r0 + 8];
+        const float z2 = Zm[(kk + t + 4) * GR_LDT + r0], z3 = Zm[(kk + t + 4) * GR_LDT + r0 + 8];
+        const float u0 = Um[(kk + t) * GR_LDT + r0], u1 = Um[(kk + t) * GR_LDT + r0 + 8];
+        const float u2 = Um[(kk + t + 4) * GR_LDT + r0], u3 = Um[(kk + t + 4) * GR_LDT + r0 + 8];
+        const uint32_t oa[4] = {tf32(o0), tf32(o1), tf32(o2), tf32(o3)};
+        const uint32_t za[4] = {tf32(z0), tf32(z1), tf32(z2), tf32(z3)};
+        const uint32_t oe[4] = {tf32(o0 * ec0), tf32(o1 * ec1), tf32(o2 * ec0), tf32(o3 * ec1)};
+        const uint32_t ze[4] = {tf32(-z0 * ec0), tf32(-z1 * ec1), tf32(-z2 * ec0), tf32(-z3 * ec1)};
+        const uint32_t ue[4] = {tf32(u0 * el0), tf32(u1 * el1), tf32(u2 * el0), tf32(u3 * el1)};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {  // F, W: columns j = 32 ch + 8 n + g
+          const int j = ch * 32 + n * 8;
+          if (j > rg * 16 + 15) break;
+          const uint32_t b0 = tf32(Um[(kk + t) * GR_LDT + j + g]), b1 = tf32(Um[(kk + t + 4) * GR_LDT + j + g]);
+          mma_tf32(f[n], oa, b0, b1);
+          mma_tf32(wm[n], za, b0, b1);
+        }
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          const int c = ch * (DK / 2) + n * 8 + g;
+          const uint32_t b0 = tf32(Sm[(kk + t) * LDS + c]), b1 = tf32(Sm[(kk + t + 4) * LDS + c]);
+          const uint32_t e0 = tf32(Dm[(kk + t) * LDS + c]), e1 = tf32(Dm[(kk + t + 4) * LDS + c]);
+          mma_tf32(q[n], oe, b0, b1);
+          mma_tf32(k[n], ze, b0, b1);
+          mma_tf32(k[n], ue, e0, e1);
+        }
+      }
+    }
+    // F and W with their decays and masks
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int j = ch * 32 + n * 8 + 2 * t;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int i = r0 + (p >> 1) * 8, jj = j + (p & 1);
+        const float d = jj <= i ? expf(vc[i] - vc[jj]) : 0.f;
+        Fm[i * GR_LDA + jj] = jj <= i ? d * f[n][p] : 0.f;
+        Wm[i * GR_LDA + jj] = jj < i ? d * wm[n][p] : 0.f;
+      }
+    }
+    // K~ = f_k K16, Q~ = f_q Q16
+    const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
+    const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
+    for (int i = tid; i < 2 * DR_C * (DK / 8); i += 256) {
+      const int isq = i >= DR_C * (DK / 8), ii = i - isq * DR_C * (DK / 8);
+      const int r = ii / (DK / 8), c = ii % (DK / 8);
+      const uint4 x = *reinterpret_cast<const uint4*>(kq + isq * DR_C * DK * 2 + img_off(r, c, DK * 2));
+      const float fs = tf[(isq ? TF_FQ : TF_FK) * DR_C + r];
+      float* dst = (isq ? Dm : Sm) + r * LDS + c * 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = unpack_f16x2((&x.x)[j]);
+        dst[2 * j] = y.x * fs;
+        dst[2 * j + 1] = y.y * fs;
+      }
+    }
+    __syncthreads();
+    // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~
+#pragma unroll 1
+    for (int kk = 0; kk < DR_C; kk += 8) {
+      const bool lower = kk <= rg * 16 + 15, upper = kk + 7 >= rg * 16;  // tiles of F, W and of their transposes
+      uint32_t fa[4], wa[4], ft[4], wt[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int i = r0 + (p & 1) * 8, j = kk + t + (p >> 1) * 4;
+        fa[p] = tf32(Fm[i * GR_LDA + j]);
+        wa[p] = tf32(-Wm[i * GR_LDA + j]);
+        ft[p] = tf32(Fm[j * GR_LDA + i]);
+        wt[p] = tf32(-Wm[j * GR_LDA + i]);
+      }
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        const int c = ch * (DK / 2) + n * 8 + g;
+        const uint32_t b0 = tf32(Sm[(kk + t) * LDS + c]), b1 = tf32(Sm[(kk + t + 4) * LDS + c]);
+        if (lower) {
+          mma_tf32(q[n], fa, b0, b1);
+          mma_tf32(k[n], wa, b0, b1);
+        }
+        if (upper) {
+          mma_tf32(k[n], wt, b0, b1);
+          const uint32_t e0 = tf32(Dm[(kk + t) * LDS + c]), e1 = tf32(Dm[(kk + t + 4) * LDS + c]);
+          mma_tf32(k[n], ft, e0, e1);
+        }
+      }
+    }
+  }
+
+  // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)), the dot over both column halves
+  const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
+  const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
+  float* dots = Fm;  // [2 halves][2][64]
+  __syncthreads();
+#pragma unroll
+  for (int isq = 0; isq < 2; ++isq)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int row = r0 + 8 * p;
+      float s = 0.f;
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        const int c = ch * (DK / 2) + n * 8 + 2 * t;
+        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(kq + isq * DR_C * DK * 2 +
+                                                                       img_off(row, c >> 3, DK * 2) + (c & 7) * 2));
+        s += x.x * (isq ? q[n][2 * p] : k[n][2 * p]) + x.y * (isq ? q[n][2 * p + 1] : k[n][2 * p + 1]);
+      }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (t == 0) dots[(ch * 2 + isq) * DR_C + row] = s;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int isq = 0; isq < 2; ++isq)
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int row = r0 + 8 * p;
+      if (row >= cu.len) continue;
+      const float dot = (dots[isq * DR_C + row] + dots[(2 + isq) * DR_C + row]) * tf[(isq ? TF_PQ : TF_PK) * DR_C + row];
+      const float hs = tf[(isq ? TF_HQ : TF_HK) * DR_C + row];
+      __nv_bfloat16* out =
+          (isq ? a.dQ + (int64_t)(cu.tok + row) * a.ldq : a.dK + (int64_t)(cu.tok + row) * a.ldk) + (int64_t)hq * a.dk;
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        const int c = ch * (DK / 2) + n * 8 + 2 * t;
+        if (c >= a.dk) continue;
+        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(kq + isq * DR_C * DK * 2 +
+                                                                       img_off(row, c >> 3, DK * 2) + (c & 7) * 2));
+        const float y0 = hs * ((isq ? q[n][2 * p] : k[n][2 * p]) - x.x * dot);
+        const float y1 = hs * ((isq ? q[n][2 * p + 1] : k[n][2 * p + 1]) - x.y * dot);
+        *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(y0, y1);
+      }
+    }
+}
+
+}  // namespace ttt

@@ -4,6 +4,7 @@
 
 #include "host.cuh"
 #include "kernels_delta.cuh"
+#include "kernels_delta_bwd.cuh"
 #include "kernels_delta_seq.cuh"
 #include "ttt.h"
 
@@ -19,6 +20,8 @@ struct DeltaWs {
   uint8_t* blk;
   int blk_bytes;
   int64_t max_chunks;
+  // backward pass
+  float *tok, *keep_s, *keep_ds, *keep_e, *keep_z, *w_part, *b_part, *x_part;
   size_t total;
 };
 
@@ -42,13 +45,24 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
     return p;
   };
   w.max_chunks = T / DR_C + n_seq;
-  w.blk_bytes = DR_HBLK;
+  w.blk_bytes = DR_HBLK + (backward ? DR_TILE : 0);
   w.status = reinterpret_cast<unsigned int*>(take(256));
   w.seqs = reinterpret_cast<DrSeq*>(take((size_t)std::max(n_seq, 1) * sizeof(DrSeq)));
   w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
   if (dt == TTT_BF16) {
     w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
     w.blk = take((size_t)w.max_chunks * d.heads_v * w.blk_bytes);
+  }
+  if (dt == TTT_BF16 && backward) {
+    const size_t blocks = (size_t)w.max_chunks * d.heads_v, n16 = (d.dv + 15) / 16;
+    w.tok = reinterpret_cast<float*>(take((size_t)w.max_chunks * d.heads_qk * TF_N * DR_C * 4));
+    w.keep_s = reinterpret_cast<float*>(take(blocks * d.dv * d.dk * 4));
+    w.keep_ds = reinterpret_cast<float*>(take(blocks * d.dv * d.dk * 4));
+    w.keep_e = reinterpret_cast<float*>(take(blocks * d.dv * DR_C * 4));
+    w.keep_z = reinterpret_cast<float*>(take(blocks * d.dv * DR_C * 4));
+    w.w_part = reinterpret_cast<float*>(take(blocks * n16 * DR_C * 4));
+    w.b_part = reinterpret_cast<float*>(take(blocks * n16 * DR_C * 4));
+    w.x_part = reinterpret_cast<float*>(take(blocks * n16 * 4));
   }
   w.total = off;
   return w;
@@ -106,17 +120,41 @@ int state_warps(int64_t chains, int n16, int most) {
   return w;
 }
 
+// Launches a pass over the chunks of each sequence: blocks of `warps` x 16 value channels.
+template <typename Args>
+int launch_pass(void (*k)(Args), const Args& a, int n_seq, int warps, int smem, cudaStream_t s) {
+  const int n16 = (a.dv + 15) / 16;
+  TTT_TRY(smem_opt_in((const void*)k, smem));
+  TTT_TRY(launch_pdl(k, dim3(n_seq, (n16 + warps - 1) / warps, a.hv), dim3(warps * 32), smem, s, a));
+  TTT_LAUNCHED();
+  return TTT_OK;
+}
+
+template <int DK, bool BACK>
+int launch_prep(const PrepArgs& pa, const DeltaWs& w, cudaStream_t s) {
+  TTT_TRY(smem_opt_in((const void*)k_delta_prep<DK, BACK>, prep_smem<DK>()));
+  TTT_TRY(launch_pdl(k_delta_prep<DK, BACK>, dim3((unsigned)w.max_chunks, pa.hk), dim3(128), prep_smem<DK>(), s, pa));
+  TTT_LAUNCHED();
+  return TTT_OK;
+}
+
 template <int DK>
 int run_delta_fwd(const PrepArgs& pa, StateArgs sa, int n_seq, const DeltaWs& w, cudaStream_t s) {
-  const int psm = prep_smem<DK>();
-  TTT_TRY(smem_opt_in((const void*)k_delta_prep<DK, false>, psm));
-  TTT_TRY(launch_pdl(k_delta_prep<DK, false>, dim3((unsigned)w.max_chunks, pa.hk), dim3(128), psm, s, pa));
-  TTT_LAUNCHED();
-  const int n16 = (sa.dv + 15) / 16;
-  const int warps = state_warps((int64_t)n_seq * sa.hv, n16, DK >= 256 ? 4 : 8);
-  const int ssm = state_smem<DK>(warps);
-  TTT_TRY(smem_opt_in((const void*)k_delta_state<DK>, ssm));
-  TTT_TRY(launch_pdl(k_delta_state<DK>, dim3(n_seq, (n16 + warps - 1) / warps, sa.hv), dim3(warps * 32), ssm, s, sa));
+  TTT_TRY((launch_prep<DK, false>(pa, w, s)));
+  const int warps = state_warps((int64_t)n_seq * sa.hv, (sa.dv + 15) / 16, DK >= 256 ? 4 : 8);
+  return launch_pass(k_delta_state<DK, false>, sa, n_seq, warps, state_smem<DK, false>(warps), s);
+}
+
+template <int DK>
+int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, int n_seq,
+                  const DeltaWs& w, cudaStream_t s) {
+  TTT_TRY((launch_prep<DK, true>(pa, w, s)));
+  const int warps =
+      state_warps((int64_t)n_seq * sa.hv, (sa.dv + 15) / 16, DK >= 256 ? 2 : DK >= 128 ? 4 : 8);
+  TTT_TRY(launch_pass(k_delta_state<DK, true>, sa, n_seq, warps, state_smem<DK, true>(warps), s));
+  TTT_TRY(launch_pass(k_delta_reverse<DK>, ra, n_seq, warps, state_smem<DK, true>(warps), s));
+  TTT_TRY(smem_opt_in((const void*)k_delta_grad<DK>, grad_smem<DK>()));
+  TTT_TRY(launch_pdl(k_delta_grad<DK>, dim3((unsigned)w.max_chunks, ga.hk), dim3(256), grad_smem<DK>(), s, ga));
   TTT_LAUNCHED();
   return TTT_OK;
 }
@@ -171,6 +209,55 @@ SeqArgs<T> seq_args(const void* Q, const void* K, const void* V, const float* g,
   return a;
 }
 
+PrepArgs prep_args(const void* Q, const void* K, const float* g, const float* beta, float scale,
+                   const ttt_delta_dims& d, const DeltaIo& x, const DeltaWs& w) {
+  PrepArgs a{};
+  a.Q = (const __nv_bfloat16*)Q;
+  a.K = (const __nv_bfloat16*)K;
+  a.g = g;
+  a.beta = beta;
+  a.ldq = x.ldq;
+  a.ldk = x.ldk;
+  a.hk = d.heads_qk;
+  a.hv = d.heads_v;
+  a.dk = d.dk;
+  a.l2norm = x.l2norm;
+  a.scale = scale;
+  a.chunks = w.chunks;
+  a.kq = w.kq;
+  a.blk = w.blk;
+  a.blk_bytes = w.blk_bytes;
+  a.tok = w.tok;
+  return a;
+}
+
+// What the passes over the chunks share (StateArgs, ReverseArgs).
+template <typename Args>
+void pass_args(Args& a, const void* V, const ttt_delta_dims& d, const DeltaIo& x, const DeltaWs& w) {
+  a.V = (const __nv_bfloat16*)V;
+  a.ldv = x.ldv;
+  a.ldo = x.ldo;
+  a.hk = d.heads_qk;
+  a.hv = d.heads_v;
+  a.dk = d.dk;
+  a.dv = d.dv;
+  a.seqs = w.seqs;
+  a.kq = w.kq;
+  a.blk = w.blk;
+  a.blk_bytes = w.blk_bytes;
+  a.guard = Guard{w.status, wait_timeout_ns()};
+  a.keep_s = w.keep_s;
+  a.keep_e = w.keep_e;
+  a.w_part = w.w_part;
+}
+
+StateArgs state_args(const void* V, const float* S0, const ttt_delta_dims& d, const DeltaIo& x, const DeltaWs& w) {
+  StateArgs a{};
+  pass_args(a, V, d, x, w);
+  a.S0 = S0;
+  return a;
+}
+
 int delta_check_call(const ttt_delta_dims& d, ttt_dtype dt, int64_t T, int n_seq, bool packed, const ttt_io_cfg* io,
                      bool backward, void* ws, size_t ws_bytes) {
   if ((dt != TTT_FP32 && dt != TTT_BF16) || !delta_dims_ok(d) || T < 0 || n_seq < 0 || !io) return TTT_ERR_INVALID;
@@ -209,29 +296,87 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
     a.seqs = w.seqs;
     return run_tokens<float>(a, (unsigned)n_seq, s);
   }
-  PrepArgs pa{(const __nv_bfloat16*)Q, (const __nv_bfloat16*)K, g, beta, x.ldq, x.ldk, dims.heads_qk, dims.heads_v,
-              dims.dk, x.l2norm, scale, w.chunks, w.kq, w.blk, w.blk_bytes, nullptr};
-  StateArgs sa{};
-  sa.V = (const __nv_bfloat16*)V;
+  const PrepArgs pa = prep_args(Q, K, g, beta, scale, dims, x, w);
+  StateArgs sa = state_args(V, S0, dims, x, w);
   sa.O = (__nv_bfloat16*)O;
-  sa.ldv = x.ldv;
-  sa.ldo = x.ldo;
-  sa.S0 = S0;
   sa.S = S;
-  sa.hk = dims.heads_qk;
-  sa.hv = dims.heads_v;
-  sa.dk = dims.dk;
-  sa.dv = dims.dv;
-  sa.seqs = w.seqs;
-  sa.kq = w.kq;
-  sa.blk = w.blk;
-  sa.blk_bytes = w.blk_bytes;
-  sa.guard = Guard{w.status, wait_timeout_ns()};
   switch (dk_pad(dims.dk)) {
     case 64: return run_delta_fwd<64>(pa, sa, n_seq, w, s);
     case 128: return run_delta_fwd<128>(pa, sa, n_seq, w, s);
     case 192: return run_delta_fwd<192>(pa, sa, n_seq, w, s);
     default: return run_delta_fwd<256>(pa, sa, n_seq, w, s);
+  }
+}
+
+int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, const float* g, const float* beta,
+                               const float* S0, const void* dO, const float* dS, void* dQ, void* dK, void* dV,
+                               float* dg, float* dbeta, float* dS0, const int32_t* cu_seqlens, int n_seq, int64_t T,
+                               float scale, ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws,
+                               size_t ws_bytes, void* stream) {
+  if (dtype == TTT_FP32) return TTT_ERR_UNSUPPORTED;
+  TTT_TRY(delta_check_call(dims, dtype, T, n_seq, cu_seqlens != nullptr, io, true, ws, ws_bytes));
+  DeltaIo x;
+  const bool any = T > 0 && n_seq > 0;
+  TTT_TRY(delta_check(Q, K, V, g, beta, dO, dims, io, dtype, any, x));
+  for (const void* p : {(const void*)S0, (const void*)dS, (const void*)dS0})
+    if (!aligned16(p)) return TTT_ERR_ALIGN;
+  if (!aligned4(cu_seqlens) || !aligned4(dg) || !aligned4(dbeta)) return TTT_ERR_ALIGN;
+  if (any) {
+    TTT_TRY(check_rows(dQ, x.ldq, (int64_t)dims.heads_qk * dims.dk, dtype));
+    TTT_TRY(check_rows(dK, x.ldk, (int64_t)dims.heads_qk * dims.dk, dtype));
+    TTT_TRY(check_rows(dV, x.ldv, (int64_t)dims.heads_v * dims.dv, dtype));
+    if (!dg || !dbeta) return TTT_ERR_INVALID;
+    for (const void* out : {(const void*)dQ, (const void*)dK, (const void*)dV})
+      if (out == Q || out == K || out == V || out == dO) return TTT_ERR_INVALID;
+  }
+  if (n_seq == 0) return TTT_OK;
+  cudaStream_t s = (cudaStream_t)stream;
+  const DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, true);
+  ProfScope ps(TTT_PROF_DELTA, s);
+  TTT_TRY(launch_plan(cu_seqlens, n_seq, T, w, s));
+  const PrepArgs pa = prep_args(Q, K, g, beta, scale, dims, x, w);
+  StateArgs sa = state_args(V, S0, dims, x, w);
+  sa.dO = (const __nv_bfloat16*)dO;
+  ReverseArgs ra{};
+  pass_args(ra, V, dims, x, w);
+  ra.dO = (const __nv_bfloat16*)dO;
+  ra.dV = (__nv_bfloat16*)dV;
+  ra.dS = dS;
+  ra.dS0 = dS0;
+  ra.keep_ds = w.keep_ds;
+  ra.keep_z = w.keep_z;
+  ra.b_part = w.b_part;
+  ra.x_part = w.x_part;
+  GradArgs ga{};
+  ga.dO = (const __nv_bfloat16*)dO;
+  ga.ldo = x.ldo;
+  ga.ldq = x.ldq;
+  ga.ldk = x.ldk;
+  ga.dQ = (__nv_bfloat16*)dQ;
+  ga.dK = (__nv_bfloat16*)dK;
+  ga.dg = dg;
+  ga.dbeta = dbeta;
+  ga.hk = dims.heads_qk;
+  ga.hv = dims.heads_v;
+  ga.dk = dims.dk;
+  ga.dv = dims.dv;
+  ga.chunks = w.chunks;
+  ga.kq = w.kq;
+  ga.blk = w.blk;
+  ga.blk_bytes = w.blk_bytes;
+  ga.tok = w.tok;
+  ga.keep_s = w.keep_s;
+  ga.keep_e = w.keep_e;
+  ga.keep_ds = w.keep_ds;
+  ga.keep_z = w.keep_z;
+  ga.w_part = w.w_part;
+  ga.b_part = w.b_part;
+  ga.x_part = w.x_part;
+  switch (dk_pad(dims.dk)) {
+    case 64: return run_delta_bwd<64>(pa, sa, ra, ga, n_seq, w, s);
+    case 128: return run_delta_bwd<128>(pa, sa, ra, ga, n_seq, w, s);
+    case 192: return run_delta_bwd<192>(pa, sa, ra, ga, n_seq, w, s);
+    default: return run_delta_bwd<256>(pa, sa, ra, ga, n_seq, w, s);
   }
 }
 

@@ -92,6 +92,8 @@ def lib() -> ctypes.CDLL:
             "ttt_delta_workspace_bytes": (SZ, [DeltaDims, I64, I, I, I]),
             "ttt_delta_chunked": (I, [P, P, P, P, P, P, P, P, P, I, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P, SZ,
                                       P]),
+            "ttt_delta_chunked_backward": (I, [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, I, I64, F, DeltaDims,
+                                               ctypes.POINTER(IOCfg), I, P, SZ, P]),
             "ttt_delta_step": (I, [P, P, P, P, P, P, I, P, P, I64, F, DeltaDims, ctypes.POINTER(IOCfg), I, P]),
             "ttt_block_norm": (I, [P, P, P, P, P, P, P, P, I64, ctypes.POINTER(NormCfg), I, P]),
             "ttt_block_norm_workspace_bytes": (SZ, [ctypes.POINTER(NormCfg), I64]),
@@ -334,6 +336,23 @@ def ttt_delta_chunked(Q, K, V, g, beta, S0, S, O, T, dm: DeltaDims, io: IOCfg, w
     _check("ttt_delta_chunked", lib().ttt_delta_chunked(
         _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S0), _ptr(S), _ptr(O), _ptr(cu_seqlens), n_seq, T, scale,
         dm, ctypes.byref(io), dtype_code(K.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def ttt_delta_chunked_backward(Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbeta, dS0, T, dm: DeltaDims, io: IOCfg,
+                               ws, cu_seqlens=None, n_seq=1, scale=1.0, stream=None):
+    """The gradient of ttt_delta_chunked from dO and dS (None: zeros); S0, dS0 may be None."""
+    _same_device(Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbeta, dS0, cu_seqlens, ws)
+    _delta_tokens(Q, K, V, g, beta, T, dm, io)
+    _delta_tokens(dQ, dK, dV, dg, dbeta, T, dm, io)
+    _rows("dO", dO, T, dm.heads_v * dm.dv, io.ld_o, K.dtype)
+    if dK.dtype != K.dtype:
+        raise ValueError(f"dK is {dK.dtype}, expected {K.dtype}")
+    _delta_states(dm, n_seq, S0=S0, dS=dS, dS0=dS0)
+    _offsets(cu_seqlens, n_seq)
+    _check("ttt_delta_chunked_backward", lib().ttt_delta_chunked_backward(
+        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S0), _ptr(dO), _ptr(dS), _ptr(dQ), _ptr(dK), _ptr(dV),
+        _ptr(dg), _ptr(dbeta), _ptr(dS0), _ptr(cu_seqlens), n_seq, T, scale, dm, ctypes.byref(io),
+        dtype_code(K.dtype), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def ttt_delta_step(Q, K, V, g, beta, S, O, B, dm: DeltaDims, io: IOCfg, slots=None, scale=1.0, stream=None):
