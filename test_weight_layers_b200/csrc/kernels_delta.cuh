@@ -205,14 +205,16 @@ __global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
       // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
       const float inv = pow2i(-e), norm = sqrtf(ss);
       const bool normed = a.l2norm && norm * inv > 1e-12f;
-      float f = row < ch.len ? inv : 0.f;
-      if (a.l2norm && row < ch.len) f = normed ? 1.f / norm : inv * 1e12f;
+      float f = normed ? 1.f / norm : a.l2norm ? inv * 1e12f : inv;
       if (isq) f *= a.scale;
+      const float back = f * s;  // 1 / max(||k||, 1e-12) (or 1), for the way back
+      // a zero row has no scale to undo; its factor would only set the scale of what it is multiplied with
+      if (row >= ch.len || m == 0.f) f = 0.f;
       (isq ? fq : fk)[row] = f;
       if constexpr (BACK) {
         float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
         tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
-        tf[(isq ? TF_HQ : TF_HK) * DR_C] = f * s;
+        tf[(isq ? TF_HQ : TF_HK) * DR_C] = back;
         tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
       }
     }

@@ -12,7 +12,7 @@ namespace {
 constexpr int kNormMaxD = 8192;
 
 // How a call's rows map to kernel rows: groups become rows of their own where nothing ties the columns of a
-// row together but w_post (no second norm, no residual scale).
+// row together but w_post (no second norm, no residual scale or gradient over all columns).
 struct NormShape {
   int split, D, tpr, nv;
   bool groups;
@@ -195,7 +195,7 @@ int ttt_block_norm_backward(const void* X, const void* Y, const void* Z, const f
   if (T > 0 && (!Y || (!dXout && !dN))) return TTT_ERR_INVALID;
   if ((dZ && !Z && T > 0) || (dX && !X && T > 0)) return TTT_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
-  const NormShape sh = norm_shape(*cfg, dN || res_scale || dres_scale);
+  const NormShape sh = norm_shape(*cfg, dN || res_scale || dres_scale || dw_pre);
   ProfScope ps(TTT_PROF_BNORM, s);
   int64_t blocks = 0;
   if (T > 0) {
