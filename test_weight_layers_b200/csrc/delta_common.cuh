@@ -43,8 +43,8 @@ enum {
 // Bytes of a value head's chunk block: Y hi | Y lo | P hi | vectors (| P lo, for the backward pass)
 constexpr int DR_HBLK = 3 * DR_TILE + DR_NVEC * DR_C * 4;
 
-struct DrSeq {   // one sequence: first token, length (-1: the call is refused), first chunk
-  int tok, len, chunk0, pad;
+struct DrSeq {   // one sequence: first token, length (-1: the call is refused), first chunk, its number
+  int tok, len, chunk0, id;
 };
 struct DrChunk {  // one chunk: first token, tokens in it (-1: unused entry)
   int tok, len;

@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
                                                      unsigned int* status) {
   __shared__ int warp_sum[32];
   __shared__ int carry;
+  __shared__ int order[1024], key[1024];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = *(volatile unsigned int*)status != DEV_OK;
   const int even = n_seq > 0 ? T / n_seq : 0;  // without offsets: sequences of equal length
@@ -29,14 +30,39 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
       }
     }
   bad = __syncthreads_or(bad);
+  // up to 1024 sequences are taken longest first, so that the passes' long blocks start early
+  const bool sorted = cu && n_seq > 1 && n_seq <= 1024;
+  if (sorted) {
+    int n = 2;
+    while (n < n_seq) n <<= 1;
+    if (tid < n) {
+      order[tid] = tid;
+      key[tid] = tid < n_seq ? cu[tid + 1] - cu[tid] : INT32_MIN;
+    }
+    for (int k = 2; k <= n; k <<= 1)
+      for (int j = k >> 1; j; j >>= 1) {
+        __syncthreads();
+        const int o = tid ^ j;
+        if (tid < n && o > tid) {
+          const int a = key[tid], b = key[o], ia = order[tid], ib = order[o];
+          const bool after = a < b || (a == b && ia > ib);  // a belongs behind b
+          if (after == ((tid & k) == 0)) {
+            key[tid] = b, key[o] = a;
+            order[tid] = ib, order[o] = ia;
+          }
+        }
+      }
+    __syncthreads();
+  }
   if (tid == 0) carry = 0;
   __syncthreads();
   for (int i0 = 0; i0 < n_seq; i0 += 1024) {
     const int i = i0 + tid;
-    int tok = 0, len = 0;
+    int tok = 0, len = 0, id = i;
     if (i < n_seq) {
-      tok = cu ? cu[i] : i * even;
-      len = bad ? -1 : (cu ? cu[i + 1] - tok : even);
+      if (sorted) id = order[i];
+      tok = cu ? cu[id] : id * even;
+      len = bad ? -1 : (cu ? cu[id + 1] - tok : even);
     }
     const int n = len > 0 ? (len + DR_C - 1) / DR_C : 0;
     int sum = n;
@@ -56,7 +82,7 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
     }
     __syncthreads();
     const int first = carry + sum - n + (warp ? warp_sum[warp - 1] : 0);
-    if (i < n_seq) seqs[i] = DrSeq{tok, len, first, 0};
+    if (i < n_seq) seqs[i] = DrSeq{tok, len, first, id};
     __syncthreads();
     if (tid == 1023) carry = first + n;
     __syncthreads();
@@ -107,9 +133,11 @@ enum { TF_FK = 0, TF_FQ = 1, TF_HK = 2, TF_HQ = 3, TF_PK = 4, TF_PQ = 5, TF_N = 
 
 constexpr int PREP_LD = 68;  // floats per row of the fp32 64 x 64 tiles
 
+// The fp16 images are dead once their products are taken; the fp32 tiles L and Y take their place.
 template <int DK>
 constexpr int prep_smem() {
-  return 2 * DR_C * DK * 2 + 4 * DR_C * PREP_LD * 4 + DR_C * 8 + 8 * DR_C * 4;
+  constexpr int images = 2 * DR_C * DK * 2, tiles = 2 * DR_C * PREP_LD * 4;
+  return (images > tiles ? images : tiles) + DR_C * 8 + 3 * DR_C * 4;
 }
 
 // Row scale (a power of two) of row `i`'s 64 floats at `p`, over both half-row threads.
@@ -142,93 +170,105 @@ __device__ __forceinline__ void store_half_row(const float* p, int i, int half, 
 }
 
 template <int DK, bool BACK>
-__global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
+__global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int IMAGES = 2 * DR_C * DK * 2, TILES = 2 * DR_C * PREP_LD * 4;
   uint8_t* k16 = smem;
   uint8_t* q16 = k16 + DR_C * DK * 2;
-  float* KK = reinterpret_cast<float*>(q16 + DR_C * DK * 2);  // raw products of the scaled rows
-  float* QK = KK + DR_C * PREP_LD;
-  float* Lm = QK + DR_C * PREP_LD;
-  float* Ym = Lm + DR_C * PREP_LD;
-  double* c = reinterpret_cast<double*>(Ym + DR_C * PREP_LD);
+  float* Lm = reinterpret_cast<float*>(smem);
+  float* Ym = Lm + DR_C * PREP_LD;  // P first, then Y
+  double* c = reinterpret_cast<double*>(smem + (IMAGES > TILES ? IMAGES : TILES));
   float* fk = reinterpret_cast<float*>(c + DR_C);
   float* fq = fk + DR_C;
   float* bet = fq + DR_C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
   const int ci = blockIdx.x, hq = blockIdx.y;
   pdl_wait();
   const DrChunk ch = a.chunks[ci];
   if (ch.len < 0) return;
 
-  // token rows -> scaled fp16 images and their factors
+  // token rows -> scaled fp16 images and their factors: LPR lanes to a row, BATCH loads of a lane in flight
   uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
+  constexpr int LPR = DK <= 64 ? 8 : DK <= 128 ? 16 : 32, RPI = 32 / LPR, ITERS = 32 / RPI;
+  constexpr int BATCH = 8;
+  const int rl = lane % LPR, rsub = lane / LPR;
 #pragma unroll 1
-  for (int r = warp; r < 2 * DR_C; r += 4) {
-    const int row = r & (DR_C - 1);
-    const bool isq = r >= DR_C;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (row < ch.len && lane * 8 < a.dk) {
-      const __nv_bfloat16* p = isq ? a.Q + (int64_t)(ch.tok + row) * a.ldq : a.K + (int64_t)(ch.tok + row) * a.ldk;
-      raw = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)hq * a.dk + lane * 8));
-    }
-    float x[8];
+  for (int b0 = 0; b0 < ITERS; b0 += BATCH) {
+    uint4 raw[BATCH];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = (&raw.x)[j];
-      x[2 * j] = __uint_as_float(w << 16);
-      x[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = row_exp(m, DR_TOK_EXP);
-    const float s = pow2i(e);
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] *= s;
-      ss += x[j] * x[j];
-    }
-    if (lane * 8 < DK) {
-      uint4 h;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) (&h.x)[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
-      const uint32_t off = img_off(row, lane, DK * 2);
-      *reinterpret_cast<uint4*>((isq ? q16 : k16) + off) = h;
-      *reinterpret_cast<uint4*>(kq + (isq ? DR_C * DK * 2 : 0) + off) = h;
+    for (int b = 0; b < BATCH; ++b) {
+      const int r = warp * 32 + (b0 + b) * RPI + rsub;  // rows 0..63 are K's, 64..127 Q's
+      const int row = r & (DR_C - 1);
+      raw[b] = make_uint4(0, 0, 0, 0);
+      if (row < ch.len && rl * 8 < a.dk) {
+        const __nv_bfloat16* p =
+            r >= DR_C ? a.Q + (int64_t)(ch.tok + row) * a.ldq : a.K + (int64_t)(ch.tok + row) * a.ldk;
+        raw[b] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)hq * a.dk + rl * 8));
+      }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) {
-      // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
-      const float inv = pow2i(-e), norm = sqrtf(ss);
-      const bool normed = a.l2norm && norm * inv > 1e-12f;
-      float f = normed ? 1.f / norm : a.l2norm ? inv * 1e12f : inv;
-      if (isq) f *= a.scale;
-      const float back = f * s;  // 1 / max(||k||, 1e-12) (or 1), for the way back
-      // a zero row has no scale to undo; its factor would only set the scale of what it is multiplied with
-      if (row >= ch.len || m == 0.f) f = 0.f;
-      (isq ? fq : fk)[row] = f;
-      if constexpr (BACK) {
-        float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
-        tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
-        tf[(isq ? TF_HQ : TF_HK) * DR_C] = back;
-        tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
+    for (int b = 0; b < BATCH; ++b) {
+      const int r = warp * 32 + (b0 + b) * RPI + rsub;
+      const int row = r & (DR_C - 1);
+      const bool isq = r >= DR_C;
+      float x[8], m = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = (&raw[b].x)[j];
+        x[2 * j] = __uint_as_float(w << 16);
+        x[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
+        m = max_abs2(m, x[2 * j], x[2 * j + 1]);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int e = row_exp(m, DR_TOK_EXP);
+      const float s = pow2i(e);
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] *= s;
+        ss += x[j] * x[j];
+      }
+      if (rl * 8 < DK) {
+        uint4 h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) (&h.x)[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
+        const uint32_t off = img_off(row, rl, DK * 2);
+        *reinterpret_cast<uint4*>((isq ? q16 : k16) + off) = h;
+        *reinterpret_cast<uint4*>(kq + (isq ? DR_C * DK * 2 : 0) + off) = h;
+      }
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (rl == 0) {
+        // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
+        const float inv = pow2i(-e), norm = sqrtf(ss);
+        const bool normed = a.l2norm && norm * inv > 1e-12f;
+        float f = normed ? 1.f / norm : a.l2norm ? inv * 1e12f : inv;
+        if (isq) f *= a.scale;
+        const float back = f * s;  // 1 / max(||k||, 1e-12) (or 1), for the way back
+        // a zero row has no scale to undo; its factor would only set the scale of what it is multiplied with
+        if (row >= ch.len || m == 0.f) f = 0.f;
+        (isq ? fq : fk)[row] = f;
+        if constexpr (BACK) {
+          float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
+          tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
+          tf[(isq ? TF_HQ : TF_HK) * DR_C] = back;
+          tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
+        }
       }
     }
   }
   __syncthreads();
 
   // K16 K16^T and Q16 K16^T on and below the diagonal; warp w has rows [16 w, 16 w + 16)
+  float ak[8][4], aq[8][4];
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ak[n][j] = aq[n][j] = 0.f;
   {
     const uint32_t kb = smem_u32(k16), qb = smem_u32(q16);
-    float ak[8][4], aq[8][4];
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ak[n][j] = aq[n][j] = 0.f;
 #pragma unroll 2
     for (int kt = 0; kt < DK / 16; ++kt) {
       uint32_t fa[4], fb[4];
@@ -245,15 +285,6 @@ __global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
         mma_f16(aq[2 * np + 1], fb, b[2], b[3]);
       }
     }
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int col = n * 8 + 2 * t, r0 = warp * 16 + g;
-      *reinterpret_cast<float2*>(KK + r0 * PREP_LD + col) = make_float2(ak[n][0], ak[n][1]);
-      *reinterpret_cast<float2*>(KK + (r0 + 8) * PREP_LD + col) = make_float2(ak[n][2], ak[n][3]);
-      *reinterpret_cast<float2*>(QK + r0 * PREP_LD + col) = make_float2(aq[n][0], aq[n][1]);
-      *reinterpret_cast<float2*>(QK + (r0 + 8) * PREP_LD + col) = make_float2(aq[n][2], aq[n][3]);
-    }
   }
 
   const int rep = a.hv / a.hk;
@@ -262,47 +293,64 @@ __global__ void __launch_bounds__(128) k_delta_prep(const PrepArgs a) {
     const int h = hq * rep + hr;
     uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * a.blk_bytes;
     float* vec = reinterpret_cast<float*>(blk + 3 * DR_TILE);
-    __syncthreads();  // the tiles of the value head before are read
     // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
+    double s = 0.0;
     if (tid < DR_C) {
       const bool live = tid < ch.len;
       const int64_t at = (int64_t)(ch.tok + tid) * a.hv + h;
-      double s = live ? (double)a.g[at] : 0.0;
-      bet[tid] = live ? a.beta[at] : 0.f;
+      s = live ? (double)a.g[at] : 0.0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double v = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += v;
       }
+    }
+    __syncthreads();  // the images, or the tiles of the value head before, are read
+    if (tid < DR_C) {
       c[tid] = s;
+      bet[tid] = tid < ch.len ? a.beta[(int64_t)(ch.tok + tid) * a.hv + h] : 0.f;
     }
     __syncthreads();
-    if (tid >= 32 && tid < DR_C) c[tid] += c[31];  // (c[31] itself is not written here)
+    const double c31 = c[31];
+    // L and P in the products' layout
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int i = warp * 16 + g + 8 * p;
+      const double cii = c[i] + (i >= 32 ? c31 : 0.0);
+      const float fki = fk[i], fqi = fq[i];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int j = n * 8 + 2 * t;
+        float2 l = make_float2(0.f, 0.f), y = l;
+        if (n * 8 <= warp * 16 + 15) {
+          const double2 cj = *reinterpret_cast<const double2*>(c + j);
+          const double base = n >= 4 ? c31 : 0.0;
+          const float2 fj = *reinterpret_cast<const float2*>(fk + j);
+          if (j <= i) {
+            const float d = expf((float)(cii - (cj.x + base))) * fj.x;
+            y.x = d * fqi * aq[n][2 * p];
+            if (j < i) l.x = d * fki * ak[n][2 * p];
+          }
+          if (j + 1 <= i) {
+            const float d = expf((float)(cii - (cj.y + base))) * fj.y;
+            y.y = d * fqi * aq[n][2 * p + 1];
+            if (j + 1 < i) l.y = d * fki * ak[n][2 * p + 1];
+          }
+        }
+        *reinterpret_cast<float2*>(Lm + i * PREP_LD + j) = l;
+        *reinterpret_cast<float2*>(Ym + i * PREP_LD + j) = y;
+      }
+    }
     __syncthreads();
-    // L and P, two threads to a row
     const int i = tid >> 1, half = tid & 1;
     {
-      const double cii = c[i];
-      const float fki = fk[i], fqi = fq[i];
-      float* L = Lm + i * PREP_LD;
-      float* P = Ym + i * PREP_LD;
-#pragma unroll 4
-      for (int j = half * 32; j < half * 32 + 32; ++j) {
-        float l = 0.f, p = 0.f;
-        if (j <= i) {
-          const float d = expf((float)(cii - c[j])) * fk[j];
-          p = d * fqi * QK[i * PREP_LD + j];
-          if (j < i) l = d * fki * KK[i * PREP_LD + j];
-        }
-        L[j] = l;
-        P[j] = p;
-      }
-      __syncwarp();
+      const float* P = Ym + i * PREP_LD;
       const int e = half_row_exp(P, half);
       store_half_row(P, i, half, pow2i(e), blk + 2 * DR_TILE, BACK ? blk + DR_HBLK : nullptr);
       if (!half) {
-        const double G = c[DR_C - 1];
+        const double G = c[DR_C - 1] + c31, cii = c[i] + (i >= 32 ? c31 : 0.0);
         const float ec = expf((float)cii), el = expf((float)(G - cii));
+        const float fki = fk[i], fqi = fq[i];
         vec[DV_PS * DR_C + i] = pow2i(-e);
         vec[DV_AR * DR_C + i] = ec * fki;
         vec[DV_BETA * DR_C + i] = bet[i];
@@ -428,15 +476,16 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
-  const int h = blockIdx.z, hq = h / (a.hv / a.hk);
-  const int v0 = (blockIdx.y * nwarp + warp) * 16;  // first value channel of this warp (may lie past dv)
+  const int vblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
+  const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
+  const int v0 = (blockIdx.x % vblocks * nwarp + warp) * 16;  // first value channel of this warp (may lie past dv)
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
     fence_mbar_init();
   }
   pdl_wait();
-  const DrSeq sq = a.seqs[blockIdx.x];
+  const DrSeq sq = a.seqs[blockIdx.x / (vblocks * a.hv)];
   __syncthreads();
   if (sq.len < 0) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
@@ -456,7 +505,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   };
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)blockIdx.x * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll

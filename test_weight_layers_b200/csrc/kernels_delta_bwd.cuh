@@ -54,8 +54,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
-  const int h = blockIdx.z, hq = h / (a.hv / a.hk);
-  const int v0 = (blockIdx.y * nwarp + warp) * 16;
+  const int vblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
+  const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
+  const int v0 = (blockIdx.x % vblocks * nwarp + warp) * 16;
   const int n16 = (a.dv + 15) / 16;
   if (tid == 0) {
     mbar_init(&full[0], 1);
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     fence_mbar_init();
   }
   pdl_wait();
-  const DrSeq sq = a.seqs[blockIdx.x];
+  const DrSeq sq = a.seqs[blockIdx.x / (vblocks * a.hv)];
   __syncthreads();
   if (sq.len < 0) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
   };
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)blockIdx.x * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
     if (sq.len < 0) return;
     tok = sq.tok;
     len = sq.len;
+    state = sq.id;
   } else if (a.slots) {
     state = a.slots[blockIdx.x];
     if (state < 0 || state >= a.n_slots) return;

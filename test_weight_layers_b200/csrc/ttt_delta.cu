@@ -114,6 +114,7 @@ int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaS
 // Warps of a state-pass block (16 value channels each).  Fewer warps spread few heads over more SMs; more
 // share one staged copy of the chunk's operands.
 int state_warps(int64_t chains, int n16, int most) {
+  if (const char* e = getenv("DW")) return std::min(most, atoi(e));
   int w = std::min(most, 8);
   while (w > 1 && chains * ((n16 + w - 1) / w) < sm_count()) w >>= 1;
   while (w > 1 && (n16 + w - 1) / w == (n16 + w / 2 - 1) / (w / 2)) w >>= 1;  // no warps without channels
@@ -123,9 +124,10 @@ int state_warps(int64_t chains, int n16, int most) {
 // Launches a pass over the chunks of each sequence: blocks of `warps` x 16 value channels.
 template <typename Args>
 int launch_pass(void (*k)(Args), const Args& a, int n_seq, int warps, int smem, cudaStream_t s) {
-  const int n16 = (a.dv + 15) / 16;
+  const int64_t vblocks = (a.dv + warps * 16 - 1) / (warps * 16);
+  if (vblocks * a.hv * n_seq > INT32_MAX) return TTT_ERR_UNSUPPORTED;
   TTT_TRY(smem_opt_in((const void*)k, smem));
-  TTT_TRY(launch_pdl(k, dim3(n_seq, (n16 + warps - 1) / warps, a.hv), dim3(warps * 32), smem, s, a));
+  TTT_TRY(launch_pdl(k, dim3((unsigned)(vblocks * a.hv * n_seq)), dim3(warps * 32), smem, s, a));
   TTT_LAUNCHED();
   return TTT_OK;
 }
