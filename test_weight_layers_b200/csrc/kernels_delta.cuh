@@ -137,7 +137,7 @@ constexpr int PREP_LD = 68;  // floats per row of the fp32 64 x 64 tiles
 template <int DK>
 constexpr int prep_smem() {
   constexpr int images = 2 * DR_C * DK * 2, tiles = 2 * DR_C * PREP_LD * 4;
-  return (images > tiles ? images : tiles) + DR_C * 8 + 3 * DR_C * 4;
+  return (images > tiles ? images : tiles) + DR_C * 8 + 5 * DR_C * 4;
 }
 
 // Row scale (a power of two) of row `i`'s 64 floats at `p`, over both half-row threads.
@@ -169,6 +169,87 @@ __device__ __forceinline__ void store_half_row(const float* p, int i, int half, 
   }
 }
 
+// (I + L beta) Y = -L for the strictly lower L, in 16 x 16 blocks (128 threads).  The diagonal blocks by
+// forward substitution, a thread to a column; then, by their distance from the diagonal,
+//     Y_ij = T + Y_ii beta_i T,   T = -L_ij - sum_{j <= k < i} L_ik beta_k Y_kj
+// since (I + L_ii beta_i)^-1 = I + Y_ii beta_i.  Substitution over all 64 rows at once is a chain four times
+// as long that only half of the threads share: 8.8 us a block against 1.6 us.
+__device__ __forceinline__ void solve_y(const float* Lm, float* Ym, const float* bet, int tid) {
+  if (tid < DR_C) {
+    const int b0 = tid & ~15, cc = tid & 15;
+    float w[16];  // beta_j Y_j of this column
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const float* L = Lm + (b0 + r) * PREP_LD + b0;
+      float s0 = -L[cc], s1 = 0.f;  // L is zero on and above the diagonal
+#pragma unroll
+      for (int j = 0; j < r; j += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(L + j);
+        s0 -= l.x * w[j];
+        if (j + 1 < r) s1 -= l.y * w[j + 1];
+        if (j + 2 < r) s0 -= l.z * w[j + 2];
+        if (j + 3 < r) s1 -= l.w * w[j + 3];
+      }
+      const float y = cc < r ? s0 + s1 : 0.f;
+      w[r] = bet[b0 + r] * y;
+      Ym[(b0 + r) * PREP_LD + tid] = y;
+#pragma unroll
+      for (int d = 16; d < DR_C; d += 16)  // P lay here: zero the blocks above the diagonal
+        if (b0 >= d) Ym[(b0 - d + r) * PREP_LD + tid] = 0.f;
+    }
+  }
+  const int r = tid >> 3, c2 = (tid & 7) * 2;  // this thread's row and two columns of each block
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {
+    float2 v[3];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 4 - d; ++n) {  // block (n + d, n)
+      const float* L = Lm + ((n + d) * 16 + r) * PREP_LD;
+      float2 s = *reinterpret_cast<const float2*>(L + n * 16 + c2);
+      s.x = -s.x, s.y = -s.y;
+#pragma unroll
+      for (int k = 0; k < d; ++k)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const int kj = (n + k) * 16 + j;
+          const float4 l = *reinterpret_cast<const float4*>(L + kj);
+          const float4 b = *reinterpret_cast<const float4*>(bet + kj);
+          const float lb[4] = {l.x * b.x, l.y * b.y, l.z * b.z, l.w * b.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 y = *reinterpret_cast<const float2*>(Ym + (kj + q) * PREP_LD + n * 16 + c2);
+            s.x -= lb[q] * y.x;
+            s.y -= lb[q] * y.y;
+          }
+        }
+      *reinterpret_cast<float2*>(Ym + ((n + d) * 16 + r) * PREP_LD + n * 16 + c2) = s;  // T
+      v[n] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 4 - d; ++n) {
+      const int i0 = (n + d) * 16;
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(Ym + (i0 + r) * PREP_LD + i0 + j);
+        const float4 b = *reinterpret_cast<const float4*>(bet + i0 + j);
+        const float lb[4] = {l.x * b.x, l.y * b.y, l.z * b.z, l.w * b.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 y = *reinterpret_cast<const float2*>(Ym + (i0 + j + q) * PREP_LD + n * 16 + c2);
+          v[n].x += lb[q] * y.x;
+          v[n].y += lb[q] * y.y;
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 4 - d; ++n)
+      *reinterpret_cast<float2*>(Ym + ((n + d) * 16 + r) * PREP_LD + n * 16 + c2) = v[n];
+  }
+}
+
 template <int DK, bool BACK>
 __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -181,6 +262,7 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
   float* fk = reinterpret_cast<float*>(c + DR_C);
   float* fq = fk + DR_C;
   float* bet = fq + DR_C;
+  float* rowm = bet + DR_C;  // [128] row maxima
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int ci = blockIdx.x, hq = blockIdx.y;
@@ -188,78 +270,100 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
   const DrChunk ch = a.chunks[ci];
   if (ch.len < 0) return;
 
-  // token rows -> scaled fp16 images and their factors: LPR lanes to a row, BATCH loads of a lane in flight
+  // the first value head's gates, read ahead
+  const int rep = a.hv / a.hk;
+  float g_next = 0.f, b_next = 0.f;
+  const int64_t gate0 = (int64_t)(ch.tok + tid) * a.hv + hq * rep;
+  if (tid < ch.len) {
+    g_next = __ldg(a.g + gate0);
+    b_next = __ldg(a.beta + gate0);
+  }
+  // token rows -> scaled fp16 images: LPR lanes to a row, BATCH rows of a lane group in flight, each step taken
+  // for all of them before the next (the reductions' latency is what this phase costs)
   uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
   constexpr int LPR = DK <= 64 ? 8 : DK <= 128 ? 16 : 32, RPI = 32 / LPR, ITERS = 32 / RPI;
-  constexpr int BATCH = 8;
+  constexpr int BATCH = ITERS < 8 ? ITERS : 8;
   const int rl = lane % LPR, rsub = lane / LPR;
 #pragma unroll 1
   for (int b0 = 0; b0 < ITERS; b0 += BATCH) {
     uint4 raw[BATCH];
+    float m[BATCH], ss[BATCH];
+    // rows 0..63 are K's, 64..127 Q's; a warp has 32 rows of one of them
+    const bool isq = warp >= 2;
+    const int rb = (warp & 1) * 32 + b0 * RPI + rsub;
+    const __nv_bfloat16* src = (isq ? a.Q + (int64_t)ch.tok * a.ldq : a.K + (int64_t)ch.tok * a.ldk) +
+                               (int64_t)hq * a.dk + rl * 8;
+    const int64_t ld = isq ? a.ldq : a.ldk;
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int r = warp * 32 + (b0 + b) * RPI + rsub;  // rows 0..63 are K's, 64..127 Q's
-      const int row = r & (DR_C - 1);
+      const int row = rb + b * RPI;
       raw[b] = make_uint4(0, 0, 0, 0);
-      if (row < ch.len && rl * 8 < a.dk) {
-        const __nv_bfloat16* p =
-            r >= DR_C ? a.Q + (int64_t)(ch.tok + row) * a.ldq : a.K + (int64_t)(ch.tok + row) * a.ldk;
-        raw[b] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)hq * a.dk + rl * 8));
-      }
+      if (row < ch.len && rl * 8 < a.dk) raw[b] = __ldg(reinterpret_cast<const uint4*>(src + row * ld));
     }
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int r = warp * 32 + (b0 + b) * RPI + rsub;
-      const int row = r & (DR_C - 1);
-      const bool isq = r >= DR_C;
-      float x[8], m = 0.f;
+      m[b] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t w = (&raw[b].x)[j];
-        x[2 * j] = __uint_as_float(w << 16);
-        x[2 * j + 1] = __uint_as_float(w & 0xffff0000u);
-        m = max_abs2(m, x[2 * j], x[2 * j + 1]);
+        m[b] = max_abs2(m[b], __uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
       }
+    }
 #pragma unroll
-      for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int e = row_exp(m, DR_TOK_EXP);
-      const float s = pow2i(e);
-      float ss = 0.f;
+    for (int o = LPR / 2; o; o >>= 1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] *= s;
-        ss += x[j] * x[j];
+      for (int b = 0; b < BATCH; ++b) m[b] = fmaxf(m[b], __shfl_xor_sync(0xffffffffu, m[b], o));
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const float s = pow2i(row_exp(m[b], DR_TOK_EXP));
+      ss[b] = 0.f;
+      uint4 h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = (&raw[b].x)[j];
+        const float x = __uint_as_float(w << 16) * s, y = __uint_as_float(w & 0xffff0000u) * s;
+        ss[b] += x * x + y * y;
+        (&h.x)[j] = pack_f16x2(x, y);
       }
       if (rl * 8 < DK) {
-        uint4 h;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) (&h.x)[j] = pack_f16x2(x[2 * j], x[2 * j + 1]);
-        const uint32_t off = img_off(row, rl, DK * 2);
+        const uint32_t off = img_off(rb + b * RPI, rl, DK * 2);
         *reinterpret_cast<uint4*>((isq ? q16 : k16) + off) = h;
         *reinterpret_cast<uint4*>(kq + (isq ? DR_C * DK * 2 : 0) + off) = h;
       }
-#pragma unroll
-      for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (rl == 0) {
-        // k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
-        const float inv = pow2i(-e), norm = sqrtf(ss);
-        const bool normed = a.l2norm && norm * inv > 1e-12f;
-        float f = normed ? 1.f / norm : a.l2norm ? inv * 1e12f : inv;
-        if (isq) f *= a.scale;
-        const float back = f * s;  // 1 / max(||k||, 1e-12) (or 1), for the way back
-        // a zero row has no scale to undo; its factor would only set the scale of what it is multiplied with
-        if (row >= ch.len || m == 0.f) f = 0.f;
-        (isq ? fq : fk)[row] = f;
-        if constexpr (BACK) {
-          float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
-          tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
-          tf[(isq ? TF_HQ : TF_HK) * DR_C] = back;
-          tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
-        }
-      }
     }
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1)
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) ss[b] += __shfl_xor_sync(0xffffffffu, ss[b], o);
+    if (rl == 0)
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        rowm[(isq ? DR_C : 0) + rb + b * RPI] = m[b];
+        fk[(isq ? DR_C : 0) + rb + b * RPI] = ss[b];
+      }
   }
   __syncthreads();
+  {
+    // the rows' factors, one thread to a row: k^ = k / max(||k||, 1e-12) with ||k|| = 2^-e sqrt(ss)
+    const bool isq = tid >= DR_C;
+    const int row = tid & (DR_C - 1);
+    const float mm = rowm[tid], ss = fk[tid];
+    const int e = row_exp(mm, DR_TOK_EXP);
+    const float inv = pow2i(-e), norm = sqrtf(ss);
+    const bool normed = a.l2norm && norm * inv > 1e-12f;
+    float f = normed ? 1.f / norm : a.l2norm ? inv * 1e12f : inv;
+    if (isq) f *= a.scale;
+    const float back = f * pow2i(e);  // 1 / max(||k||, 1e-12) (or 1), for the way back
+    // a zero row has no scale to undo; its factor would only set the scale of what it is multiplied with
+    if (row >= ch.len || mm == 0.f) f = 0.f;
+    fk[tid] = f;  // (fq follows fk)
+    if constexpr (BACK) {
+      float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C + row;
+      tf[(isq ? TF_FQ : TF_FK) * DR_C] = f;
+      tf[(isq ? TF_HQ : TF_HK) * DR_C] = back;
+      tf[(isq ? TF_PQ : TF_PK) * DR_C] = normed ? 1.f / ss : 0.f;
+    }
+  }
 
   // K16 K16^T and Q16 K16^T on and below the diagonal; warp w has rows [16 w, 16 w + 16)
   float ak[8][4], aq[8][4];
@@ -287,18 +391,19 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
     }
   }
 
-  const int rep = a.hv / a.hk;
 #pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
     uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * a.blk_bytes;
     float* vec = reinterpret_cast<float*>(blk + 3 * DR_TILE);
     // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
-    double s = 0.0;
+    double s = (double)g_next;
+    const float b_now = b_next;
+    if (tid < ch.len && hr + 1 < rep) {
+      g_next = __ldg(a.g + gate0 + hr + 1);
+      b_next = __ldg(a.beta + gate0 + hr + 1);
+    }
     if (tid < DR_C) {
-      const bool live = tid < ch.len;
-      const int64_t at = (int64_t)(ch.tok + tid) * a.hv + h;
-      s = live ? (double)a.g[at] : 0.0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const double v = __shfl_up_sync(0xffffffffu, s, o);
@@ -308,7 +413,7 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
     __syncthreads();  // the images, or the tiles of the value head before, are read
     if (tid < DR_C) {
       c[tid] = s;
-      bet[tid] = tid < ch.len ? a.beta[(int64_t)(ch.tok + tid) * a.hv + h] : 0.f;
+      bet[tid] = b_now;
     }
     __syncthreads();
     const double c31 = c[31];
@@ -361,28 +466,7 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
       }
     }
     __syncthreads();
-    // (I + L beta) Y = -L by forward substitution, one column to a thread
-    if (tid < DR_C) {
-      float w[DR_C];  // beta_j Y_j of this column
-#pragma unroll
-      for (int r = 0; r < DR_C; ++r) {
-        const float* L = Lm + r * PREP_LD;
-        float s0 = -L[tid], s1 = 0.f, s2 = 0.f, s3 = 0.f;  // L is zero on and above the diagonal
-#pragma unroll
-        for (int j = 0; j + 3 < r; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(L + j);
-          s0 -= l.x * w[j];
-          s1 -= l.y * w[j + 1];
-          s2 -= l.z * w[j + 2];
-          s3 -= l.w * w[j + 3];
-        }
-#pragma unroll
-        for (int j = r & ~3; j < r; ++j) s1 -= L[j] * w[j];
-        const float y = tid < r ? (s0 + s1) + (s2 + s3) : 0.f;
-        w[r] = bet[r] * y;
-        Ym[r * PREP_LD + tid] = y;
-      }
-    }
+    solve_y(Lm, Ym, bet, tid);
     __syncthreads();
     const int e = half_row_exp(Ym + i * PREP_LD, half);
     store_half_row(Ym + i * PREP_LD, i, half, pow2i(e), blk, blk + DR_TILE);
