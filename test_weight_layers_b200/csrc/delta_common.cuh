@@ -43,8 +43,10 @@ enum {
 // Bytes of a value head's chunk block: Y hi | Y lo | P hi | vectors (| P lo, for the backward pass)
 constexpr int DR_HBLK = 3 * DR_TILE + DR_NVEC * DR_C * 4;
 
-struct DrSeq {   // one sequence: first token, length (-1: the call is refused), first chunk, its number
-  int tok, len, chunk0, id;
+// A sequence, or a segment of one: first token, tokens in it (-1: nothing to do), first chunk, the sequence's
+// number, the segment's number in it and how many it has.
+struct DrSeq {
+  int tok, len, chunk0, id, seg, nseg, pad0, pad1;
 };
 struct DrChunk {  // one chunk: first token, tokens in it (-1: unused entry)
   int tok, len;
@@ -75,6 +77,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four neighbouring 8-wide tiles: independent products in a row, so that the next four on the same accumulators
+// do not wait for them (a product's latency is that of four issues of one warp).
+__device__ __forceinline__ void mma_f16x4(float (*c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2][4]) {
+  mma_f16(c[0], a, b[0][0], b[0][1]);
+  mma_f16(c[1], a, b[0][2], b[0][3]);
+  mma_f16(c[2], a, b[1][0], b[1][1]);
+  mma_f16(c[3], a, b[1][2], b[1][3]);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {

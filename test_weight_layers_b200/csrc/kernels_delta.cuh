@@ -8,15 +8,16 @@
 namespace ttt {
 
 // ---------------------------------------------------------------------------
-// Chunk table.  One block: checks the offsets (0 <= cu[i] <= cu[i+1] <= T),
-// writes each sequence's first chunk and each chunk's first token and length.
-// Refused offsets, or an error already recorded in the status word, mark every
-// sequence with length -1: the kernels after it then write nothing.
-__global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu, int n_seq, int T, int max_chunks,
-                                                     DrSeq* __restrict__ seqs, DrChunk* __restrict__ chunks,
-                                                     unsigned int* status) {
-  __shared__ int warp_sum[32];
-  __shared__ int carry;
+// Chunk table.  One block: checks the offsets (0 <= cu[i] <= cu[i+1] <= T), cuts
+// the sequences into segments of seg_chunks chunks (0: none is cut), and writes
+// the segments and each chunk's first token and length.  Refused offsets, or an
+// error already recorded in the status word, mark every segment with length -1:
+// the kernels after it then write nothing.
+__global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu, int n_seq, int T, int seg_chunks,
+                                                     int max_segs, int max_chunks, DrSeq* __restrict__ seqs,
+                                                     DrChunk* __restrict__ chunks, unsigned int* status) {
+  __shared__ long long warp_sum[32];
+  __shared__ long long carry;
   __shared__ int order[1024], key[1024];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = *(volatile unsigned int*)status != DEV_OK;
@@ -65,35 +66,42 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
       len = bad ? -1 : (cu ? cu[id + 1] - tok : even);
     }
     const int n = len > 0 ? (len + DR_C - 1) / DR_C : 0;
-    int sum = n;
+    const int ns = i >= n_seq ? 0 : seg_chunks > 0 && n > 0 ? (n + seg_chunks - 1) / seg_chunks : 1;
+    const long long both = (long long)ns << 32 | n;  // segments and chunks, scanned together
+    long long sum = both;
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
     if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
     if (warp == 0) {
-      int w = warp_sum[lane];
+      long long w = warp_sum[lane];
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, w, o);
+        const long long v = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += v;
       }
       warp_sum[lane] = w;
     }
     __syncthreads();
-    const int first = carry + sum - n + (warp ? warp_sum[warp - 1] : 0);
-    if (i < n_seq) seqs[i] = DrSeq{tok, len, first, id};
+    const long long first = carry + sum - both + (warp ? warp_sum[warp - 1] : 0);
+    for (int k = 0; k < ns; ++k) {
+      const int c0 = k * seg_chunks;
+      const int l = ns == 1 ? len : min(seg_chunks * DR_C, len - c0 * DR_C);
+      seqs[(int)(first >> 32) + k] = DrSeq{tok + c0 * DR_C, l, (int)first + c0, id, k, ns, 0, 0};
+    }
     __syncthreads();
-    if (tid == 1023) carry = first + n;
+    if (tid == 1023) carry = first + both;
     __syncthreads();
   }
-  const int total = carry;
+  const int total = (int)carry, nsegs = (int)(carry >> 32);
+  for (int i = nsegs + tid; i < max_segs; i += 1024) seqs[i] = DrSeq{0, -1, 0, 0, 0, 1, 0, 0};
   __threadfence_block();
   __syncthreads();
   for (int c = tid; c < max_chunks; c += 1024) {
     DrChunk e{0, -1};
     if (c < total) {
-      int lo = 0, hi = n_seq - 1;  // the last sequence whose first chunk is <= c (empty ones before it share it)
+      int lo = 0, hi = nsegs - 1;  // the last segment whose first chunk is <= c (empty ones before it share it)
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (seqs[mid].chunk0 <= c) lo = mid;
@@ -483,6 +491,12 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
 // the writes U^T that of U^T K and U^T P^T.  No warp waits for another inside
 // a chunk; shared memory holds only what all warps read (K16, Q16, Y, P),
 // brought by bulk copies one chunk ahead.
+//
+// Few heads leave most SMs idle while a long sequence runs chunk by chunk.  S' is linear in S, so the sequence is
+// then cut into segments: the scan pass runs each from a zero state (N, its end) and from the unit matrix without
+// values (Phi, its transition, dk more rows of the same kind), the join pass chains S <- S Phi + N over the
+// segments, and the state pass proper starts each segment from its own state.  2.6 times the products of one pass
+// (dk = dv), on as many SMs as there are segments.
 struct StateArgs {
   const __nv_bfloat16* V;
   __nv_bfloat16* O;
@@ -495,6 +509,11 @@ struct StateArgs {
   const uint8_t* blk;
   int blk_bytes;
   Guard guard;
+  // segments: [segment][hv][dv][dk] states at their starts and scan results, [segment][hv] transitions (fp16 hi
+  // and lo images [DK][DK], rows scaled) and their rows' inverse scales [segment][hv][DK]
+  float *seg_s, *seg_n;
+  uint8_t* phi;
+  float* phi_scale;
   // backward pass: recompute the states, keep them and the errors, and sum dO . O
   const __nv_bfloat16* dO;  // rows of stride ldo
   float* keep_s;            // [chunk][hv][dv][dk]
@@ -504,6 +523,8 @@ struct StateArgs {
 
 constexpr int DR_VROW = 48;                  // bytes per row of a warp's V / O tile (32 used): conflict-free 8x8 tiles
 constexpr int DR_VTILE = DR_C * DR_VROW;
+
+enum { PASS_OUT = 0, PASS_BACK = 1, PASS_SCAN = 2 };  // what a state pass is for
 
 template <int DK, bool BACK>
 constexpr int state_stage() {
@@ -548,9 +569,10 @@ __device__ __forceinline__ uint32_t vtile_addr(uint32_t base, int lane, int n0) 
   return base + (n0 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4);
 }
 
-template <int DK, bool BACK>
+template <int DK, int PASS>
 __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr bool BACK = PASS == PASS_BACK, SCAN = PASS == PASS_SCAN;
   constexpr int STAGE = state_stage<DK, BACK>();
   constexpr int KQ = 2 * DR_C * DK * 2;
   constexpr int HB = STAGE - KQ;
@@ -560,43 +582,65 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
-  const int vblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
+  const int nblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
+  const int vblocks = nblocks + (SCAN ? (DK + nwarp * 16 - 1) / (nwarp * 16) : 0);
   const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
-  const int v0 = (blockIdx.x % vblocks * nwarp + warp) * 16;  // first value channel of this warp (may lie past dv)
+  const int vb0 = blockIdx.x % vblocks;
+  const bool phi = SCAN && vb0 >= nblocks;  // rows of the transition instead of value channels
+  const int v0 = ((phi ? vb0 - nblocks : vb0) * nwarp + warp) * 16;  // first row of this warp (may lie past the end)
+  const int dv_in = phi ? 0 : a.dv;  // the transition's rows take no values
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
     fence_mbar_init();
   }
   pdl_wait();
-  const DrSeq sq = a.seqs[blockIdx.x / (vblocks * a.hv)];
+  const int si = blockIdx.x / (vblocks * a.hv);
+  const DrSeq sq = a.seqs[si];
   __syncthreads();
   if (sq.len < 0) return;
+  // a last segment's scan has no use, nor has a first one's transition (nor, with two segments, any)
+  if (SCAN && (sq.seg == sq.nseg - 1 || (phi && sq.seg == 0))) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
   auto load_stage = [&](int n) {  // one thread
     const int64_t ci = sq.chunk0 + n;
     uint8_t* st = smem + (n & 1) * STAGE;
-    mbar_expect_tx(&full[n & 1], KQ + HB);
-    bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, &full[n & 1]);
-    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, &full[n & 1]);
+    const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
+    const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
+    if constexpr (SCAN) {  // without Q16 and P
+      mbar_expect_tx(&full[n & 1], KQ / 2 + HB - DR_TILE);
+      bulk_load(st, kq, KQ / 2, &full[n & 1]);
+      bulk_load(st + KQ, blk, 2 * DR_TILE, &full[n & 1]);
+      bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, &full[n & 1]);
+    } else {
+      mbar_expect_tx(&full[n & 1], KQ + HB);
+      bulk_load(st, kq, KQ, &full[n & 1]);
+      bulk_load(st + KQ, blk, HB, &full[n & 1]);
+    }
   };
   auto load_v = [&](int n) {
-    load_vtile(smem_u32(vbuf + (n & 1) * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
+    load_vtile(smem_u32(vbuf + (n & 1) * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, dv_in, lane);
     if constexpr (BACK)
       load_vtile(smem_u32(vbuf + (2 + (n & 1)) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
     cp_commit();
   };
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
+  // a first segment starts from S0; the others from the join's state, or in the scan from zero or the unit matrix
+  const float* from = sq.seg == 0 ? (a.S0 ? a.S0 + srow * a.dk : nullptr) : SCAN ? nullptr : a.seg_s + grow * a.dk;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
       float2 x = make_float2(0.f, 0.f);
-      if (a.S0 && r < a.dv && col < a.dk) x = *reinterpret_cast<const float2*>(a.S0 + (srow + r) * a.dk + col);
+      if (phi) {
+        if (r < a.dk) x = make_float2(col == r ? 1.f : 0.f, col + 1 == r ? 1.f : 0.f);
+      } else if (from && r < a.dv && col < a.dk) {
+        x = *reinterpret_cast<const float2*>(from + (int64_t)r * a.dk + col);
+      }
       s[n][2 * p] = x.x;
       s[n][2 * p + 1] = x.y;
     }
@@ -655,21 +699,19 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
       uint32_t hi[4], lo[4];
       split_a(s[2 * kt], s[2 * kt + 1], sc0, sc1, hi, lo);
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t b[4];
-        ldsm4(b, addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
-        mma_f16(r[2 * np], hi, b[0], b[1]);
-        mma_f16(r[2 * np + 1], hi, b[2], b[3]);
-        mma_f16(r[2 * np], lo, b[0], b[1]);
-        mma_f16(r[2 * np + 1], lo, b[2], b[3]);
-        // the outputs are rounded to bf16: S's hi part alone (2^-12) is enough for them
-        ldsm4(b, addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
-        mma_f16(o[2 * np], hi, b[0], b[1]);
-        mma_f16(o[2 * np + 1], hi, b[2], b[3]);
-        if constexpr (BACK) {  // the gates' gradients are sums of dO . O in fp32
-          mma_f16(o[2 * np], lo, b[0], b[1]);
-          mma_f16(o[2 * np + 1], lo, b[2], b[3]);
+      for (int np = 0; np < 4; np += 2) {
+        uint32_t b[2][4], c[2][4];
+        ldsm4(b[0], addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
+        ldsm4(b[1], addr_bn(kb, lane, np * 16 + 16, kt * 2, DK * 2));
+        mma_f16x4(r + 2 * np, hi, b);
+        if constexpr (!SCAN) {
+          // the outputs are rounded to bf16: S's hi part alone (2^-12) is enough for them
+          ldsm4(c[0], addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
+          ldsm4(c[1], addr_bn(qb, lane, np * 16 + 16, kt * 2, DK * 2));
+          mma_f16x4(o + 2 * np, hi, c);
         }
+        mma_f16x4(r + 2 * np, lo, b);
+        if constexpr (BACK) mma_f16x4(o + 2 * np, lo, c);  // the gates' gradients are sums of dO . O in fp32
       }
     }
     // R = V - e^c K S^T, then the scale of beta R
@@ -751,7 +793,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
       }
     }
     // O = e^c Q S^T + P U, accumulated in U's scale over P's row scales
-    {
+    if constexpr (!SCAN) {
       m0 = m1 = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -864,19 +906,51 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         uint32_t hi[4], lo[4];
         split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          uint32_t b[4];
-          ldsm4t(b, addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
-          mma_f16(s[2 * np], hi, b[0], b[1]);
-          mma_f16(s[2 * np + 1], hi, b[2], b[3]);
-          mma_f16(s[2 * np], lo, b[0], b[1]);
-          mma_f16(s[2 * np + 1], lo, b[2], b[3]);
+        for (int np = 0; np < DK / 16; np += 2) {
+          uint32_t b[2][4];
+          ldsm4t(b[0], addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
+          ldsm4t(b[1], addr_bk(kb, lane, kt * 16, np * 2 + 2, DK * 2));
+          mma_f16x4(s + 2 * np, hi, b);
+          mma_f16x4(s + 2 * np, lo, b);
         }
       }
     }
     __syncthreads();  // the stage is read; the next copy into it may start
   }
-  if (a.S) {
+  if (phi) {  // Phi as split images, each row at its own scale
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m0 = max_abs2(m0, s[n][0], s[n][1]);
+      m1 = max_abs2(m1, s[n][2], s[n][3]);
+    }
+    const int e0 = row_exp(quad_max(m0), DR_ROW_EXP), e1 = row_exp(quad_max(m1), DR_ROW_EXP);
+    if (v0 < DK) {
+      uint8_t* img = a.phi + ((int64_t)si * a.hv + h) * (2 * DK * DK * 2);
+      float* sc = a.phi_scale + ((int64_t)si * a.hv + h) * DK;
+      if (t == 0) {
+        sc[v0 + g] = inv0 * pow2i(-e0);
+        sc[v0 + g + 8] = inv1 * pow2i(-e1);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t hi, lo;
+          const float w = pow2i(p ? e1 : e0);
+          split2(s[n][2 * p] * w, s[n][2 * p + 1] * w, hi, lo);
+          const uint32_t off = img_off(v0 + g + 8 * p, n, DK * 2) + 4 * t;
+          *reinterpret_cast<uint32_t*>(img + off) = hi;
+          *reinterpret_cast<uint32_t*>(img + DK * DK * 2 + off) = lo;
+        }
+    }
+    return;
+  }
+  // the state after the sequence; in the scan, the start of the second segment or what a segment adds
+  float* to = a.S ? a.S + srow * a.dk : nullptr;
+  if (SCAN) to = sq.seg == 0 ? a.seg_s + (grow + (int64_t)a.hv * a.dv) * a.dk : a.seg_n + grow * a.dk;
+  else if (sq.seg < sq.nseg - 1) to = nullptr;
+  if (to) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -884,8 +958,161 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
         const float i = p ? inv1 : inv0;
         if (r < a.dv && col < a.dk)
-          *reinterpret_cast<float2*>(a.S + (srow + r) * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
+          *reinterpret_cast<float2*>(to + (int64_t)r * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
       }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join pass: the states at the segments' starts, from what the scan left,
+//     S_{k+1} = S_k Phi_k + N_k                (state pass)
+//     dS_{k-1} = dS_k Phi_k^T + N'_k           (REVERSE: gradient at the segments' ends)
+// A warp owns 16 rows and keeps them in registers over the segments; Phi comes in blocks of 64 rows
+// (of 64 columns of its transpose: the same bytes' rows hold them) through a ring of two stages.
+struct JoinArgs {
+  const DrSeq* seqs;
+  int hv, dk, dv;
+  float* seg_s;        // [segment][hv][dv][dk]: start states, or gradients at the ends
+  const float* seg_n;  // what each segment adds
+  const uint8_t* phi;
+  const float* phi_scale;
+  Guard guard;
+};
+
+template <int DK>
+constexpr int join_smem() {
+  return 2 * 2 * DR_C * DK * 2 + 2 * DK * 4 + 64;
+}
+
+template <int DK, bool REVERSE>
+__global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int NT = DK / 8, KB = DK / DR_C, BLK = DR_C * DK * 2;  // BLK: bytes of 64 rows of an image
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  float* scale = reinterpret_cast<float*>(smem + 4 * BLK);  // [2][DK] inverse row scales of Phi, by segment parity
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale + 2 * DK);
+  const int vblocks = (a.dv + 63) / 64;
+  const int h = blockIdx.x / vblocks % a.hv, v0 = (blockIdx.x % vblocks * 4 + warp) * 16;
+  const int si = blockIdx.x / (vblocks * a.hv);
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const DrSeq sq = a.seqs[si];
+  __syncthreads();
+  if (sq.len < 0 || sq.seg != 0 || sq.nseg < 3) return;
+  const int steps = sq.nseg - 2, total = steps * KB;  // segments 1 .. nseg - 2, in this order or from the last
+  auto seg_of = [&](int q) { return si + (REVERSE ? sq.nseg - 2 - q : 1 + q); };
+  auto load = [&](int q) {  // one thread: 64 rows of Phi, hi and lo
+    const uint8_t* img = a.phi + ((int64_t)seg_of(q / KB) * a.hv + h) * (2 * DK * DK * 2) + q % KB * BLK;
+    uint8_t* st = smem + (q & 1) * 2 * BLK;
+    mbar_expect_tx(&full[q & 1], 2 * BLK);
+    bulk_load(st, img, BLK, &full[q & 1]);
+    bulk_load(st + BLK, img + DK * DK * 2, BLK, &full[q & 1]);
+  };
+  float s[NT][4];
+  auto rows = [&](float* base, int seg, int n, int p) {  // this thread's pair of row 8 p, tile n; null past the end
+    const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+    return r < a.dv && col < a.dk ? base + (((int64_t)seg * a.hv + h) * a.dv + r) * a.dk + col : nullptr;
+  };
+  auto load_s = [&](int seg) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float* x = rows(a.seg_s, seg, n, p);
+        const float2 v = x ? *reinterpret_cast<const float2*>(x) : make_float2(0.f, 0.f);
+        s[n][2 * p] = v.x;
+        s[n][2 * p + 1] = v.y;
+      }
+  };
+  load_s(REVERSE ? si + sq.nseg - 2 : si + 1);
+  if (tid == 0) load(0);
+#pragma unroll 1
+  for (int q = 0; q < steps; ++q) {
+    const int seg = seg_of(q), to = REVERSE ? seg - 1 : seg + 1;
+    float* sc = scale + (q & 1) * DK;
+    for (int i = tid; i < DK; i += 128) sc[i] = a.phi_scale[((int64_t)seg * a.hv + h) * DK + i];
+    __syncthreads();
+    // forward: Phi's row scales meet S's columns; reverse: the result's columns
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (!REVERSE) {
+        const float2 f = *reinterpret_cast<const float2*>(sc + n * 8 + 2 * t);
+        s[n][0] *= f.x, s[n][1] *= f.y, s[n][2] *= f.x, s[n][3] *= f.y;
+      }
+      m0 = max_abs2(m0, s[n][0], s[n][1]);
+      m1 = max_abs2(m1, s[n][2], s[n][3]);
+    }
+    const int e0 = row_exp(quad_max(m0), DR_ROW_EXP), e1 = row_exp(quad_max(m1), DR_ROW_EXP);
+    const float w0 = pow2i(e0), w1 = pow2i(e1), i0 = pow2i(-e0), i1 = pow2i(-e1);
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int at = q * KB + kb;
+      if (tid == 0 && at + 1 < total) load(at + 1);
+      mbar_wait(&full[at & 1], (at >> 1) & 1, a.guard);
+      const uint32_t ph = smem_u32(smem + (at & 1) * 2 * BLK), pl = ph + BLK;
+      if constexpr (!REVERSE) {  // rows kb 64.. of Phi: 64 of the sum's terms, all columns
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int kt = kb * 4 + k4;
+          uint32_t hi[4], lo[4];
+          split_a(s[2 * kt], s[2 * kt + 1], w0, w1, hi, lo);
+#pragma unroll
+          for (int np = 0; np < DK / 16; np += 2) {
+            uint32_t b[2][4], c[2][4];
+            ldsm4t(b[0], addr_bk(ph, lane, k4 * 16, np * 2, DK * 2));
+            ldsm4t(b[1], addr_bk(ph, lane, k4 * 16, np * 2 + 2, DK * 2));
+            ldsm4t(c[0], addr_bk(pl, lane, k4 * 16, np * 2, DK * 2));
+            ldsm4t(c[1], addr_bk(pl, lane, k4 * 16, np * 2 + 2, DK * 2));
+            mma_f16x4(acc + 2 * np, hi, b);
+            mma_f16x4(acc + 2 * np, lo, b);
+            mma_f16x4(acc + 2 * np, hi, c);
+          }
+        }
+      } else {  // rows kb 64.. of Phi are these columns of the result: all terms
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt) {
+          uint32_t hi[4], lo[4];
+          split_a(s[2 * kt], s[2 * kt + 1], w0, w1, hi, lo);
+#pragma unroll
+          for (int np = 0; np < 4; np += 2) {
+            uint32_t b[2][4], c[2][4];
+            ldsm4(b[0], addr_bn(ph, lane, np * 16, kt * 2, DK * 2));
+            ldsm4(b[1], addr_bn(ph, lane, np * 16 + 16, kt * 2, DK * 2));
+            ldsm4(c[0], addr_bn(pl, lane, np * 16, kt * 2, DK * 2));
+            ldsm4(c[1], addr_bn(pl, lane, np * 16 + 16, kt * 2, DK * 2));
+            mma_f16x4(acc + kb * 8 + 2 * np, hi, b);
+            mma_f16x4(acc + kb * 8 + 2 * np, lo, b);
+            mma_f16x4(acc + kb * 8 + 2 * np, hi, c);
+          }
+        }
+      }
+      __syncthreads();  // the stage is read
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 f = REVERSE ? *reinterpret_cast<const float2*>(sc + n * 8 + 2 * t) : make_float2(1.f, 1.f);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float i = p ? i1 : i0;
+        const float* add = rows(const_cast<float*>(a.seg_n), seg, n, p);
+        const float2 v = add ? *reinterpret_cast<const float2*>(add) : make_float2(0.f, 0.f);
+        s[n][2 * p] = acc[n][2 * p] * i * f.x + v.x;
+        s[n][2 * p + 1] = acc[n][2 * p + 1] * i * f.y + v.y;
+        float* out = rows(a.seg_s, to, n, p);
+        if (out) *reinterpret_cast<float2*>(out) = make_float2(s[n][2 * p], s[n][2 * p + 1]);
+      }
+    }
   }
 }
 

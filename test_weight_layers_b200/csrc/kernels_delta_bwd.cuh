@@ -39,10 +39,13 @@ struct ReverseArgs {
   float* w_part;   // [chunk][hv][dv / 16][64]: dO.O in, dO.O - dV.V out
   float* b_part;   // [chunk][hv][dv / 16][64] E.Z
   float* x_part;   // [chunk][hv][dv / 16] <S, dS>
+  // segments: [segment][hv][dv][dk] gradients at their ends (of the segments before the last) and scan results
+  float *seg_ds, *seg_n;
 };
 
-// As the state pass: a warp owns 16 value channels and keeps dS [16][dk] in registers.
-template <int DK>
+// As the state pass: a warp owns 16 value channels and keeps dS [16][dk] in registers.  SCAN: only what a segment
+// adds to the gradient that passes through it (from zero; the last segment from dS).
+template <int DK, bool SCAN>
 __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int STAGE = state_stage<DK, true>();
@@ -64,9 +67,10 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     fence_mbar_init();
   }
   pdl_wait();
-  const DrSeq sq = a.seqs[blockIdx.x / (vblocks * a.hv)];
+  const int si = blockIdx.x / (vblocks * a.hv);
+  const DrSeq sq = a.seqs[si];
   __syncthreads();
-  if (sq.len < 0) return;
+  if (sq.len < 0 || (SCAN && sq.seg == 0)) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
   auto load_stage = [&](int n, int buf) {  // one thread
@@ -77,20 +81,22 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, &full[buf]);
   };
   auto load_v = [&](int n, int buf) {
-    load_vtile(smem_u32(vbuf + buf * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
+    if constexpr (!SCAN) load_vtile(smem_u32(vbuf + buf * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
     load_vtile(smem_u32(vbuf + (2 + buf) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
     cp_commit();
   };
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
+  const float* from = sq.seg == sq.nseg - 1 ? (a.dS ? a.dS + srow * a.dk : nullptr) : SCAN ? nullptr
+                                                                                         : a.seg_ds + grow * a.dk;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
       float2 x = make_float2(0.f, 0.f);
-      if (a.dS && r < a.dv && col < a.dk) x = *reinterpret_cast<const float2*>(a.dS + (srow + r) * a.dk + col);
+      if (from && r < a.dv && col < a.dk) x = *reinterpret_cast<const float2*>(from + (int64_t)r * a.dk + col);
       s[n][2 * p] = x.x;
       s[n][2 * p + 1] = x.y;
     }
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
       for (int p = 0; p < 2; ++p) {
         const int r = v0 + g + 8 * p, col = k * 8 + 2 * t;
         const float i = p ? inv1 : inv0;
-        if (r < a.dv && col < a.dk)
+        if (!SCAN && r < a.dv && col < a.dk)
           *reinterpret_cast<float2*>(a.keep_ds + (blk * a.dv + r) * a.dk + col) =
               make_float2(s[k][2 * p] * i, s[k][2 * p + 1] * i);
       }
@@ -268,50 +274,51 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
       }
     }
     // keep Z, the gates' row sums, dV = beta Z
+    if constexpr (!SCAN) {
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      uint32_t v[4], y[4];
-      ldsm4t(v, vtile_addr(vb, lane, np * 16));
+      for (int np = 0; np < 4; ++np) {
+        uint32_t v[4], y[4];
+        ldsm4t(v, vtile_addr(vb, lane, np * 16));
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int k = 2 * np + q, col = k * 8 + 2 * t;
-        const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
-        float ex = 0.f, ey = 0.f;
+        for (int q = 0; q < 2; ++q) {
+          const int k = 2 * np + q, col = k * 8 + 2 * t;
+          const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+          float ex = 0.f, ey = 0.f;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          if (v0 + g + 8 * p < a.dv) {
-            const int64_t at = (blk * a.dv + v0 + g + 8 * p) * DR_C + col;
-            *reinterpret_cast<float2*>(a.keep_z + at) = make_float2(r[k][2 * p], r[k][2 * p + 1]);
-            const float2 e = *reinterpret_cast<const float2*>(a.keep_e + at);
-            ex += e.x * r[k][2 * p];
-            ey += e.y * r[k][2 * p + 1];
+          for (int p = 0; p < 2; ++p)
+            if (v0 + g + 8 * p < a.dv) {
+              const int64_t at = (blk * a.dv + v0 + g + 8 * p) * DR_C + col;
+              *reinterpret_cast<float2*>(a.keep_z + at) = make_float2(r[k][2 * p], r[k][2 * p + 1]);
+              const float2 e = *reinterpret_cast<const float2*>(a.keep_e + at);
+              ex += e.x * r[k][2 * p];
+              ey += e.y * r[k][2 * p + 1];
+            }
+          const float d00 = be.x * r[k][0], d01 = be.y * r[k][1], d10 = be.x * r[k][2], d11 = be.y * r[k][3];
+          const uint32_t x0 = v[2 * q], x1 = v[2 * q + 1];
+          float wx = d00 * __uint_as_float(x0 << 16) + d10 * __uint_as_float(x1 << 16);
+          float wy = d01 * __uint_as_float(x0 & 0xffff0000u) + d11 * __uint_as_float(x1 & 0xffff0000u);
+#pragma unroll
+          for (int m = 4; m < 32; m <<= 1) {
+            ex += __shfl_xor_sync(0xffffffffu, ex, m);
+            ey += __shfl_xor_sync(0xffffffffu, ey, m);
+            wx += __shfl_xor_sync(0xffffffffu, wx, m);
+            wy += __shfl_xor_sync(0xffffffffu, wy, m);
           }
-        const float d00 = be.x * r[k][0], d01 = be.y * r[k][1], d10 = be.x * r[k][2], d11 = be.y * r[k][3];
-        const uint32_t x0 = v[2 * q], x1 = v[2 * q + 1];
-        float wx = d00 * __uint_as_float(x0 << 16) + d10 * __uint_as_float(x1 << 16);
-        float wy = d01 * __uint_as_float(x0 & 0xffff0000u) + d11 * __uint_as_float(x1 & 0xffff0000u);
-#pragma unroll
-        for (int m = 4; m < 32; m <<= 1) {
-          ex += __shfl_xor_sync(0xffffffffu, ex, m);
-          ey += __shfl_xor_sync(0xffffffffu, ey, m);
-          wx += __shfl_xor_sync(0xffffffffu, wx, m);
-          wy += __shfl_xor_sync(0xffffffffu, wy, m);
+          if (g == 0 && v0 < a.dv) {
+            const int64_t at = (blk * n16 + v0 / 16) * DR_C + col;
+            const float2 oo = *reinterpret_cast<const float2*>(a.w_part + at);
+            *reinterpret_cast<float2*>(a.w_part + at) = make_float2(oo.x - wx, oo.y - wy);
+            *reinterpret_cast<float2*>(a.b_part + at) = make_float2(ex, ey);
+          }
+          y[2 * q] = pack_bf16x2(d00, d01);
+          y[2 * q + 1] = pack_bf16x2(d10, d11);
         }
-        if (g == 0 && v0 < a.dv) {
-          const int64_t at = (blk * n16 + v0 / 16) * DR_C + col;
-          const float2 oo = *reinterpret_cast<const float2*>(a.w_part + at);
-          *reinterpret_cast<float2*>(a.w_part + at) = make_float2(oo.x - wx, oo.y - wy);
-          *reinterpret_cast<float2*>(a.b_part + at) = make_float2(ex, ey);
-        }
-        y[2 * q] = pack_bf16x2(d00, d01);
-        y[2 * q + 1] = pack_bf16x2(d10, d11);
+        __syncwarp();  // every lane has read these tokens of the V tile; dV takes their place
+        stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
       }
-      __syncwarp();  // every lane has read these tokens of the V tile; dV takes their place
-      stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
+      __syncwarp();
+      store_vtile(vbuf + buf * DR_VTILE, a.dV, a.ldv, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
     }
-    __syncwarp();
-    store_vtile(vbuf + buf * DR_VTILE, a.dV, a.ldv, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
-
     // dS = e^{c_C} dS' + (e^c dO)^T Q - (e^c beta Z)^T K
     {
       m0 = m1 = 0.f;
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
       }
     }
     // <S, dS> of these channels
-    {
+    if constexpr (!SCAN) {
       float x0 = 0.f, x1 = 0.f;
 #pragma unroll
       for (int k = 0; k < NT; ++k)
@@ -396,7 +403,11 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     }
     __syncthreads();  // the stage is read; the next copy into it may start
   }
-  if (a.dS0) {
+  // the gradient of the state before the sequence; in the scan, that at the end of the segment before the last or
+  // what a segment adds
+  float* to = a.dS0 && sq.seg == 0 ? a.dS0 + srow * a.dk : nullptr;
+  if (SCAN) to = sq.seg == sq.nseg - 1 ? a.seg_ds + (grow - (int64_t)a.hv * a.dv) * a.dk : a.seg_n + grow * a.dk;
+  if (to) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -404,8 +415,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
         const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
         const float i = p ? inv1 : inv0;
         if (r < a.dv && col < a.dk)
-          *reinterpret_cast<float2*>(a.dS0 + (srow + r) * a.dk + col) =
-              make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
+          *reinterpret_cast<float2*>(to + (int64_t)r * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
       }
   }
 }

@@ -20,6 +20,9 @@ struct DeltaWs {
   uint8_t* blk;
   int blk_bytes;
   int64_t max_chunks;
+  int seg_chunks, max_segs;  // chunks of a segment (0: sequences are not cut)
+  float *seg_s, *seg_n, *phi_scale;
+  uint8_t* phi;
   // backward pass
   float *tok, *keep_s, *keep_ds, *keep_e, *keep_z, *w_part, *b_part, *x_part;
   size_t total;
@@ -35,6 +38,26 @@ bool delta_dims_supported(const ttt_delta_dims& d) {
   return d.dk % 8 == 0 && d.dv % 8 == 0 && d.dk <= 256 && d.dv <= 1024 && d.heads_v <= 4096;
 }
 
+// Blocks of 4 warps (64 value channels) that the passes have for each sequence.
+int64_t pass_blocks(const ttt_delta_dims& d) { return (int64_t)d.heads_v * ((d.dv + 63) / 64); }
+
+// Segments.  Uncut, the passes have n_seq * pass_blocks blocks, each on its own SM for the length of a sequence.
+// Cut into k segments a sequence costs 2.6 times the products on k times the blocks, and a chain of k joins, so it is
+// cut where at least 3 segments fit on the card's 148 SMs and the sequences are long enough: 131,072 tokens, 4 heads
+// of 192: 10.1 ms uncut, 2.4 ms in 12 segments; 1,374 tokens: 117 us and 66 us.  Eight sequences of 16 heads leave
+// no SM idle and stay whole.  The length that goes into the rule is the mean one; the device cuts each by its own.
+constexpr int kDeltaSms = 148;
+int seg_chunks(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
+  if (dt != TTT_BF16 || n_seq < 1) return 0;
+  const int64_t blocks = pass_blocks(d) * n_seq, chunks = (T / n_seq + DR_C - 1) / DR_C;
+  const int64_t most = kDeltaSms / blocks;
+  if (most < 3 || chunks < 12) return 0;
+  // short sequences: a join costs about as much as a chunk of both passes, so neither many joins nor long segments
+  int64_t k = (chunks + most - 1) / most;
+  while (k * k * 2 < chunks) ++k;
+  return (int)k;
+}
+
 DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward) {
   DeltaWs w{};
   uint8_t* b = static_cast<uint8_t*>(base);
@@ -46,12 +69,21 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
   };
   w.max_chunks = T / DR_C + n_seq;
   w.blk_bytes = DR_HBLK + (backward ? DR_TILE : 0);
+  w.seg_chunks = seg_chunks(d, T, n_seq, dt);
+  w.max_segs = n_seq + (w.seg_chunks ? (int)(w.max_chunks / w.seg_chunks) : 0);
   w.status = reinterpret_cast<unsigned int*>(take(256));
-  w.seqs = reinterpret_cast<DrSeq*>(take((size_t)std::max(n_seq, 1) * sizeof(DrSeq)));
+  w.seqs = reinterpret_cast<DrSeq*>(take((size_t)std::max(w.max_segs, 1) * sizeof(DrSeq)));
   w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
   if (dt == TTT_BF16) {
     w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
     w.blk = take((size_t)w.max_chunks * d.heads_v * w.blk_bytes);
+  }
+  if (w.seg_chunks) {
+    const size_t segs = (size_t)w.max_segs * d.heads_v, dkp = dk_pad(d.dk);
+    w.seg_s = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
+    w.seg_n = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
+    w.phi = take(segs * 2 * dkp * dkp * 2);
+    w.phi_scale = reinterpret_cast<float*>(take(segs * dkp * 4));
   }
   if (dt == TTT_BF16 && backward) {
     const size_t blocks = (size_t)w.max_chunks * d.heads_v, n16 = (d.dv + 15) / 16;
@@ -106,30 +138,49 @@ int smem_opt_in(const void* fn, int bytes) {
 }
 
 int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaStream_t s) {
-  k_delta_plan<<<1, 1024, 0, s>>>(cu, n_seq, (int)T, (int)w.max_chunks, w.seqs, w.chunks, w.status);
+  k_delta_plan<<<1, 1024, 0, s>>>(cu, n_seq, (int)T, w.seg_chunks, w.max_segs, (int)w.max_chunks, w.seqs, w.chunks,
+                                  w.status);
   TTT_LAUNCHED();
   return TTT_OK;
 }
 
-// Warps of a state-pass block (16 value channels each).  Fewer warps spread few heads over more SMs; more
-// share one staged copy of the chunk's operands.
-int state_warps(int64_t chains, int n16, int most) {
-  if (const char* e = getenv("DW")) return std::min(most, atoi(e));
-  int w = std::min(most, 8);
-  while (w > 1 && chains * ((n16 + w - 1) / w) < sm_count()) w >>= 1;
-  while (w > 1 && (n16 + w - 1) / w == (n16 + w / 2 - 1) / (w / 2)) w >>= 1;  // no warps without channels
-  return w;
+// Warps of a pass block (16 value channels each): four, one to a sub-partition of the SM.  A warp's chain of products
+// is bound by its own latency, so eight share an SM at 0.6 of the speed each (packed prompts of 16 heads: 435 us
+// with 8, 260 with 4, 353 with 2, which share a staged copy of the operands with fewer); two where shared memory
+// holds no more (dk = 256 on the way back).
+template <int DK>
+constexpr int pass_warps(bool back) {
+  return back && DK > 192 ? 2 : 4;
 }
+int pass_warps_for(int most, int dv) { return std::min(most, (dv + 15) / 16); }
 
-// Launches a pass over the chunks of each sequence: blocks of `warps` x 16 value channels.
+// Launches a pass over the chunks of each segment.  `rows`: rows of 16 that share a block of `warps`, per head.
 template <typename Args>
-int launch_pass(void (*k)(Args), const Args& a, int n_seq, int warps, int smem, cudaStream_t s) {
-  const int64_t vblocks = (a.dv + warps * 16 - 1) / (warps * 16);
-  if (vblocks * a.hv * n_seq > INT32_MAX) return TTT_ERR_UNSUPPORTED;
+int launch_pass(void (*k)(Args), const Args& a, int segs, int64_t blocks_per_head, int warps, int smem,
+                cudaStream_t s) {
+  if (blocks_per_head * a.hv * segs > INT32_MAX) return TTT_ERR_UNSUPPORTED;
   TTT_TRY(smem_opt_in((const void*)k, smem));
-  TTT_TRY(launch_pdl(k, dim3((unsigned)(vblocks * a.hv * n_seq)), dim3(warps * 32), smem, s, a));
+  TTT_TRY(launch_pdl(k, dim3((unsigned)(blocks_per_head * a.hv * segs)), dim3(warps * 32), smem, s, a));
   TTT_LAUNCHED();
   return TTT_OK;
+}
+
+int64_t blocks_of(int rows, int warps) { return (rows + 16 * warps - 1) / (16 * warps); }
+
+template <int DK, bool REVERSE>
+int launch_join(const StateArgs& sa, float* seg_s, const DeltaWs& w, cudaStream_t s) {
+  JoinArgs ja{sa.seqs, sa.hv, sa.dk, sa.dv, seg_s, w.seg_n, w.phi, w.phi_scale, sa.guard};
+  return launch_pass(k_delta_join<DK, REVERSE>, ja, w.max_segs, (sa.dv + 63) / 64, 4, join_smem<DK>(), s);
+}
+
+// The states at the segments' starts (nothing to do for uncut sequences).
+template <int DK>
+int run_scan(const StateArgs& sa, const DeltaWs& w, cudaStream_t s) {
+  if (!w.seg_chunks) return TTT_OK;
+  const int warps = pass_warps<DK>(false);
+  TTT_TRY(launch_pass(k_delta_state<DK, PASS_SCAN>, sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
+                      warps, state_smem<DK, false>(warps), s));
+  return launch_join<DK, false>(sa, w.seg_s, w, s);
 }
 
 template <int DK, bool BACK>
@@ -141,20 +192,26 @@ int launch_prep(const PrepArgs& pa, const DeltaWs& w, cudaStream_t s) {
 }
 
 template <int DK>
-int run_delta_fwd(const PrepArgs& pa, StateArgs sa, int n_seq, const DeltaWs& w, cudaStream_t s) {
+int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream_t s) {
   TTT_TRY((launch_prep<DK, false>(pa, w, s)));
-  const int warps = state_warps((int64_t)n_seq * sa.hv, (sa.dv + 15) / 16, DK >= 256 ? 4 : 8);
-  return launch_pass(k_delta_state<DK, false>, sa, n_seq, warps, state_smem<DK, false>(warps), s);
+  TTT_TRY(run_scan<DK>(sa, w, s));
+  const int warps = pass_warps_for(pass_warps<DK>(false), sa.dv);
+  return launch_pass(k_delta_state<DK, PASS_OUT>, sa, w.max_segs, blocks_of(sa.dv, warps), warps,
+                     state_smem<DK, false>(warps), s);
 }
 
 template <int DK>
-int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, int n_seq,
-                  const DeltaWs& w, cudaStream_t s) {
+int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, const DeltaWs& w, cudaStream_t s) {
   TTT_TRY((launch_prep<DK, true>(pa, w, s)));
-  const int warps =
-      state_warps((int64_t)n_seq * sa.hv, (sa.dv + 15) / 16, DK >= 256 ? 2 : DK >= 128 ? 4 : 8);
-  TTT_TRY(launch_pass(k_delta_state<DK, true>, sa, n_seq, warps, state_smem<DK, true>(warps), s));
-  TTT_TRY(launch_pass(k_delta_reverse<DK>, ra, n_seq, warps, state_smem<DK, true>(warps), s));
+  TTT_TRY(run_scan<DK>(sa, w, s));
+  const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps);
+  const int64_t blocks = blocks_of(sa.dv, warps);
+  TTT_TRY(launch_pass(k_delta_state<DK, PASS_BACK>, sa, w.max_segs, blocks, warps, smem, s));
+  if (w.seg_chunks) {  // the transitions are the state pass's, transposed
+    TTT_TRY(launch_pass(k_delta_reverse<DK, true>, ra, w.max_segs, blocks, warps, smem, s));
+    TTT_TRY((launch_join<DK, true>(sa, w.seg_s, w, s)));
+  }
+  TTT_TRY(launch_pass(k_delta_reverse<DK, false>, ra, w.max_segs, blocks, warps, smem, s));
   TTT_TRY(smem_opt_in((const void*)k_delta_grad<DK>, grad_smem<DK>()));
   TTT_TRY(launch_pdl(k_delta_grad<DK>, dim3((unsigned)w.max_chunks, ga.hk), dim3(256), grad_smem<DK>(), s, ga));
   TTT_LAUNCHED();
@@ -251,12 +308,16 @@ void pass_args(Args& a, const void* V, const ttt_delta_dims& d, const DeltaIo& x
   a.keep_s = w.keep_s;
   a.keep_e = w.keep_e;
   a.w_part = w.w_part;
+  a.seg_n = w.seg_n;
 }
 
 StateArgs state_args(const void* V, const float* S0, const ttt_delta_dims& d, const DeltaIo& x, const DeltaWs& w) {
   StateArgs a{};
   pass_args(a, V, d, x, w);
   a.S0 = S0;
+  a.seg_s = w.seg_s;
+  a.phi = w.phi;
+  a.phi_scale = w.phi_scale;
   return a;
 }
 
@@ -303,10 +364,10 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
   sa.O = (__nv_bfloat16*)O;
   sa.S = S;
   switch (dk_pad(dims.dk)) {
-    case 64: return run_delta_fwd<64>(pa, sa, n_seq, w, s);
-    case 128: return run_delta_fwd<128>(pa, sa, n_seq, w, s);
-    case 192: return run_delta_fwd<192>(pa, sa, n_seq, w, s);
-    default: return run_delta_fwd<256>(pa, sa, n_seq, w, s);
+    case 64: return run_delta_fwd<64>(pa, sa, w, s);
+    case 128: return run_delta_fwd<128>(pa, sa, w, s);
+    case 192: return run_delta_fwd<192>(pa, sa, w, s);
+    default: return run_delta_fwd<256>(pa, sa, w, s);
   }
 }
 
@@ -349,6 +410,7 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
   ra.keep_z = w.keep_z;
   ra.b_part = w.b_part;
   ra.x_part = w.x_part;
+  ra.seg_ds = w.seg_s;  // (the start states are read by then)
   GradArgs ga{};
   ga.dO = (const __nv_bfloat16*)dO;
   ga.ldo = x.ldo;
@@ -375,10 +437,10 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
   ga.b_part = w.b_part;
   ga.x_part = w.x_part;
   switch (dk_pad(dims.dk)) {
-    case 64: return run_delta_bwd<64>(pa, sa, ra, ga, n_seq, w, s);
-    case 128: return run_delta_bwd<128>(pa, sa, ra, ga, n_seq, w, s);
-    case 192: return run_delta_bwd<192>(pa, sa, ra, ga, n_seq, w, s);
-    default: return run_delta_bwd<256>(pa, sa, ra, ga, n_seq, w, s);
+    case 64: return run_delta_bwd<64>(pa, sa, ra, ga, w, s);
+    case 128: return run_delta_bwd<128>(pa, sa, ra, ga, w, s);
+    case 192: return run_delta_bwd<192>(pa, sa, ra, ga, w, s);
+    default: return run_delta_bwd<256>(pa, sa, ra, ga, w, s);
   }
 }
 

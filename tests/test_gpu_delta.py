@@ -137,7 +137,11 @@ SHAPES = [
     ([70], 1, 1, 8, 8, 1, True, False),
     ([300], 1, 1, 64, 264, 1, False, False),     # more value channels than keys, past four blocks of 64
     ([0, 0], 1, 1, 64, 64, 1, True, False),
-    ([5000], 1, 1, 64, 64, 1, True, False),      # long enough for everything that depends on the length
+    ([5000], 1, 1, 64, 64, 1, True, False),      # few heads and long: cut into segments
+    ([1500, 0, 2100, 30, 1], 1, 1, 192, 192, 1, True, True),
+    ([1000, 1], 1, 2, 256, 64, 1, True, False),
+    ([1700, 800], 1, 2, 128, 72, 1, False, False),
+    ([1024, 1025], 2, 2, 40, 16, 0, True, False),
 ]
 
 
