@@ -968,7 +968,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
 //     S_{k+1} = S_k Phi_k + N_k                (state pass)
 //     dS_{k-1} = dS_k Phi_k^T + N'_k           (REVERSE: gradient at the segments' ends)
 // A warp owns 16 rows and keeps them in registers over the segments; Phi comes in blocks of 64 rows
-// (of 64 columns of its transpose: the same bytes' rows hold them) through a ring of two stages.
+// (of 64 columns of its transpose: the same bytes' rows hold them) through a ring of two stages, and what a
+// segment adds is copied in while its products run: nothing in a step waits for a load of its own.
 struct JoinArgs {
   const DrSeq* seqs;
   int hv, dk, dv;
@@ -981,7 +982,7 @@ struct JoinArgs {
 
 template <int DK>
 constexpr int join_smem() {
-  return 2 * 2 * DR_C * DK * 2 + 2 * DK * 4 + 64;
+  return 2 * 2 * DR_C * DK * 2 + 2 * DK * 4 + DR_C * DK * 4 + 64;
 }
 
 template <int DK, bool REVERSE>
@@ -991,13 +992,16 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   float* scale = reinterpret_cast<float*>(smem + 4 * BLK);  // [2][DK] inverse row scales of Phi, by segment parity
-  uint64_t* full = reinterpret_cast<uint64_t*>(scale + 2 * DK);
+  float* add = scale + 2 * DK;  // [64][dk] N of the step
+  uint64_t* full = reinterpret_cast<uint64_t*>(add + DR_C * DK);  // [2] ring, [1] N
   const int vblocks = (a.dv + 63) / 64;
-  const int h = blockIdx.x / vblocks % a.hv, v0 = (blockIdx.x % vblocks * 4 + warp) * 16;
+  const int h = blockIdx.x / vblocks % a.hv, row0 = blockIdx.x % vblocks * 64, v0 = row0 + warp * 16;
+  const uint32_t add_bytes = min(64, a.dv - row0) * a.dk * 4;
   const int si = blockIdx.x / (vblocks * a.hv);
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
+    mbar_init(&full[2], 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -1009,9 +1013,13 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
   auto load = [&](int q) {  // one thread: 64 rows of Phi, hi and lo
     const uint8_t* img = a.phi + ((int64_t)seg_of(q / KB) * a.hv + h) * (2 * DK * DK * 2) + q % KB * BLK;
     uint8_t* st = smem + (q & 1) * 2 * BLK;
-    mbar_expect_tx(&full[q & 1], 2 * BLK);
+    const bool first = q % KB == 0;  // the step's row scales come with its first block
+    mbar_expect_tx(&full[q & 1], 2 * BLK + (first ? DK * 4 : 0));
     bulk_load(st, img, BLK, &full[q & 1]);
     bulk_load(st + BLK, img + DK * DK * 2, BLK, &full[q & 1]);
+    if (first)
+      bulk_load(scale + (q / KB & 1) * DK, a.phi_scale + ((int64_t)seg_of(q / KB) * a.hv + h) * DK, DK * 4,
+                &full[q & 1]);
   };
   float s[NT][4];
   auto rows = [&](float* base, int seg, int n, int p) {  // this thread's pair of row 8 p, tile n; null past the end
@@ -1034,9 +1042,12 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
 #pragma unroll 1
   for (int q = 0; q < steps; ++q) {
     const int seg = seg_of(q), to = REVERSE ? seg - 1 : seg + 1;
-    float* sc = scale + (q & 1) * DK;
-    for (int i = tid; i < DK; i += 128) sc[i] = a.phi_scale[((int64_t)seg * a.hv + h) * DK + i];
-    __syncthreads();
+    const float* sc = scale + (q & 1) * DK;
+    if (tid == 0) {
+      mbar_expect_tx(&full[2], add_bytes);
+      bulk_load(add, a.seg_n + (((int64_t)seg * a.hv + h) * a.dv + row0) * a.dk, add_bytes, &full[2]);
+    }
+    mbar_wait(&full[(q * KB) & 1], ((q * KB) >> 1) & 1, a.guard);
     // forward: Phi's row scales meet S's columns; reverse: the result's columns
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -1099,20 +1110,23 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
       }
       __syncthreads();  // the stage is read
     }
+    mbar_wait(&full[2], q & 1, a.guard);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float2 f = REVERSE ? *reinterpret_cast<const float2*>(sc + n * 8 + 2 * t) : make_float2(1.f, 1.f);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const float i = p ? i1 : i0;
-        const float* add = rows(const_cast<float*>(a.seg_n), seg, n, p);
-        const float2 v = add ? *reinterpret_cast<const float2*>(add) : make_float2(0.f, 0.f);
+        const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
+        const float2 v = r < a.dv && col < a.dk ? *reinterpret_cast<const float2*>(add + (r - row0) * a.dk + col)
+                                                : make_float2(0.f, 0.f);
         s[n][2 * p] = acc[n][2 * p] * i * f.x + v.x;
         s[n][2 * p + 1] = acc[n][2 * p + 1] * i * f.y + v.y;
         float* out = rows(a.seg_s, to, n, p);
         if (out) *reinterpret_cast<float2*>(out) = make_float2(s[n][2 * p], s[n][2 * p + 1]);
       }
     }
+    __syncthreads();  // N is read
   }
 }
 
