@@ -28,7 +28,6 @@ struct NormArgs {
   int D;          // columns of a kernel row
   int group;      // columns per mean of y
   float eps;
-  int vec;        // rows are 16-byte aligned and D a multiple of 8
   int norm2;      // second norm present
   float* part;    // backward: [blocks][3][D] column sums of (w_post, lambda, w_pre)
 };
@@ -63,11 +62,12 @@ __device__ __forceinline__ Raw8<float> pack8(const float (&x)[8], float) {
   return r;
 }
 
-// Columns [col, col + 8) of a row, zero past D.  Plain loads: an output may be one of the inputs.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p, int col, int D, int vec) {
+// Columns [col, col + 8) of a row, zero past D.  VEC: rows and weights are 16-byte aligned, D a multiple of 8.
+// Plain loads: an output may be one of the inputs.
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int col, int D) {
   Raw8<T> r;
-  if (vec) {
+  if constexpr (VEC) {
 #pragma unroll
     for (int j = 0; j < (int)(sizeof(T) / 2); ++j)
       r.q[j] = col < D ? reinterpret_cast<const uint4*>(p + col)[j] : make_uint4(0, 0, 0, 0);
@@ -79,10 +79,10 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int col, int D, int vec) {
   }
   return r;
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int col, int D, int vec, const float (&x)[8]) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* p, int col, int D, const float (&x)[8]) {
   const Raw8<T> r = pack8(x, T());
-  if (vec) {
+  if constexpr (VEC) {
     if (col < D)
 #pragma unroll
       for (int j = 0; j < (int)(sizeof(T) / 2); ++j) reinterpret_cast<uint4*>(p + col)[j] = r.q[j];
@@ -94,23 +94,28 @@ __device__ __forceinline__ void store8(T* p, int col, int D, int vec, const floa
   }
 }
 // 8 weights from column `col` of a vector of `n` (ones where there is none, zero past n)
+template <bool VEC>
 __device__ __forceinline__ void weight8(const float* w, int col, int n, float (&x)[8]) {
-  if (!w) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 1.f;
-  } else if (col + 8 <= n && (reinterpret_cast<uintptr_t>(w + col) & 15u) == 0) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w + col));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(w + col + 4));
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  for (int j = 0; j < 8; ++j) x[j] = w ? 0.f : 1.f;
+  if (!w) return;
+  if constexpr (VEC) {
+    if (col < n) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(w + col));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(w + col + 4));
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = col + j < n ? __ldg(w + col + j) : 0.f;
+    for (int j = 0; j < 8; ++j)
+      if (col + j < n) x[j] = __ldg(w + col + j);
   }
 }
 
-// Sums over the TPR threads of a row (TPR = 32: a warp; else the whole block).
+// Sums over the TPR threads of a row (TPR = 32: a warp; else the whole block).  The sums of a row have a buffer
+// each, so that one barrier does: a buffer is written again only after the barriers of the others.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[TPR / 32]) {
 #pragma unroll
   for (int o = 16; o; o >>= 1)
 #pragma unroll
@@ -118,16 +123,18 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     const int warp = threadIdx.x >> 5;
-    __syncthreads();  // the sums before are read
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[i * W + warp] = v[i];
+      for (int i = 0; i < N; ++i) red[i][warp] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += red[i * W + w];
+      for (int w = 0; w < W; w += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&red[i][w]);
+        s += (x.x + x.y) + (x.z + x.w);
+      }
       v[i] = s;
     }
   }
@@ -158,33 +165,53 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], int t, int D, int grou
   }
 }
 
+// Where kernel row r starts: row r / split, part r % split of its columns, stepped without divisions.
+struct RowAt {
+  int64_t row;
+  int part;
+  __device__ __forceinline__ RowAt(int64_t r, int split) : row(split == 1 ? r : r / split), part(split == 1 ? 0 : (int)(r % split)) {}
+  __device__ __forceinline__ void step(const RowAt& by, int split) {
+    row += by.row;
+    part += by.part;
+    if (part >= split) part -= split, ++row;
+  }
+  template <typename T>
+  __device__ __forceinline__ T* in(T* p, int64_t ld, int D) const {
+    return p + row * ld + part * D;
+  }
+};
+
+// The logistic function.  bf16 rows take the hardware's exponential and reciprocal (2^-21, far below the outputs'
+// rounding): the exact ones are a third of the instructions of a pass that is otherwise bound by HBM.
 template <typename T>
-__device__ __forceinline__ T* norm_row(T* p, int64_t row, int64_t ld, const NormArgs<std::remove_const_t<T>>& a) {
-  if (!p) return nullptr;
-  if (a.split == 1) return p + row * ld;
-  return p + row / a.split * ld + row % a.split * a.D;
+__device__ __forceinline__ float sigmoid_f(float z) {
+  if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
+  else return 1.f / (1.f + expf(-z));
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
-
 // TPR threads to a row, NV chunks of 8 columns to a thread; GROUPS: several means of y to a row.
-template <typename T, int TPR, int NV, bool GROUPS>
+// Measured (131,072 x 768, bf16, all operands): NORM_F.
+template <typename T, int TPR, int NV, bool GROUPS, bool VEC>
 __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm(const NormArgs<T> a) {
   constexpr int BLOCK = TPR > 128 ? TPR : 128;
   constexpr int RPB = BLOCK / TPR;  // rows per block
-  __shared__ float red[TPR / 32 + 1];
+  __shared__ __align__(16) float red[2][TPR / 32];
   extern __shared__ float gbuf[];
   const int t = threadIdx.x % TPR, rb = threadIdx.x / TPR;
   float* buf = gbuf + rb * ((a.D + 7) / 8);
-  for (int64_t row = (int64_t)blockIdx.x * RPB + rb; row < a.rows; row += (int64_t)gridDim.x * RPB) {
-    const T *xr = norm_row(a.X, row, a.ldx, a), *yr = norm_row(a.Y, row, a.ldy, a), *zr = norm_row(a.Z, row, a.ldz, a);
+  const bool xr = a.X != nullptr, zr = a.Z != nullptr;
+  const float inv_group = 1.f / (float)a.group, inv_d = 1.f / (float)a.D;
+  const int64_t r0 = (int64_t)blockIdx.x * RPB + rb, step = (int64_t)gridDim.x * RPB;
+  RowAt at(r0, a.split);
+  const RowAt by(step, a.split);
+  for (int64_t row = r0; row < a.rows; row += step, at.step(by, a.split)) {
     Raw8<T> y[NV], x[NV], z[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      y[i] = load8(yr, col, a.D, a.vec);
-      if (zr) z[i] = load8(zr, col, a.D, a.vec);
-      if (xr) x[i] = load8(xr, col, a.D, a.vec);
+      y[i] = load8<VEC>(at.in(a.Y, a.ldy, a.D), col, a.D);
+      if (zr) z[i] = load8<VEC>(at.in(a.Z, a.ldz, a.D), col, a.D);
+      if (xr) x[i] = load8<VEC>(at.in(a.X, a.ldx, a.D), col, a.D);
     }
     float sy[NV], s1[1] = {0.f};
 #pragma unroll
@@ -198,193 +225,201 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm(const Norm
     }
     if constexpr (GROUPS) group_sum<TPR>(sy, t, a.D, a.group, buf);
     else row_sum<TPR>(s1, red);
+    const float ry1 = rsqrtf(s1[0] * inv_group + a.eps);
     float p[NV][8], s2[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      const float ry = rsqrtf((GROUPS ? sy[i] : s1[0]) / (float)a.group + a.eps);
-      float w[8], l[8], v[8];
+      const float ry = GROUPS ? rsqrtf(sy[i] * inv_group + a.eps) : ry1;
+      float w[8], v[8];
       unpack8(y[i], p[i]);
-      weight8(a.w_post, GROUPS ? col % a.group : col, a.group, w);
+      weight8<VEC>(a.w_post, GROUPS ? col % a.group : col, a.group, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[i][j] = p[i][j] * ry * w[j];
       if (zr) {
         unpack8(z[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[i][j] *= v[j] * sigmoid_f(v[j]);
+        for (int j = 0; j < 8; ++j) p[i][j] *= v[j] * sigmoid_f<T>(v[j]);
       }
       if (a.lam) {
-        weight8(a.lam, col, a.D, l);
+        weight8<VEC>(a.lam, col, a.D, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[i][j] *= l[j];
+        for (int j = 0; j < 8; ++j) p[i][j] *= w[j];
       }
       if (xr) {
         unpack8(x[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[i][j] += v[j];
       }
-      if (a.Xo) store8(norm_row(a.Xo, row, a.ldxo, a), col, a.D, a.vec, p[i]);
+      if (a.Xo) store8<VEC>(at.in(a.Xo, a.ldxo, a.D), col, a.D, p[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s2[0] += p[i][j] * p[i][j];
     }
     if (a.N) {
-      row_sum<TPR>(s2, red);
-      const float r = rsqrtf(s2[0] / (float)a.D + a.eps);
+      row_sum<TPR>(s2, red + 1);
+      const float r = rsqrtf(s2[0] * inv_d + a.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + t) * 8;
         float w[8];
-        weight8(a.w_pre, col, a.D, w);
+        weight8<VEC>(a.w_pre, col, a.D, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[i][j] *= r * w[j];
-        store8(norm_row(a.N, row, a.ldn, a), col, a.D, a.vec, p[i]);
+        store8<VEC>(at.in(a.N, a.ldn, a.D), col, a.D, p[i]);
       }
+    } else if (TPR > 32 && !GROUPS) {
+      __syncthreads();  // a row with one sum only: its buffer is read
     }
   }
 }
 
-template <typename T, int TPR, int NV, bool GROUPS>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm_bwd(const NormArgs<T> a) {
+// The gradient.  A thread keeps its columns for all its rows: their weights and their sums stay in registers, and
+// the next row's loads are in flight while one is worked on.
+// Measured (65,536 x 2,048, bf16, all operands): NORM_B.
+template <typename T, int TPR, int NV, bool GROUPS, bool VEC>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 512 / TPR : 4) : 1)
+    k_block_norm_bwd(const NormArgs<T> a) {
   constexpr int BLOCK = TPR > 128 ? TPR : 128;
   constexpr int RPB = BLOCK / TPR;
-  __shared__ float red[2 * (TPR / 32) + 1];
+  __shared__ __align__(16) float red[4][TPR / 32];  // sum 0, the two of sum 1, sum 2
   extern __shared__ float gbuf[];
   const int t = threadIdx.x % TPR, rb = threadIdx.x / TPR;
   float* buf = gbuf + rb * ((a.D + 7) / 8);
+  const bool xr = a.X != nullptr, zr = a.Z != nullptr, gr = a.dXo != nullptr, nr = a.dN != nullptr;
+  const float inv_group = 1.f / (float)a.group, inv_d = 1.f / (float)a.D;
   float c_post[NV][8], c_lam[NV][8], c_pre[NV][8];  // this thread's column sums
+  float wq[NV][8], lm[NV][8], wp[NV][8];            // and its columns' weights
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * TPR + t) * 8;
+    weight8<VEC>(a.w_post, GROUPS ? col % a.group : col, a.group, wq[i]);
+    weight8<VEC>(a.lam, col, a.D, lm[i]);
+    weight8<VEC>(a.w_pre, col, a.D, wp[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) c_post[i][j] = c_lam[i][j] = c_pre[i][j] = 0.f;
-
-  for (int64_t row = (int64_t)blockIdx.x * RPB + rb; row < a.rows; row += (int64_t)gridDim.x * RPB) {
-    const T *xr = norm_row(a.X, row, a.ldx, a), *yr = norm_row(a.Y, row, a.ldy, a), *zr = norm_row(a.Z, row, a.ldz, a);
-    const T *gr = norm_row(a.dXo, row, a.ldxo, a), *nr = norm_row(a.dN, row, a.ldn, a);
-    Raw8<T> y[NV], x[NV], z[NV], gx[NV], gn[NV];
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * RPB + rb, step = (int64_t)gridDim.x * RPB;
+  RowAt at(r0, a.split), ahead = at;
+  const RowAt by(step, a.split);
+  Raw8<T> ny[NV], nx[NV], nz[NV], ngx[NV], ngn[NV];
+  auto load_row = [&] {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      y[i] = load8(yr, col, a.D, a.vec);
-      if (zr) z[i] = load8(zr, col, a.D, a.vec);
-      if (gr) gx[i] = load8(gr, col, a.D, a.vec);
+      ny[i] = load8<VEC>(ahead.in(a.Y, a.ldy, a.D), col, a.D);
+      if (zr) nz[i] = load8<VEC>(ahead.in(a.Z, a.ldz, a.D), col, a.D);
+      if (gr) ngx[i] = load8<VEC>(ahead.in(a.dXo, a.ldxo, a.D), col, a.D);
       if (nr) {
-        gn[i] = load8(nr, col, a.D, a.vec);
-        if (xr) x[i] = load8(xr, col, a.D, a.vec);
+        ngn[i] = load8<VEC>(ahead.in(a.dN, a.ldn, a.D), col, a.D);
+        if (xr) nx[i] = load8<VEC>(ahead.in(a.X, a.ldx, a.D), col, a.D);
       }
     }
+    ahead.step(by, a.split);
+  };
+  if (r0 < a.rows) load_row();
+  for (int64_t row = r0; row < a.rows; row += step, at.step(by, a.split)) {
+    Raw8<T> x[NV], z[NV], gx[NV], gn[NV];
+    float yh[NV][8];
     float sy[NV], s1[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float v[8];
-      unpack8(y[i], v);
+      unpack8(ny[i], yh[i]);
+      x[i] = nx[i], z[i] = nz[i], gx[i] = ngx[i], gn[i] = ngn[i];
       sy[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sy[i] += v[j] * v[j];
+      for (int j = 0; j < 8; ++j) sy[i] += yh[i][j] * yh[i][j];
       s1[0] += sy[i];
     }
+    if (row + step < a.rows) load_row();
     if constexpr (GROUPS) group_sum<TPR>(sy, t, a.D, a.group, buf);
     else row_sum<TPR>(s1, red);
-    // x' again, and the two sums of its norm
+    // s(z), s'(z), x' again, and the two sums of its norm
+    float sl[NV][8], ds[NV][8], xo[NV][8], ry[NV];
     float s2[2] = {0.f, 0.f};  // sum x'^2, sum t x'
-    float r = 0.f, m = 0.f;
-    if (nr) {
+    const float ry1 = rsqrtf(s1[0] * inv_group + a.eps);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + t) * 8;
-        const float ry = rsqrtf((GROUPS ? sy[i] : s1[0]) / (float)a.group + a.eps);
-        float p[8], w[8], l[8], v[8];
-        unpack8(y[i], p);
-        weight8(a.w_post, GROUPS ? col % a.group : col, a.group, w);
-        weight8(a.lam, col, a.D, l);
+    for (int i = 0; i < NV; ++i) {
+      ry[i] = GROUPS ? rsqrtf(sy[i] * inv_group + a.eps) : ry1;
+      float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] *= ry * w[j] * l[j];
-        if (zr) {
-          unpack8(z[i], v);
+      for (int j = 0; j < 8; ++j) yh[i][j] *= ry[i], sl[i][j] = 1.f, ds[i][j] = 0.f;
+      if (zr) {
+        unpack8(z[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] *= v[j] * sigmoid_f(v[j]);
+        for (int j = 0; j < 8; ++j) {
+          const float sg = sigmoid_f<T>(v[j]);
+          sl[i][j] = v[j] * sg;
+          ds[i][j] = sg + sl[i][j] * (1.f - sg);
         }
+      }
+      if (nr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xo[i][j] = lm[i][j] * (yh[i][j] * sl[i][j] * wq[i][j]);
         if (xr) {
           unpack8(x[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] += v[j];
+          for (int j = 0; j < 8; ++j) xo[i][j] += v[j];
         }
         unpack8(gn[i], v);
-        weight8(a.w_pre, col, a.D, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s2[0] += p[j] * p[j];
-          s2[1] += v[j] * w[j] * p[j];
+          s2[0] += xo[i][j] * xo[i][j];
+          s2[1] += v[j] * wp[i][j] * xo[i][j];
         }
       }
-      row_sum<TPR>(s2, red);
-      r = rsqrtf(s2[0] / (float)a.D + a.eps);
-      m = r * r * (s2[1] / (float)a.D);
+    }
+    float r = 0.f, m = 0.f;
+    if (nr) {
+      row_sum<TPR>(s2, red + 1);
+      r = rsqrtf(s2[0] * inv_d + a.eps);
+      m = r * r * (s2[1] * inv_d);
     }
     // column sums, dx, dz and the sums of u y r_y
     float u[NV][8], su[NV], s3[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      const float ry = rsqrtf((GROUPS ? sy[i] : s1[0]) / (float)a.group + a.eps);
-      float yh[8], w[8], l[8], zz[8], d[8], v[8];
-      unpack8(y[i], yh);
-      weight8(a.w_post, GROUPS ? col % a.group : col, a.group, w);
-      weight8(a.lam, col, a.D, l);
-      if (zr) unpack8(z[i], zz);
-      if (gr) {
-        unpack8(gx[i], d);
-      } else {
+      float d[8], v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = 0.f;
-      }
-      float sg[8], sl[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        yh[j] *= ry;
-        sg[j] = zr ? sigmoid_f(zz[j]) : 1.f;
-        sl[j] = zr ? zz[j] * sg[j] : 1.f;
-      }
+      for (int j = 0; j < 8; ++j) d[j] = 0.f;
+      if (gr) unpack8(gx[i], d);
       if (nr) {
-        float wp[8], xv[8];
         unpack8(gn[i], v);
-        weight8(a.w_pre, col, a.D, wp);
-        if (xr) unpack8(x[i], xv);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float xo = (xr ? xv[j] : 0.f) + l[j] * (yh[j] * w[j] * sl[j]);
-          c_pre[i][j] += v[j] * (xo * r);
-          d[j] += r * (v[j] * wp[j] - xo * m);
+          c_pre[i][j] += v[j] * (xo[i][j] * r);
+          d[j] += r * (v[j] * wp[i][j] - xo[i][j] * m);
         }
       }
       su[i] = 0.f;
       float dz[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        c_lam[i][j] += d[j] * (yh[j] * w[j] * sl[j]);
-        const float dp = d[j] * l[j];
-        c_post[i][j] += dp * yh[j] * sl[j];
-        if (zr) dz[j] = dp * yh[j] * w[j] * sg[j] * (1.f + zz[j] * (1.f - sg[j]));
-        u[i][j] = dp * w[j] * sl[j];
-        su[i] += u[i][j] * yh[j];
+        const float ys = yh[i][j] * sl[i][j], dp = d[j] * lm[i][j], dw = dp * wq[i][j];
+        c_lam[i][j] += d[j] * (ys * wq[i][j]);
+        c_post[i][j] += dp * ys;
+        dz[j] = dw * yh[i][j] * ds[i][j];
+        u[i][j] = dw * sl[i][j];
+        su[i] += u[i][j] * yh[i][j];
       }
       s3[0] += su[i];
-      if (a.dX) store8(norm_row(a.dX, row, a.ldx, a), col, a.D, a.vec, d);
-      if (zr && a.dZ) store8(norm_row(a.dZ, row, a.ldz, a), col, a.D, a.vec, dz);
+      if (a.dX) store8<VEC>(at.in(a.dX, a.ldx, a.D), col, a.D, d);
+      if (zr && a.dZ) store8<VEC>(at.in(a.dZ, a.ldz, a.D), col, a.D, dz);
     }
     if (a.dY) {
       if constexpr (GROUPS) group_sum<TPR>(su, t, a.D, a.group, buf);
-      else row_sum<TPR>(s3, red);
+      else row_sum<TPR>(s3, red + 3);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + t) * 8;
-        const float ry = rsqrtf((GROUPS ? sy[i] : s1[0]) / (float)a.group + a.eps);
-        const float mu = (GROUPS ? su[i] : s3[0]) / (float)a.group;
+        const float mu = (GROUPS ? su[i] : s3[0]) * inv_group;
         float v[8];
-        unpack8(y[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ry * (u[i][j] - v[j] * ry * mu);
-        store8(norm_row(a.dY, row, a.ldy, a), col, a.D, a.vec, v);
+        for (int j = 0; j < 8; ++j) v[j] = ry[i] * (u[i][j] - yh[i][j] * mu);
+        store8<VEC>(at.in(a.dY, a.ldy, a.D), col, a.D, v);
       }
+    } else if (TPR > 32 && !GROUPS && !nr) {
+      __syncthreads();  // a row with one sum only: its buffer is read
     }
   }
 
@@ -415,10 +450,10 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm_bwd(const 
 }
 
 // Column sums over the blocks' partial sums in a fixed order; dw_post also over the row's groups.
-// Block: 32 columns x 8 slices of the blocks.
-__global__ void __launch_bounds__(256) k_norm_cols(const float* __restrict__ part, int blocks, int D, int group,
-                                                   float* dw_post, float* dlam, float* dw_pre) {
-  __shared__ float s[8][33];
+// Block: 32 columns x 32 slices of the blocks, four loads of a slice in flight.
+__global__ void __launch_bounds__(1024) k_norm_cols(const float* __restrict__ part, int blocks, int D, int group,
+                                                    float* dw_post, float* dlam, float* dw_pre) {
+  __shared__ float s[32][33];
   const int q = blockIdx.y, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   float* out = q == 0 ? dw_post : q == 1 ? dlam : dw_pre;
   const int n = q == 0 ? group : D;
@@ -427,14 +462,22 @@ __global__ void __launch_bounds__(256) k_norm_cols(const float* __restrict__ par
   pdl_wait();
   float v = 0.f;
   if (col < n)
-    for (int b = slice; b < blocks; b += 8)
-      for (int c = col; c < D; c += n) v += part[((int64_t)b * 3 + q) * D + c];
+    for (int c = col; c < D; c += n) {
+      const float* p = part + (int64_t)q * D + c;
+      const int64_t ld = 3 * (int64_t)D;
+      for (int b = slice; b < blocks; b += 128) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = b + 32 * k < blocks ? p[(b + 32 * k) * ld] : 0.f;
+        v += (x[0] + x[1]) + (x[2] + x[3]);
+      }
+    }
   s[slice][lane] = v;
   __syncthreads();
   if (slice == 0 && col < n) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][lane];
+    for (int i = 0; i < 32; ++i) t += s[i][lane];
     out[col] = t;
   }
 }

@@ -10,6 +10,7 @@ using namespace ttt;
 namespace {
 
 constexpr int kNormMaxD = 8192;
+constexpr int kNormSms = 148;
 
 // How a call's rows map to kernel rows: groups become rows of their own where nothing ties the columns of a
 // row together but w_post (no second norm, no residual scale or gradient over all columns).
@@ -18,13 +19,18 @@ struct NormShape {
   bool groups;
 };
 
-NormShape norm_shape(const ttt_norm_cfg& c, bool row_wide) {
+// Threads of a row and chunks of 8 columns per thread.  Forward: a warp to a row up to 1024 columns (no barriers),
+// but one chunk to a thread where the rows are too few to fill the card.  Backward: up to ten tensors' registers and
+// three column sums per chunk, so at most two chunks per thread.
+NormShape norm_shape(const ttt_norm_cfg& c, bool row_wide, bool back, int64_t T) {
   NormShape s{};
   s.split = !row_wide && c.group < c.D ? c.D / c.group : 1;
   s.D = c.D / s.split;
   s.groups = c.group < s.D;
   const int chunks = (s.D + 7) / 8;
-  s.tpr = chunks <= 128 ? 32 : chunks <= 512 ? 128 : 256;
+  if (back) s.tpr = chunks <= 64 ? 32 : chunks <= 128 ? 128 : chunks <= 512 ? 256 : 512;
+  else if (T * s.split <= 4 * kNormSms) s.tpr = chunks <= 32 ? 32 : chunks <= 128 ? 128 : chunks <= 256 ? 256 : 512;
+  else s.tpr = chunks <= 128 ? 32 : chunks <= 512 ? 128 : 256;
   s.nv = (chunks + s.tpr - 1) / s.tpr;
   return s;
 }
@@ -32,7 +38,7 @@ NormShape norm_shape(const ttt_norm_cfg& c, bool row_wide) {
 int64_t norm_blocks(const NormShape& s, int64_t T) {
   const int block = std::max(128, s.tpr), rpb = block / s.tpr;
   const int64_t rows = T * s.split;
-  return std::max<int64_t>(1, std::min<int64_t>((rows + rpb - 1) / rpb, (int64_t)sm_count() * (512 / block)));
+  return std::max<int64_t>(1, std::min<int64_t>((rows + rpb - 1) / rpb, (int64_t)kNormSms * (512 / block)));
 }
 
 bool norm_cfg_ok(const ttt_norm_cfg* c) {
@@ -47,39 +53,52 @@ bool vec_ok(const void* p, int64_t ld, ttt_dtype dt) {
 }
 bool elem_ok(const void* p, ttt_dtype dt) { return (reinterpret_cast<uintptr_t>(p) & (esize(dt) - 1)) == 0; }
 
-template <typename T, int TPR, int NV>
-int launch_norm(const NormArgs<T>& a, bool groups, bool back, int64_t blocks, cudaStream_t s) {
+template <typename T, int TPR, int NV, bool GROUPS, bool VEC>
+int launch_norm(const NormArgs<T>& a, bool back, int64_t blocks, cudaStream_t s) {
   constexpr int block = TPR > 128 ? TPR : 128;
   const int chunks = (a.D + 7) / 8, rpb = block / TPR;
-  size_t smem = groups ? (size_t)rpb * chunks * 4 : 0;
+  size_t smem = GROUPS ? (size_t)rpb * chunks * 4 : 0;
   if (back) {
-    if (rpb > 1) smem = std::max(smem, (size_t)a.D * 4);
-    if (groups) k_block_norm_bwd<T, TPR, NV, true><<<(unsigned)blocks, block, smem, s>>>(a);
-    else k_block_norm_bwd<T, TPR, NV, false><<<(unsigned)blocks, block, smem, s>>>(a);
+    if constexpr (NV <= 2) {
+      if (rpb > 1) smem = std::max(smem, (size_t)a.D * 4);
+      k_block_norm_bwd<T, TPR, NV, GROUPS, VEC><<<(unsigned)blocks, block, smem, s>>>(a);
+    }
   } else {
-    if (groups) k_block_norm<T, TPR, NV, true><<<(unsigned)blocks, block, smem, s>>>(a);
-    else k_block_norm<T, TPR, NV, false><<<(unsigned)blocks, block, smem, s>>>(a);
+    k_block_norm<T, TPR, NV, GROUPS, VEC><<<(unsigned)blocks, block, smem, s>>>(a);
   }
   TTT_LAUNCHED();
   return TTT_OK;
 }
 
-template <typename T, int TPR>
-int launch_norm_nv(const NormArgs<T>& a, const NormShape& sh, bool back, int64_t blocks, cudaStream_t s) {
-  switch (sh.nv) {
-    case 1: return launch_norm<T, TPR, 1>(a, sh.groups, back, blocks, s);
-    case 2: return launch_norm<T, TPR, 2>(a, sh.groups, back, blocks, s);
-    case 3: return launch_norm<T, TPR, 3>(a, sh.groups, back, blocks, s);
-    default: return launch_norm<T, TPR, 4>(a, sh.groups, back, blocks, s);
+template <typename T, int TPR, int NV>
+int launch_norm_any(const NormArgs<T>& a, const NormShape& sh, bool vec, bool back, int64_t blocks, cudaStream_t s) {
+  if (sh.groups) {
+    return vec ? launch_norm<T, TPR, NV, true, true>(a, back, blocks, s)
+               : launch_norm<T, TPR, NV, true, false>(a, back, blocks, s);
   }
+  return vec ? launch_norm<T, TPR, NV, false, true>(a, back, blocks, s)
+             : launch_norm<T, TPR, NV, false, false>(a, back, blocks, s);
 }
 
+// The shapes that norm_shape gives.
 template <typename T>
-int run_norm(NormArgs<T> a, const NormShape& sh, bool back, int64_t blocks, cudaStream_t s) {
-  switch (sh.tpr) {
-    case 32: return launch_norm_nv<T, 32>(a, sh, back, blocks, s);
-    case 128: return launch_norm_nv<T, 128>(a, sh, back, blocks, s);
-    default: return launch_norm_nv<T, 256>(a, sh, back, blocks, s);
+int run_norm(const NormArgs<T>& a, const NormShape& sh, bool vec, bool back, int64_t blocks, cudaStream_t s) {
+  switch (sh.tpr * 8 + sh.nv) {
+    case 32 * 8 + 1: return launch_norm_any<T, 32, 1>(a, sh, vec, back, blocks, s);
+    case 32 * 8 + 2: return launch_norm_any<T, 32, 2>(a, sh, vec, back, blocks, s);
+    case 32 * 8 + 3: return launch_norm_any<T, 32, 3>(a, sh, vec, back, blocks, s);
+    case 32 * 8 + 4: return launch_norm_any<T, 32, 4>(a, sh, vec, back, blocks, s);
+    case 128 * 8 + 1: return launch_norm_any<T, 128, 1>(a, sh, vec, back, blocks, s);
+    case 128 * 8 + 2: return launch_norm_any<T, 128, 2>(a, sh, vec, back, blocks, s);
+    case 128 * 8 + 3: return launch_norm_any<T, 128, 3>(a, sh, vec, back, blocks, s);
+    case 128 * 8 + 4: return launch_norm_any<T, 128, 4>(a, sh, vec, back, blocks, s);
+    case 256 * 8 + 1: return launch_norm_any<T, 256, 1>(a, sh, vec, back, blocks, s);
+    case 256 * 8 + 2: return launch_norm_any<T, 256, 2>(a, sh, vec, back, blocks, s);
+    case 256 * 8 + 3: return launch_norm_any<T, 256, 3>(a, sh, vec, back, blocks, s);
+    case 256 * 8 + 4: return launch_norm_any<T, 256, 4>(a, sh, vec, back, blocks, s);
+    case 512 * 8 + 1: return launch_norm_any<T, 512, 1>(a, sh, vec, back, blocks, s);
+    case 512 * 8 + 2: return launch_norm_any<T, 512, 2>(a, sh, vec, back, blocks, s);
+    default: return TTT_ERR_UNSUPPORTED;
   }
 }
 
@@ -110,12 +129,12 @@ int check_norm(const NormCall& c, const ttt_norm_cfg& cfg, ttt_dtype dt, int64_t
   }
   for (const void* p : {(const void*)c.w_post, (const void*)c.lam, (const void*)c.w_pre})
     if (!elem_ok(p, TTT_FP32)) return TTT_ERR_ALIGN;
+    else if (!aligned16(p)) vec = 0;
   return TTT_OK;
 }
 
 template <typename T>
-NormArgs<T> norm_args(const NormCall& c, const ttt_norm_cfg& cfg, const NormShape& sh, const int64_t (&ld)[5], int vec,
-                      int64_t rows) {
+NormArgs<T> norm_args(const NormCall& c, const ttt_norm_cfg& cfg, const NormShape& sh, const int64_t (&ld)[5], int64_t rows) {
   NormArgs<T> a{};
   a.X = (const T*)c.X;
   a.Y = (const T*)c.Y;
@@ -140,7 +159,6 @@ NormArgs<T> norm_args(const NormCall& c, const ttt_norm_cfg& cfg, const NormShap
   a.D = sh.D;
   a.group = cfg.group;
   a.eps = cfg.eps;
-  a.vec = vec;
   return a;
 }
 
@@ -160,19 +178,19 @@ int ttt_block_norm(const void* X, const void* Y, const void* Z, const float* w_p
   if (T == 0) return TTT_OK;
   if (!Y || (!Xout && !N)) return TTT_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
-  const NormShape sh = norm_shape(*cfg, N || res_scale);
+  const NormShape sh = norm_shape(*cfg, N || res_scale, false, T);
   const int block = std::max(128, sh.tpr), rpb = block / sh.tpr;
-  const int64_t blocks = std::min<int64_t>((T * sh.split + rpb - 1) / rpb, (int64_t)sm_count() * (2048 / block));
+  const int64_t blocks = std::min<int64_t>((T * sh.split + rpb - 1) / rpb, (int64_t)kNormSms * (2048 / block));
   ProfScope ps(TTT_PROF_BNORM, s);
-  if (dtype == TTT_FP32) return run_norm(norm_args<float>(c, *cfg, sh, ld, vec, T), sh, false, blocks, s);
-  return run_norm(norm_args<__nv_bfloat16>(c, *cfg, sh, ld, vec, T), sh, false, blocks, s);
+  if (dtype == TTT_FP32) return run_norm(norm_args<float>(c, *cfg, sh, ld, T), sh, vec != 0, false, blocks, s);
+  return run_norm(norm_args<__nv_bfloat16>(c, *cfg, sh, ld, T), sh, vec != 0, false, blocks, s);
 }
 
 size_t ttt_block_norm_workspace_bytes(const ttt_norm_cfg* cfg, int64_t T) {
   if (!norm_cfg_ok(cfg) || !norm_cfg_supported(*cfg) || T < 0) return 0;
   size_t most = 0;
   for (bool wide : {false, true}) {
-    const NormShape sh = norm_shape(*cfg, wide);
+    const NormShape sh = norm_shape(*cfg, wide, true, T);
     most = std::max(most, (size_t)norm_blocks(sh, std::max<int64_t>(T, 1)) * 3 * sh.D * 4);
   }
   return up256(most);
@@ -195,20 +213,20 @@ int ttt_block_norm_backward(const void* X, const void* Y, const void* Z, const f
   if (T > 0 && (!Y || (!dXout && !dN))) return TTT_ERR_INVALID;
   if ((dZ && !Z && T > 0) || (dX && !X && T > 0)) return TTT_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
-  const NormShape sh = norm_shape(*cfg, dN || res_scale || dres_scale || dw_pre);
+  const NormShape sh = norm_shape(*cfg, dN || res_scale || dres_scale || dw_pre, true, T);
   ProfScope ps(TTT_PROF_BNORM, s);
   int64_t blocks = 0;
   if (T > 0) {
     blocks = norm_blocks(sh, T);
     auto go = [&](auto a) {
       a.part = cols ? (float*)ws : nullptr;
-      return run_norm(a, sh, true, blocks, s);
+      return run_norm(a, sh, vec != 0, true, blocks, s);
     };
-    TTT_TRY(dtype == TTT_FP32 ? go(norm_args<float>(c, *cfg, sh, ld, vec, T))
-                              : go(norm_args<__nv_bfloat16>(c, *cfg, sh, ld, vec, T)));
+    TTT_TRY(dtype == TTT_FP32 ? go(norm_args<float>(c, *cfg, sh, ld, T))
+                              : go(norm_args<__nv_bfloat16>(c, *cfg, sh, ld, T)));
   }
   if (!cols) return TTT_OK;
-  TTT_TRY(launch_pdl(k_norm_cols, dim3((sh.D + 31) / 32, 3), dim3(256), 0, s, (const float*)ws, (int)blocks, sh.D,
+  TTT_TRY(launch_pdl(k_norm_cols, dim3((sh.D + 31) / 32, 3), dim3(1024), 0, s, (const float*)ws, (int)blocks, sh.D,
                      cfg->group, dw_post, dres_scale, dw_pre));
   TTT_LAUNCHED();
   return TTT_OK;
