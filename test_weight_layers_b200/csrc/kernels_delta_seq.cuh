@@ -53,19 +53,30 @@ struct SeqArgs {
   int n_slots, rows;  // decoding step
 };
 
-// A warp holds ROWS rows of S (value channels), lane l the columns VEC (32 i + l) + 0..VEC-1
-// of each; a token costs one pass over the registers and one warp reduction of 2 ROWS + 3 sums.
-// Bound by the state's bytes in a decoding step (read and written once), by the
-// reduction's latency over a sequence.
-template <typename T, int VEC, int NV, int ROWS>
+// A token as a warp needs it: lane l the columns VEC (32 i + l) + 0..VEC-1 of k and q, lane r < ROWS the value of
+// row r, and the scalars that do not depend on the state.
+template <int E>
+struct Token {
+  float k[E], q[E], v, beta, g;  // as loaded
+  float fk, fq, kq, al;          // norms' factors, k . q, exp(g)
+};
+
+// A warp holds ROWS rows of S (value channels), lane l the columns VEC (32 i + l) + 0..VEC-1 of each; a token
+// costs one pass over the registers and one warp reduction: of S k and S q per row, and of k.k, q.q, k.q.
+//   Decoding step (SEQ = false): bound by the state's bytes, read and written once: STEP_B for 235 rows of 16
+// heads of 128 x 128.
+//   Sequences (SEQ): bound by the chain reduction -> update; the next token's norms are reduced beside this
+// token's products and the one after it is being loaded: SEQ_T a token (two rows to a warp).
+template <typename T, int VEC, int NV, int ROWS, bool SEQ>
 __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
   __shared__ int next_row;
+  constexpr int E = NV * VEC;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int h = blockIdx.y, hq = h / (a.hv / a.hk);
   const int r0 = (blockIdx.z * 4 + warp) * ROWS;
   int64_t tok = blockIdx.x, state = blockIdx.x;
   int len = 1;
-  if (a.seqs) {
+  if constexpr (SEQ) {
     pdl_wait();
     const DrSeq sq = a.seqs[blockIdx.x];
     if (sq.len < 0) return;
@@ -76,7 +87,7 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
     state = a.slots[blockIdx.x];
     if (state < 0 || state >= a.n_slots) return;
   }
-  float s[ROWS][NV * VEC];
+  float s[ROWS][E];
   const int64_t srow = (state * a.hv + h) * a.dv;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r)
@@ -90,82 +101,151 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
         for (int j = 0; j < VEC; ++j) s[r][i * VEC + j] = 0.f;
       }
     }
-  // rows of one slot run in row order in the block of the first of them
-  auto next_same = [&](int after) {
-    if (threadIdx.x == 0) next_row = INT32_MAX;
-    __syncthreads();
-    for (int b = after + 1 + (int)threadIdx.x; b < a.rows; b += 128)
-      if (a.slots[b] == (int)state) atomicMin(&next_row, b);
-    __syncthreads();
-    const int n = next_row;
-    __syncthreads();
-    return n;
-  };
-  if (!a.seqs && a.slots) {
-    bool earlier = false;
-    for (int b = threadIdx.x; b < (int)blockIdx.x; b += 128) earlier |= a.slots[b] == (int)state;
-    if (__syncthreads_or(earlier)) return;
-  }
-
-#pragma unroll 1
-  for (int n = 0; n < len;) {
-    float k[NV * VEC], q[NV * VEC];
+  auto load = [&](Token<E>& x, int64_t tok) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = VEC * (32 * i + lane);
       if (col < a.dk) {
-        load_vec<VEC>(a.K + tok * a.ldk + (int64_t)hq * a.dk + col, &k[i * VEC]);
-        load_vec<VEC>(a.Q + tok * a.ldq + (int64_t)hq * a.dk + col, &q[i * VEC]);
+        load_vec<VEC>(a.K + tok * a.ldk + (int64_t)hq * a.dk + col, &x.k[i * VEC]);
+        load_vec<VEC>(a.Q + tok * a.ldq + (int64_t)hq * a.dk + col, &x.q[i * VEC]);
       } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) k[i * VEC + j] = q[i * VEC + j] = 0.f;
+        for (int j = 0; j < VEC; ++j) x.k[i * VEC + j] = x.q[i * VEC + j] = 0.f;
       }
     }
-    const float be = a.beta[tok * a.hv + h], al = expf(a.g[tok * a.hv + h]);
-    float v = 0.f;
-    if (lane < ROWS && r0 + lane < a.dv) v = load_one(a.V + tok * a.ldv + (int64_t)h * a.dv + r0 + lane);
-    float p[2 * ROWS + 3];
+    x.beta = a.beta[tok * a.hv + h];
+    x.g = a.g[tok * a.hv + h];
+    x.v = 0.f;
+    if (SEQ && lane < ROWS && r0 + lane < a.dv) x.v = load_one(a.V + tok * a.ldv + (int64_t)h * a.dv + r0 + lane);
+  };
+  auto dots = [&](const Token<E>& x, float* p) {  // k.k, q.q, k.q of this lane's columns
+    p[0] = p[1] = p[2] = 0.f;
 #pragma unroll
-    for (int j = 0; j < 2 * ROWS + 3; ++j) p[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) {
-      p[2 * ROWS] += k[i] * k[i];
-      p[2 * ROWS + 1] += q[i] * q[i];
-      p[2 * ROWS + 2] += k[i] * q[i];
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        p[2 * r] += s[r][i] * k[i];
-        p[2 * r + 1] += s[r][i] * q[i];
-      }
+    for (int i = 0; i < E; ++i) {
+      p[0] += x.k[i] * x.k[i];
+      p[1] += x.q[i] * x.q[i];
+      p[2] += x.k[i] * x.q[i];
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < 2 * ROWS + 3; ++j) p[j] += __shfl_xor_sync(0xffffffffu, p[j], o);
-    float fk = 1.f, fq = 1.f;
+  };
+  auto factors = [&](Token<E>& x, const float* p) {
+    x.fk = x.fq = 1.f;
     if (a.l2norm) {
-      fk = 1.f / fmaxf(sqrtf(p[2 * ROWS]), 1e-12f);
-      fq = 1.f / fmaxf(sqrtf(p[2 * ROWS + 1]), 1e-12f);
+      x.fk = 1.f / fmaxf(sqrtf(p[0]), 1e-12f);
+      x.fq = 1.f / fmaxf(sqrtf(p[1]), 1e-12f);
     }
-    fq *= a.scale;
+    x.fq *= a.scale;
+    x.kq = p[2];
+    x.al = expf(x.g);
+  };
+  auto products = [&](const Token<E>& x, float* p) {  // S k and S q of this lane's columns
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      p[2 * r] = p[2 * r + 1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        p[2 * r] += s[r][i] * x.k[i];
+        p[2 * r + 1] += s[r][i] * x.q[i];
+      }
+    }
+  };
+  auto update = [&](const Token<E>& x, const float* p, int64_t tok) {
     float out = 0.f;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const float u = be * (__shfl_sync(0xffffffffu, v, r) - al * (p[2 * r] * fk));
-      const float uk = u * fk;
-      const float o = fq * (al * p[2 * r + 1] + uk * p[2 * ROWS + 2]);
+      const float u = x.beta * (__shfl_sync(0xffffffffu, x.v, r) - x.al * (p[2 * r] * x.fk));
+      const float uk = u * x.fk;
+      const float o = x.fq * (x.al * p[2 * r + 1] + uk * x.kq);
       if (lane == r) out = o;
 #pragma unroll
-      for (int i = 0; i < NV * VEC; ++i) s[r][i] = al * s[r][i] + uk * k[i];
+      for (int i = 0; i < E; ++i) s[r][i] = x.al * s[r][i] + uk * x.k[i];
     }
     if (lane < ROWS && r0 + lane < a.dv) store_one(a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + lane, out);
-    if (a.seqs) {
-      ++n;
-      ++tok;
-    } else {
-      const int nx = a.slots ? next_same((int)tok) : INT32_MAX;
-      if (nx == INT32_MAX) break;
-      tok = nx;
+  };
+  constexpr int NP = 2 * ROWS + 3;
+  auto reduce = [](float (&p)[NP], int from) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if (j >= from) p[j] += __shfl_xor_sync(0xffffffffu, p[j], o);
+  };
+  float p[NP];
+  if constexpr (SEQ) {
+    Token<E> x, y;
+    if (len > 0) {
+      load(x, tok);
+      dots(x, p + 2 * ROWS);
+      reduce(p, 2 * ROWS);
+      factors(x, p + 2 * ROWS);
+    }
+    if (len > 0) load(y, tok + min(1, len - 1));
+#pragma unroll 3
+    for (int n = 0; n < len; ++n) {  // (unrolled so that the three tokens change names, not registers)
+      Token<E> z;
+      load(z, tok + min(n + 2, len - 1));  // (past the last token: that one again, unused)
+      products(x, p);
+      dots(y, p + 2 * ROWS);
+      reduce(p, 0);
+      update(x, p, tok + n);
+      factors(y, p + 2 * ROWS);
+      x = y;
+      y = z;
+    }
+  } else {
+    // rows of one slot run in row order in the block of the first of them
+    if (a.slots) {
+      bool earlier = false;
+      for (int b = threadIdx.x; b < (int)blockIdx.x; b += 128) earlier |= a.slots[b] == (int)state;
+      if (__syncthreads_or(earlier)) return;
+    }
+    // The 2 ROWS sums over the warp with the values halved at each step: the lanes whose bit is set keep the upper
+    // half and send the lower, so that 16 sums take 16 shuffles instead of 80.  Then lane l has sum l / LPI, and the
+    // 2 LPI lanes of a row do its scalar part.
+    constexpr int M = 2 * ROWS, LPI = 32 / M;
+    const int mine = lane / (2 * LPI);
+    for (;;) {
+      Token<E> x;
+      load(x, tok);
+      const float v = r0 + mine < a.dv ? load_one(a.V + tok * a.ldv + (int64_t)h * a.dv + r0 + mine) : 0.f;
+      products(x, p);
+      dots(x, p + M);
+#pragma unroll
+      for (int half = ROWS; half; half >>= 1) {
+        const int o = half * LPI;
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const float send = upper ? p[i] : p[i + half], keep = upper ? p[i + half] : p[i];
+          p[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+#pragma unroll
+      for (int o = LPI / 2; o; o >>= 1) p[0] += __shfl_xor_sync(0xffffffffu, p[0], o);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) p[M + i] += __shfl_xor_sync(0xffffffffu, p[M + i], o);
+      factors(x, p + M);
+      const float other = __shfl_xor_sync(0xffffffffu, p[0], LPI);
+      const float sk = lane & LPI ? other : p[0], sq = lane & LPI ? p[0] : other;
+      const float uk = x.beta * (v - x.al * (sk * x.fk)) * x.fk;
+      if (lane % (2 * LPI) == 0 && r0 + mine < a.dv)
+        store_one(a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + mine, x.fq * (x.al * sq + uk * x.kq));
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const float ur = __shfl_sync(0xffffffffu, uk, r * 2 * LPI);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[r][i] = x.al * s[r][i] + ur * x.k[i];
+      }
+      if (!a.slots) break;
+      if (threadIdx.x == 0) next_row = INT32_MAX;
+      __syncthreads();
+      for (int b = (int)tok + 1 + (int)threadIdx.x; b < a.rows; b += 128)
+        if (a.slots[b] == (int)state) atomicMin(&next_row, b);
+      __syncthreads();
+      tok = next_row;
+      __syncthreads();
+      if (tok == INT32_MAX) break;
     }
   }
   if (a.S) {

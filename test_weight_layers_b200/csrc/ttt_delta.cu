@@ -132,8 +132,16 @@ int delta_check(const void* Q, const void* K, const void* V, const float* g, con
   return aligned4(g) && aligned4(beta) ? TTT_OK : TTT_ERR_ALIGN;
 }
 
-int smem_opt_in(const void* fn, int bytes) {
-  TTT_CHECK(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+// Opts kernel K in to all the shared memory a block can have, once per device.
+template <auto K>
+int smem_opt_in() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  TTT_CHECK(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return TTT_OK;
+  TTT_CHECK(cudaFuncSetAttribute((const void*)K, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  done.fetch_or(bit, std::memory_order_relaxed);
   return TTT_OK;
 }
 
@@ -155,12 +163,12 @@ constexpr int pass_warps(bool back) {
 int pass_warps_for(int most, int dv) { return std::min(most, (dv + 15) / 16); }
 
 // Launches a pass over the chunks of each segment.  `rows`: rows of 16 that share a block of `warps`, per head.
-template <typename Args>
-int launch_pass(void (*k)(Args), const Args& a, int segs, int64_t blocks_per_head, int warps, int smem,
+template <auto K, typename Args>
+int launch_pass(const Args& a, int segs, int64_t blocks_per_head, int warps, int smem,
                 cudaStream_t s) {
   if (blocks_per_head * a.hv * segs > INT32_MAX) return TTT_ERR_UNSUPPORTED;
-  TTT_TRY(smem_opt_in((const void*)k, smem));
-  TTT_TRY(launch_pdl(k, dim3((unsigned)(blocks_per_head * a.hv * segs)), dim3(warps * 32), smem, s, a));
+  TTT_TRY(smem_opt_in<K>());
+  TTT_TRY(launch_pdl(K, dim3((unsigned)(blocks_per_head * a.hv * segs)), dim3(warps * 32), smem, s, a));
   TTT_LAUNCHED();
   return TTT_OK;
 }
@@ -170,7 +178,7 @@ int64_t blocks_of(int rows, int warps) { return (rows + 16 * warps - 1) / (16 * 
 template <int DK, bool REVERSE>
 int launch_join(const StateArgs& sa, float* seg_s, const DeltaWs& w, cudaStream_t s) {
   JoinArgs ja{sa.seqs, sa.hv, sa.dk, sa.dv, seg_s, w.seg_n, w.phi, w.phi_scale, sa.guard};
-  return launch_pass(k_delta_join<DK, REVERSE>, ja, w.max_segs, (sa.dv + 63) / 64, 4, join_smem<DK>(), s);
+  return launch_pass<k_delta_join<DK, REVERSE>>(ja, w.max_segs, (sa.dv + 63) / 64, 4, join_smem<DK>(), s);
 }
 
 // The states at the segments' starts (nothing to do for uncut sequences).
@@ -178,14 +186,14 @@ template <int DK>
 int run_scan(const StateArgs& sa, const DeltaWs& w, cudaStream_t s) {
   if (!w.seg_chunks) return TTT_OK;
   const int warps = pass_warps<DK>(false);
-  TTT_TRY(launch_pass(k_delta_state<DK, PASS_SCAN>, sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
-                      warps, state_smem<DK, false>(warps), s));
+  TTT_TRY((launch_pass<k_delta_state<DK, PASS_SCAN>>(sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
+                      warps, state_smem<DK, false>(warps), s)));
   return launch_join<DK, false>(sa, w.seg_s, w, s);
 }
 
 template <int DK, bool BACK>
 int launch_prep(const PrepArgs& pa, const DeltaWs& w, cudaStream_t s) {
-  TTT_TRY(smem_opt_in((const void*)k_delta_prep<DK, BACK>, prep_smem<DK>()));
+  TTT_TRY((smem_opt_in<k_delta_prep<DK, BACK>>()));
   TTT_TRY(launch_pdl(k_delta_prep<DK, BACK>, dim3((unsigned)w.max_chunks, pa.hk), dim3(128), prep_smem<DK>(), s, pa));
   TTT_LAUNCHED();
   return TTT_OK;
@@ -196,7 +204,7 @@ int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream
   TTT_TRY((launch_prep<DK, false>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
   const int warps = pass_warps_for(pass_warps<DK>(false), sa.dv);
-  return launch_pass(k_delta_state<DK, PASS_OUT>, sa, w.max_segs, blocks_of(sa.dv, warps), warps,
+  return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps), warps,
                      state_smem<DK, false>(warps), s);
 }
 
@@ -206,29 +214,39 @@ int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra
   TTT_TRY(run_scan<DK>(sa, w, s));
   const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps);
   const int64_t blocks = blocks_of(sa.dv, warps);
-  TTT_TRY(launch_pass(k_delta_state<DK, PASS_BACK>, sa, w.max_segs, blocks, warps, smem, s));
+  TTT_TRY((launch_pass<k_delta_state<DK, PASS_BACK>>(sa, w.max_segs, blocks, warps, smem, s)));
   if (w.seg_chunks) {  // the transitions are the state pass's, transposed
-    TTT_TRY(launch_pass(k_delta_reverse<DK, true>, ra, w.max_segs, blocks, warps, smem, s));
+    TTT_TRY((launch_pass<k_delta_reverse<DK, true>>(ra, w.max_segs, blocks, warps, smem, s)));
     TTT_TRY((launch_join<DK, true>(sa, w.seg_s, w, s)));
   }
-  TTT_TRY(launch_pass(k_delta_reverse<DK, false>, ra, w.max_segs, blocks, warps, smem, s));
-  TTT_TRY(smem_opt_in((const void*)k_delta_grad<DK>, grad_smem<DK>()));
+  TTT_TRY((launch_pass<k_delta_reverse<DK, false>>(ra, w.max_segs, blocks, warps, smem, s)));
+  TTT_TRY(smem_opt_in<k_delta_grad<DK>>());
   TTT_TRY(launch_pdl(k_delta_grad<DK>, dim3((unsigned)w.max_chunks, ga.hk), dim3(256), grad_smem<DK>(), s, ga));
   TTT_LAUNCHED();
   return TTT_OK;
 }
 
-template <typename T, int VEC, int NV>
-int launch_tokens(const SeqArgs<T>& a, unsigned blocks, cudaStream_t s) {
-  constexpr int ROWS = NV * VEC > 4 ? 4 : 8;
+template <typename T, int VEC, int NV, int ROWS, bool SEQ>
+int launch_tokens_rows(const SeqArgs<T>& a, unsigned blocks, cudaStream_t s) {
   const dim3 grid(blocks, a.hv, (a.dv + 4 * ROWS - 1) / (4 * ROWS));
-  if (a.seqs) {
-    TTT_TRY(launch_pdl(k_delta_tokens<T, VEC, NV, ROWS>, grid, dim3(128), 0, s, a));
+  if constexpr (SEQ) {
+    TTT_TRY(launch_pdl(k_delta_tokens<T, VEC, NV, ROWS, SEQ>, grid, dim3(128), 0, s, a));
   } else {
-    k_delta_tokens<T, VEC, NV, ROWS><<<grid, 128, 0, s>>>(a);
+    k_delta_tokens<T, VEC, NV, ROWS, SEQ><<<grid, 128, 0, s>>>(a);
   }
   TTT_LAUNCHED();
   return TTT_OK;
+}
+
+// Rows of S per warp: many where the state's bytes count (a decoding step that fills the card: loads of 4 to 8 rows
+// in flight), two where the latency of the reduction does (sequences, a few rows).
+template <typename T, int VEC, int NV>
+int launch_tokens(const SeqArgs<T>& a, unsigned blocks, cudaStream_t s) {
+  constexpr int MANY = NV * VEC > 4 ? 4 : 8;
+  if constexpr (std::is_same_v<T, float>)
+    if (a.seqs) return launch_tokens_rows<T, VEC, NV, 2, true>(a, blocks, s);
+  if ((int64_t)blocks * a.hv * a.dv < 148 * 64) return launch_tokens_rows<T, VEC, NV, 2, false>(a, blocks, s);
+  return launch_tokens_rows<T, VEC, NV, MANY, false>(a, blocks, s);
 }
 
 template <typename T>

@@ -269,26 +269,31 @@ def ttt_layer_host(W: Weights, hQ, hK, hV, hEta, hO, T, chunk, order, steps, ns:
         _stream(stream)))
 
 
-def _same_device(*tensors):
-    """All given tensors on the current CUDA device, whose stream the call is queued on."""
+def _queue(stream, *tensors):
+    """The stream to queue on, after checking that all given tensors are on the current CUDA device."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(name, t, rows, width, ld, dtype):
     """A token matrix of at least `rows` rows of `width` columns, stored with row stride ld (0: width)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{rows}][{width}] with unit column stride, got {tuple(t.shape)}")
-    if rows > 1 and t.stride(0) != (ld or width):
-        raise ValueError(f"{name} has row stride {t.stride(0)}, the call says {ld or width}")
+    size, step = t.shape, t.stride()
+    if (t.dtype is dtype and len(size) == 2 and size[0] >= rows and size[1] >= width and (step[1] == 1 or width == 1)
+            and (step[0] == (ld or width) or rows < 2)):
+        return
+    raise ValueError(f"{name} must be {dtype} [{rows}][{width}] with strides ({ld or width}, 1), got {t.dtype} "
+                     f"{list(size)} with strides {step}")
 
 
 def _dense(name, t, shape, dtype=torch.float32):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
@@ -328,20 +333,20 @@ def ttt_delta_chunked(Q, K, V, g, beta, S0, S, O, T, dm: DeltaDims, io: IOCfg, w
                       scale=1.0, stream=None):
     """The gated delta rule over n_seq packed sequences: O, and the states S after them (S0 before; either may be
     None).  cu_seqlens: int32 CUDA tensor [n_seq + 1], None for sequences of equal length."""
-    _same_device(Q, K, V, g, beta, S0, S, O, cu_seqlens, ws)
+    queue = _queue(stream, Q, K, V, g, beta, S0, S, O, cu_seqlens, ws)
     _delta_tokens(Q, K, V, g, beta, T, dm, io)
     _rows("O", O, T, dm.heads_v * dm.dv, io.ld_o, K.dtype)
     _delta_states(dm, n_seq, S0=S0, S=S)
     _offsets(cu_seqlens, n_seq)
     _check("ttt_delta_chunked", lib().ttt_delta_chunked(
-        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S0), _ptr(S), _ptr(O), _ptr(cu_seqlens), n_seq, T, scale,
-        dm, ctypes.byref(io), dtype_code(K.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+        _at(Q), _at(K), _at(V), _at(g), _at(beta), _at(S0), _at(S), _at(O), _at(cu_seqlens), n_seq, T, scale,
+        dm, ctypes.byref(io), dtype_code(K.dtype), _at(ws), ws.numel(), queue))
 
 
 def ttt_delta_chunked_backward(Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbeta, dS0, T, dm: DeltaDims, io: IOCfg,
                                ws, cu_seqlens=None, n_seq=1, scale=1.0, stream=None):
     """The gradient of ttt_delta_chunked from dO and dS (None: zeros); S0, dS0 may be None."""
-    _same_device(Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbeta, dS0, cu_seqlens, ws)
+    queue = _queue(stream, Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbeta, dS0, cu_seqlens, ws)
     _delta_tokens(Q, K, V, g, beta, T, dm, io)
     _delta_tokens(dQ, dK, dV, dg, dbeta, T, dm, io)
     _rows("dO", dO, T, dm.heads_v * dm.dv, io.ld_o, K.dtype)
@@ -350,23 +355,23 @@ def ttt_delta_chunked_backward(Q, K, V, g, beta, S0, dO, dS, dQ, dK, dV, dg, dbe
     _delta_states(dm, n_seq, S0=S0, dS=dS, dS0=dS0)
     _offsets(cu_seqlens, n_seq)
     _check("ttt_delta_chunked_backward", lib().ttt_delta_chunked_backward(
-        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S0), _ptr(dO), _ptr(dS), _ptr(dQ), _ptr(dK), _ptr(dV),
-        _ptr(dg), _ptr(dbeta), _ptr(dS0), _ptr(cu_seqlens), n_seq, T, scale, dm, ctypes.byref(io),
-        dtype_code(K.dtype), _ptr(ws), ws.numel(), _stream(stream)))
+        _at(Q), _at(K), _at(V), _at(g), _at(beta), _at(S0), _at(dO), _at(dS), _at(dQ), _at(dK), _at(dV),
+        _at(dg), _at(dbeta), _at(dS0), _at(cu_seqlens), n_seq, T, scale, dm, ctypes.byref(io),
+        dtype_code(K.dtype), _at(ws), ws.numel(), queue))
 
 
 def ttt_delta_step(Q, K, V, g, beta, S, O, B, dm: DeltaDims, io: IOCfg, slots=None, scale=1.0, stream=None):
     """One token for each of B sequences; S [n_slots][heads_v][dv][dk] is updated in place.  slots: int32 CUDA tensor
     [B], out-of-range entries marking padding rows; None: row b has slot b."""
-    _same_device(Q, K, V, g, beta, S, O, slots)
+    queue = _queue(stream, Q, K, V, g, beta, S, O, slots)
     _delta_tokens(Q, K, V, g, beta, B, dm, io)
     _rows("O", O, B, dm.heads_v * dm.dv, io.ld_o, K.dtype)
     _delta_states(dm, S.shape[0], S=S)
     if slots is not None:
         _dense("slots", slots, (B,), torch.int32)
     _check("ttt_delta_step", lib().ttt_delta_step(
-        _ptr(Q), _ptr(K), _ptr(V), _ptr(g), _ptr(beta), _ptr(S), S.shape[0], _ptr(slots), _ptr(O), B, scale, dm,
-        ctypes.byref(io), dtype_code(K.dtype), _stream(stream)))
+        _at(Q), _at(K), _at(V), _at(g), _at(beta), _at(S), S.shape[0], _at(slots), _at(O), B, scale, dm,
+        ctypes.byref(io), dtype_code(K.dtype), queue))
 
 
 def norm_cfg(D: int, group: int = 0, eps: float = 1e-6, ld_x=0, ld_y=0, ld_z=0, ld_xout=0, ld_n=0) -> NormCfg:
@@ -395,28 +400,28 @@ def ttt_block_norm(Y, Xout, T, cfg: NormCfg, X=None, Z=None, w_post=None, res_sc
                    stream=None):
     """Xout = X + res_scale * RMSNorm(Y) * w_post * SiLU(Z) and N = RMSNorm(Xout) * w_pre per row (either output may
     be None)."""
-    _same_device(Y, Xout, X, Z, w_post, res_scale, w_pre, N)
+    queue = _queue(stream, Y, Xout, X, Z, w_post, res_scale, w_pre, N)
     _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
                                   ("Xout", Xout, cfg.ld_xout), ("N", N, cfg.ld_n)),
                 (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D)))
     _check("ttt_block_norm", lib().ttt_block_norm(
-        _ptr(X), _ptr(Y), _ptr(Z), _ptr(w_post), _ptr(res_scale), _ptr(w_pre), _ptr(Xout), _ptr(N), T,
-        ctypes.byref(cfg), dtype_code(Y.dtype), _stream(stream)))
+        _at(X), _at(Y), _at(Z), _at(w_post), _at(res_scale), _at(w_pre), _at(Xout), _at(N), T,
+        ctypes.byref(cfg), dtype_code(Y.dtype), queue))
 
 
 def ttt_block_norm_backward(Y, dXout, dY, T, cfg: NormCfg, ws, X=None, Z=None, w_post=None, res_scale=None, w_pre=None,
                             dN=None, dX=None, dZ=None, dw_post=None, dres_scale=None, dw_pre=None, stream=None):
     """The gradient of ttt_block_norm from dXout and dN (None: zero); outputs that are None are not written."""
-    _same_device(Y, dXout, dY, ws, X, Z, w_post, res_scale, w_pre, dN, dX, dZ, dw_post, dres_scale, dw_pre)
+    queue = _queue(stream, Y, dXout, dY, ws, X, Z, w_post, res_scale, w_pre, dN, dX, dZ, dw_post, dres_scale, dw_pre)
     _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
                                   ("dXout", dXout, cfg.ld_xout), ("dN", dN, cfg.ld_n), ("dX", dX, cfg.ld_x),
                                   ("dY", dY, cfg.ld_y), ("dZ", dZ, cfg.ld_z)),
                 (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D),
                  ("dw_post", dw_post, cfg.group), ("dres_scale", dres_scale, cfg.D), ("dw_pre", dw_pre, cfg.D)))
     _check("ttt_block_norm_backward", lib().ttt_block_norm_backward(
-        _ptr(X), _ptr(Y), _ptr(Z), _ptr(w_post), _ptr(res_scale), _ptr(w_pre), _ptr(dXout), _ptr(dN), _ptr(dX),
-        _ptr(dY), _ptr(dZ), _ptr(dw_post), _ptr(dres_scale), _ptr(dw_pre), T, ctypes.byref(cfg), dtype_code(Y.dtype),
-        _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+        _at(X), _at(Y), _at(Z), _at(w_post), _at(res_scale), _at(w_pre), _at(dXout), _at(dN), _at(dX),
+        _at(dY), _at(dZ), _at(dw_post), _at(dres_scale), _at(dw_pre), T, ctypes.byref(cfg), dtype_code(Y.dtype),
+        _at(ws), 0 if ws is None else ws.numel(), queue))
 
 
 def ttt_selftest_wait_timeout(ws, timeout_us: int, stream=None):
