@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
   auto factors = [&](Token<E>& x, const float* p) {
     x.fk = x.fq = 1.f;
     if (a.l2norm) {
-      x.fk = 1.f / fmaxf(sqrtf(p[0]), 1e-12f);
-      x.fq = 1.f / fmaxf(sqrtf(p[1]), 1e-12f);
+      x.fk = fminf(rsqrtf(p[0]), 1e12f);  // 1 / max(||k||, 1e-12)
+      x.fq = fminf(rsqrtf(p[1]), 1e12f);
     }
     x.fq *= a.scale;
     x.kq = p[2];
@@ -148,45 +148,83 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
       }
     }
   };
-  auto update = [&](const Token<E>& x, const float* p, int64_t tok) {
-    float out = 0.f;
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const float u = x.beta * (__shfl_sync(0xffffffffu, x.v, r) - x.al * (p[2 * r] * x.fk));
-      const float uk = u * x.fk;
-      const float o = x.fq * (x.al * p[2 * r + 1] + uk * x.kq);
-      if (lane == r) out = o;
-#pragma unroll
-      for (int i = 0; i < E; ++i) s[r][i] = x.al * s[r][i] + uk * x.k[i];
-    }
-    if (lane < ROWS && r0 + lane < a.dv) store_one(a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + lane, out);
-  };
   constexpr int NP = 2 * ROWS + 3;
-  auto reduce = [](float (&p)[NP], int from) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int j = 0; j < NP; ++j)
-        if (j >= from) p[j] += __shfl_xor_sync(0xffffffffu, p[j], o);
-  };
   float p[NP];
   if constexpr (SEQ) {
+    // The 2 ROWS + 3 sums (padded to 8) over the warp by halving: a lane whose bit is set keeps the upper half of
+    // the values and sends the lower, so 8 sums take 9 shuffles; then each is read from its lane by all.
+    static_assert(ROWS == 2, "eight sums");
+    auto reduce = [&] {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 7; ++i) v[i] = p[i];
+      v[7] = 0.f;
+#pragma unroll
+      for (int half = 4; half; half >>= 1) {
+        const bool upper = lane & (half * 4);
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, half * 4);
+        }
+      }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+      for (int i = 0; i < 7; ++i) p[i] = __shfl_sync(0xffffffffu, v[0], i * 4);
+    };
+    // running pointers of the token to load next
+    const T *pk = a.K + tok * a.ldk + (int64_t)hq * a.dk, *pq = a.Q + tok * a.ldq + (int64_t)hq * a.dk;
+    const T* pv = a.V + tok * a.ldv + (int64_t)h * a.dv + r0 + lane;
+    const float *pb = a.beta + tok * a.hv + h, *pg = a.g + tok * a.hv + h;
+    T* po = a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + lane;
+    const bool own = lane < ROWS && r0 + lane < a.dv;
+    int left = len;  // tokens from the pointers on
+    auto load_next = [&](Token<E>& x) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int col = VEC * (32 * i + lane);
+        if (col < a.dk) {
+          load_vec<VEC>(pk + col, &x.k[i * VEC]);
+          load_vec<VEC>(pq + col, &x.q[i * VEC]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x.k[i * VEC + j] = x.q[i * VEC + j] = 0.f;
+        }
+      }
+      x.beta = *pb;
+      x.g = *pg;
+      x.v = own ? load_one(pv) : 0.f;
+      if (--left > 0) pk += a.ldk, pq += a.ldq, pv += a.ldv, pb += a.hv, pg += a.hv;  // (else: the last one again)
+    };
     Token<E> x, y;
     if (len > 0) {
-      load(x, tok);
+      load_next(x);
+      load_next(y);
+#pragma unroll
+      for (int i = 0; i < 2 * ROWS; ++i) p[i] = 0.f;
       dots(x, p + 2 * ROWS);
-      reduce(p, 2 * ROWS);
+      reduce();
       factors(x, p + 2 * ROWS);
     }
-    if (len > 0) load(y, tok + min(1, len - 1));
 #pragma unroll 3
     for (int n = 0; n < len; ++n) {  // (unrolled so that the three tokens change names, not registers)
       Token<E> z;
-      load(z, tok + min(n + 2, len - 1));  // (past the last token: that one again, unused)
+      load_next(z);
       products(x, p);
       dots(y, p + 2 * ROWS);
-      reduce(p, 0);
-      update(x, p, tok + n);
+      reduce();
+      float out = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const float u = x.beta * (__shfl_sync(0xffffffffu, x.v, r) - x.al * (p[2 * r] * x.fk));
+        const float uk = u * x.fk;
+        if (lane == r) out = x.fq * (x.al * p[2 * r + 1] + uk * x.kq);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[r][i] = x.al * s[r][i] + uk * x.k[i];
+      }
+      if (own) store_one(po, out);
+      po += a.ldo;
       factors(y, p + 2 * ROWS);
       x = y;
       y = z;
