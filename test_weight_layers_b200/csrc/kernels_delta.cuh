@@ -521,8 +521,12 @@ struct StateArgs {
   float* w_part;            // [chunk][hv][dv / 16][64]
 };
 
-constexpr int DR_VROW = 48;                  // bytes per row of a warp's V / O tile (32 used): conflict-free 8x8 tiles
-constexpr int DR_VTILE = DR_C * DR_VROW;
+// A warp's V, dO or O tile: 64 token rows of 16 channels, 32 bytes each, the halves of rows 4..7 of every 8 swapped
+// so that the 8 rows of an 8x8 tile lie in different banks.
+constexpr int DR_VTILE = DR_C * 32;
+__device__ __forceinline__ uint32_t vtile_off(int row, int half) {
+  return (uint32_t)(row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
+}
 
 enum { PASS_OUT = 0, PASS_BACK = 1, PASS_SCAN = 2 };  // what a state pass is for
 
@@ -535,9 +539,10 @@ template <bool BACK>
 constexpr int state_warp_smem() {
   return (BACK ? 4 : 2) * DR_VTILE;
 }
+constexpr int DR_ETILE = 16 * DR_C * 4;  // a warp's E rows (reverse pass)
 template <int DK, bool BACK>
-constexpr int state_smem(int warps) {
-  return 2 * state_stage<DK, BACK>() + warps * state_warp_smem<BACK>() + 64;
+constexpr int state_smem(int warps, bool etile = false) {
+  return 2 * state_stage<DK, BACK>() + warps * (state_warp_smem<BACK>() + (etile ? DR_ETILE : 0)) + 64;
 }
 
 // A warp's 64 x 16 tile of token rows `p` (first channel v0 of head h), zero outside the sequence and the head.
@@ -548,7 +553,7 @@ __device__ __forceinline__ void load_vtile(uint32_t dst, const __nv_bfloat16* p,
     const int row = it * 16 + (lane >> 1), half = lane & 1;
     const int at = n * DR_C + row;
     const bool live = at < sq.len && v0 + half * 8 < dv;
-    cp_async16(dst + row * DR_VROW + half * 16, live ? p + (int64_t)(sq.tok + at) * ld + col0 + v0 + half * 8 : p, live);
+    cp_async16(dst + vtile_off(row, half), live ? p + (int64_t)(sq.tok + at) * ld + col0 + v0 + half * 8 : p, live);
   }
 }
 // ... and its counterpart: a tile in shared memory -> token rows.
@@ -560,17 +565,36 @@ __device__ __forceinline__ void store_vtile(const uint8_t* src, __nv_bfloat16* p
     const int at = n * DR_C + row;
     if (at < sq.len && v0 + half * 8 < dv)
       *reinterpret_cast<uint4*>(p + (int64_t)(sq.tok + at) * ld + col0 + v0 + half * 8) =
-          *reinterpret_cast<const uint4*>(src + row * DR_VROW + half * 16);
+          *reinterpret_cast<const uint4*>(src + vtile_off(row, half));
   }
 }
 // Address of 8x8 matrix lane/8 of token rows n0..n0+15 of such a tile: (tokens n0 + 8 (m / 2), channels 8 (m % 2));
 // read with .trans it gives the accumulator layout of two neighbouring 8-token tiles (rows = channels).
 __device__ __forceinline__ uint32_t vtile_addr(uint32_t base, int lane, int n0) {
-  return base + (n0 + ((lane >> 4) << 3) + (lane & 7)) * DR_VROW + (((lane >> 3) & 1) << 4);
+  return base + vtile_off(n0 + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
 }
 
+// A warp's 16 rows of dk floats, rows scaled back, to `out`; `rows` of them exist.
+template <int NT>
+__device__ __forceinline__ void store_rows(float* out, const float (&s)[NT][4], float i0, float i1, int rows, int dk,
+                                           int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float* p0 = out + (int64_t)g * dk + 2 * t;
+  float* p1 = p0 + 8 * (int64_t)dk;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (n * 8 + 8 > dk) break;  // (dk is a multiple of 8)
+    if (g < rows) *reinterpret_cast<float2*>(p0 + n * 8) = make_float2(s[n][0] * i0, s[n][1] * i0);
+    if (g + 8 < rows) *reinterpret_cast<float2*>(p1 + n * 8) = make_float2(s[n][2] * i1, s[n][3] * i1);
+  }
+}
+
+// Column of an even token index in a row of the kept E: pairs are permuted by the row (mod 8), so that 8 rows' pairs
+// lie in different banks once a tile is copied to shared memory as it is.
+__device__ __forceinline__ int etile_col(int row, int col) { return (((col >> 1) ^ ((row & 7) << 2)) << 1) | (col & 1); }
+
 template <int DK, int PASS>
-__global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
+__global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr bool BACK = PASS == PASS_BACK, SCAN = PASS == PASS_SCAN;
   constexpr int STAGE = state_stage<DK, BACK>();
@@ -578,20 +602,24 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   constexpr int HB = STAGE - KQ;
   constexpr int WSM = state_warp_smem<BACK>();
   constexpr int NT = DK / 8;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = (blockDim.x >> 5) - 1;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);  // [2] stage and tiles have landed
+  uint64_t* empty = full + 2;                                                    // [2] every warp has read them
   const int nblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
   const int vblocks = nblocks + (SCAN ? (DK + nwarp * 16 - 1) / (nwarp * 16) : 0);
   const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
   const int vb0 = blockIdx.x % vblocks;
   const bool phi = SCAN && vb0 >= nblocks;  // rows of the transition instead of value channels
-  const int v0 = ((phi ? vb0 - nblocks : vb0) * nwarp + warp) * 16;  // first row of this warp (may lie past the end)
+  const int vfirst = (phi ? vb0 - nblocks : vb0) * nwarp * 16;
+  const int v0 = vfirst + warp * 16;  // first row of this warp (may lie past the end)
   const int dv_in = phi ? 0 : a.dv;  // the transition's rows take no values
   if (tid == 0) {
-    mbar_init(&full[0], 1);
-    mbar_init(&full[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 33);  // the bulk copies, and each lane's tile copies
+      mbar_init(&empty[i], nwarp);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -603,28 +631,37 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   if (SCAN && (sq.seg == sq.nseg - 1 || (phi && sq.seg == 0))) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
-  auto load_stage = [&](int n) {  // one thread
-    const int64_t ci = sq.chunk0 + n;
-    uint8_t* st = smem + (n & 1) * STAGE;
-    const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
-    const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
-    if constexpr (SCAN) {  // without Q16 and P
-      mbar_expect_tx(&full[n & 1], KQ / 2 + HB - DR_TILE);
-      bulk_load(st, kq, KQ / 2, &full[n & 1]);
-      bulk_load(st + KQ, blk, 2 * DR_TILE, &full[n & 1]);
-      bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, &full[n & 1]);
-    } else {
-      mbar_expect_tx(&full[n & 1], KQ + HB);
-      bulk_load(st, kq, KQ, &full[n & 1]);
-      bulk_load(st + KQ, blk, HB, &full[n & 1]);
+  if (warp == nwarp) {  // the last warp brings the chunks, two ahead at most
+#pragma unroll 1
+    for (int n = 0; n < nchunk; ++n) {
+      uint64_t* bar = &full[n & 1];
+      if (n >= 2) mbar_wait(&empty[n & 1], ((n >> 1) - 1) & 1, a.guard);
+      if (lane == 0) {
+        const int64_t ci = sq.chunk0 + n;
+        uint8_t* st = smem + (n & 1) * STAGE;
+        const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
+        const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
+        if constexpr (SCAN) {  // without Q16 and P
+          mbar_expect_tx(bar, KQ / 2 + HB - DR_TILE);
+          bulk_load(st, kq, KQ / 2, bar);
+          bulk_load(st + KQ, blk, 2 * DR_TILE, bar);
+          bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, bar);
+        } else {
+          mbar_expect_tx(bar, KQ + HB);
+          bulk_load(st, kq, KQ, bar);
+          bulk_load(st + KQ, blk, HB, bar);
+        }
+      }
+      for (int w = 0; w < nwarp; ++w) {
+        const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + (n & 1) * DR_VTILE);
+        load_vtile(dst, a.V, a.ldv, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
+        if constexpr (BACK)
+          load_vtile(dst + 2 * DR_VTILE, a.dO, a.ldo, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
+      }
+      cp_arrive(bar);
     }
-  };
-  auto load_v = [&](int n) {
-    load_vtile(smem_u32(vbuf + (n & 1) * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, dv_in, lane);
-    if constexpr (BACK)
-      load_vtile(smem_u32(vbuf + (2 + (n & 1)) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
-    cp_commit();
-  };
+    return;
+  }
 
   float s[NT][4];
   const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
@@ -646,20 +683,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
     }
   float inv0 = 1.f, inv1 = 1.f;  // S = s * inv: rows g and g + 8 carry a power of two
 
-  if (nchunk > 0) {
-    if (tid == 0) load_stage(0);
-    load_v(0);
-  }
 #pragma unroll 1
   for (int n = 0; n < nchunk; ++n) {
-    if (n + 1 < nchunk) {
-      if (tid == 0) load_stage(n + 1);
-      load_v(n + 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
-    __syncwarp();
     // a wait that gives up records the error; the pass then runs on (bounded) with what the stage holds
     mbar_wait(&full[n & 1], (n >> 1) & 1, a.guard);
     const uint32_t st = smem_u32(smem + (n & 1) * STAGE);
@@ -669,16 +694,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
     const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;  // this chunk's block of the kept arrays
 
     if constexpr (BACK) {
-#pragma unroll
-      for (int k = 0; k < NT; ++k)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int r = v0 + g + 8 * p, col = k * 8 + 2 * t;
-          const float i = p ? inv1 : inv0;
-          if (r < a.dv && col < a.dk)
-            *reinterpret_cast<float2*>(a.keep_s + (blk * a.dv + r) * a.dk + col) =
-                make_float2(s[k][2 * p] * i, s[k][2 * p + 1] * i);
-        }
+      store_rows<NT>(a.keep_s + (blk * a.dv + v0) * a.dk, s, inv0, inv1, a.dv - v0, a.dk, lane);
     }
     // S K^T and S Q^T
     float m0 = 0.f, m1 = 0.f;
@@ -783,7 +799,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
 #pragma unroll
           for (int p = 0; p < 2; ++p)
             if (v0 + g + 8 * p < a.dv)
-              *reinterpret_cast<float2*>(a.keep_e + (blk * a.dv + v0 + g + 8 * p) * DR_C + col) =
+              *reinterpret_cast<float2*>(a.keep_e + (blk * a.dv + v0 + g + 8 * p) * DR_C + etile_col(g, col)) =
                   make_float2(r[k][2 * p], r[k][2 * p + 1]);
         }
         r[k][0] *= be.x;  // r becomes U
@@ -915,7 +931,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
         }
       }
     }
-    __syncthreads();  // the stage is read; the next copy into it may start
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[n & 1]);  // this warp has read the stage and its tiles
   }
   if (phi) {  // Phi as split images, each row at its own scale
     float m0 = 0.f, m1 = 0.f;
@@ -950,17 +967,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_state(const StateArgs a) {
   float* to = a.S ? a.S + srow * a.dk : nullptr;
   if (SCAN) to = sq.seg == 0 ? a.seg_s + (grow + (int64_t)a.hv * a.dv) * a.dk : a.seg_n + grow * a.dk;
   else if (sq.seg < sq.nseg - 1) to = nullptr;
-  if (to) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
-        const float i = p ? inv1 : inv0;
-        if (r < a.dv && col < a.dk)
-          *reinterpret_cast<float2*>(to + (int64_t)r * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
-      }
-  }
+  if (to) store_rows<NT>(to + (int64_t)v0 * a.dk, s, inv0, inv1, a.dv - v0, a.dk, lane);
 }
 
 // ---------------------------------------------------------------------------

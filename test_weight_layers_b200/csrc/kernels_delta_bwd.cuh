@@ -8,8 +8,9 @@
 //     dQ = e^c dO S + F K
 //     dK = -e^c beta Z S - W K + e^{c_C - c} U dS' + F^T Q - W^T K
 // Scaling S by exp(g_t) at token t scales every later o and read error alike, so
-//     dg_t = <S~_t, dS~_t> = <S, dS> - sum_{i < t} (dO_i.O_i - dV_i.V_i)
-// with <S, dS> taken at each chunk's start: no sum runs over more than a chunk.
+//     dg_t = <S~_t, dS~_t> = <S', dS'> + sum_{i >= t} (dO_i.O_i - dV_i.V_i)
+//     <S', dS'> = e^{c_C} <S, dS'> + sum_j U_j . e^{c_C - c_j} dS' k_j
+// with <S', dS'> taken at each chunk's end: no sum runs over more than a chunk.
 //
 // Passes: the chunk preparation and the state pass again (they keep S, E and
 // dO.O), the reverse pass over the chunks (dS in registers as the state pass
@@ -33,12 +34,12 @@ struct ReverseArgs {
   const uint8_t* blk;
   int blk_bytes;
   Guard guard;
-  const float *keep_s, *keep_e;
+  const float* keep_e;
   float* keep_ds;  // [chunk][hv][dv][dk] dS'
   float* keep_z;   // [chunk][hv][dv][64] Z^T
   float* w_part;   // [chunk][hv][dv / 16][64]: dO.O in, dO.O - dV.V out
   float* b_part;   // [chunk][hv][dv / 16][64] E.Z
-  float* x_part;   // [chunk][hv][dv / 16] <S, dS>
+  float* x_part;   // [chunk][hv][dv / 16] sum_j U_j . e^{c_C - c_j} dS' k_j
   // segments: [segment][hv][dv][dk] gradients at their ends (of the segments before the last) and scan results
   float *seg_ds, *seg_n;
 };
@@ -46,24 +47,28 @@ struct ReverseArgs {
 // As the state pass: a warp owns 16 value channels and keeps dS [16][dk] in registers.  SCAN: only what a segment
 // adds to the gradient that passes through it (from zero; the last segment from dS).
 template <int DK, bool SCAN>
-__global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
+__global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int STAGE = state_stage<DK, true>();
   constexpr int KQ = 2 * DR_C * DK * 2;
   constexpr int HB = STAGE - KQ;
   constexpr int WSM = state_warp_smem<true>();
   constexpr int NT = DK / 8;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = (blockDim.x >> 5) - 1;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);
+  float* etile = reinterpret_cast<float*>(smem + 2 * STAGE + nwarp * WSM);  // [16 nwarp][64] E of one chunk
+  uint64_t* full = reinterpret_cast<uint64_t*>(etile + nwarp * (DR_ETILE / 4));  // [2] stages, [1] E have landed
+  uint64_t* empty = full + 3;                                                    // [2] stages, [1] E are read
   const int vblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
   const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
-  const int v0 = (blockIdx.x % vblocks * nwarp + warp) * 16;
+  const int vfirst = blockIdx.x % vblocks * nwarp * 16, v0 = vfirst + warp * 16;
   const int n16 = (a.dv + 15) / 16;
   if (tid == 0) {
-    mbar_init(&full[0], 1);
-    mbar_init(&full[1], 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&full[i], i < 2 ? 33 : 1);
+      mbar_init(&empty[i], nwarp);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -73,18 +78,36 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
   if (sq.len < 0 || (SCAN && sq.seg == 0)) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
-  auto load_stage = [&](int n, int buf) {  // one thread
-    const int64_t ci = sq.chunk0 + n;
-    uint8_t* st = smem + buf * STAGE;
-    mbar_expect_tx(&full[buf], KQ + HB);
-    bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, &full[buf]);
-    bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, &full[buf]);
-  };
-  auto load_v = [&](int n, int buf) {
-    if constexpr (!SCAN) load_vtile(smem_u32(vbuf + buf * DR_VTILE), a.V, a.ldv, sq, n, h * a.dv, v0, a.dv, lane);
-    load_vtile(smem_u32(vbuf + (2 + buf) * DR_VTILE), a.dO, a.ldo, sq, n, h * a.dv, v0, a.dv, lane);
-    cp_commit();
-  };
+  if (warp == nwarp) {  // the last warp brings the chunks, the last one first
+#pragma unroll 1
+    for (int it = 0; it < nchunk; ++it) {
+      const int n = nchunk - 1 - it, buf = it & 1;
+      const int64_t ci = sq.chunk0 + n;
+      uint64_t* bar = &full[buf];
+      if (it >= 2) mbar_wait(&empty[buf], ((it >> 1) - 1) & 1, a.guard);
+      if (lane == 0) {
+        uint8_t* st = smem + buf * STAGE;
+        mbar_expect_tx(bar, KQ + HB);
+        bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, bar);
+        bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, bar);
+      }
+      for (int w = 0; w < nwarp; ++w) {
+        const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + buf * DR_VTILE);
+        if constexpr (!SCAN) load_vtile(dst, a.V, a.ldv, sq, n, h * a.dv, vfirst + w * 16, a.dv, lane);
+        load_vtile(dst + 2 * DR_VTILE, a.dO, a.ldo, sq, n, h * a.dv, vfirst + w * 16, a.dv, lane);
+      }
+      cp_arrive(bar);
+      if constexpr (!SCAN) {  // one E tile: free from the middle of the chunk before
+        if (it >= 1) mbar_wait(&empty[2], (it - 1) & 1, a.guard);
+        if (lane == 0) {
+          const uint32_t bytes = min(nwarp * 16, a.dv - vfirst) * DR_C * 4;
+          mbar_expect_tx(&full[2], bytes);
+          bulk_load(etile, a.keep_e + ((ci * a.hv + h) * a.dv + vfirst) * DR_C, bytes, &full[2]);
+        }
+      }
+    }
+    return;
+  }
 
   float s[NT][4];
   const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
@@ -102,21 +125,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     }
   float inv0 = 1.f, inv1 = 1.f;  // dS = s * inv
 
-  if (nchunk > 0) {
-    if (tid == 0) load_stage(nchunk - 1, 0);
-    load_v(nchunk - 1, 0);
-  }
 #pragma unroll 1
   for (int it = 0; it < nchunk; ++it) {
     const int n = nchunk - 1 - it, buf = it & 1;
-    if (n > 0) {
-      if (tid == 0) load_stage(n - 1, buf ^ 1);
-      load_v(n - 1, buf ^ 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
-    __syncwarp();
     mbar_wait(&full[buf], (it >> 1) & 1, a.guard);  // (as in the state pass)
     const uint32_t st = smem_u32(smem + buf * STAGE);
     const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, ph = yl + DR_TILE;
@@ -125,17 +136,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
     const uint32_t vb = smem_u32(vbuf + buf * DR_VTILE), db = smem_u32(vbuf + (2 + buf) * DR_VTILE);
     const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;
 
-    // keep dS'
-#pragma unroll
-    for (int k = 0; k < NT; ++k)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int r = v0 + g + 8 * p, col = k * 8 + 2 * t;
-        const float i = p ? inv1 : inv0;
-        if (!SCAN && r < a.dv && col < a.dk)
-          *reinterpret_cast<float2*>(a.keep_ds + (blk * a.dv + r) * a.dk + col) =
-              make_float2(s[k][2 * p] * i, s[k][2 * p + 1] * i);
-      }
+    if constexpr (!SCAN) store_rows<NT>(a.keep_ds + (blk * a.dv + v0) * a.dk, s, inv0, inv1, a.dv - v0, a.dk, lane);
     // dS' K^T
     float m0 = 0.f, m1 = 0.f;
 #pragma unroll
@@ -213,13 +214,34 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
           mma_f16(x[2 * np + 1], hi, p[2], p[3]);
         }
       }
+      float kept = 0.f;
+      if constexpr (!SCAN) mbar_wait(&full[2], it & 1, a.guard);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float2 ak = *reinterpret_cast<const float2*>(vec + DV_AK * DR_C + k * 8 + 2 * t);
-        r[k][0] = x[k][0] * i0 + ak.x * (r[k][0] * is0);
-        r[k][1] = x[k][1] * i0 + ak.y * (r[k][1] * is0);
-        r[k][2] = x[k][2] * i1 + ak.x * (r[k][2] * is1);
-        r[k][3] = x[k][3] * i1 + ak.y * (r[k][3] * is1);
+        const int col = k * 8 + 2 * t;
+        const float2 ak = *reinterpret_cast<const float2*>(vec + DV_AK * DR_C + col);
+        const float h00 = ak.x * (r[k][0] * is0), h01 = ak.y * (r[k][1] * is0);
+        const float h10 = ak.x * (r[k][2] * is1), h11 = ak.y * (r[k][3] * is1);
+        if constexpr (!SCAN) {  // U = beta E (what lies past dv is not read: dS' is zero there, E is not)
+          const float2 be = *reinterpret_cast<const float2*>(vec + DV_BETA * DR_C + col);
+          if (v0 + g < a.dv) {
+            const float2 e = *reinterpret_cast<const float2*>(etile + (warp * 16 + g) * DR_C + etile_col(g, col));
+            kept += be.x * e.x * h00 + be.y * e.y * h01;
+          }
+          if (v0 + g + 8 < a.dv) {
+            const float2 e = *reinterpret_cast<const float2*>(etile + (warp * 16 + g + 8) * DR_C + etile_col(g, col));
+            kept += be.x * e.x * h10 + be.y * e.y * h11;
+          }
+        }
+        r[k][0] = x[k][0] * i0 + h00;
+        r[k][1] = x[k][1] * i0 + h01;
+        r[k][2] = x[k][2] * i1 + h10;
+        r[k][3] = x[k][3] * i1 + h11;
+      }
+      if constexpr (!SCAN) {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) kept += __shfl_xor_sync(0xffffffffu, kept, m);
+        if (lane == 0 && v0 < a.dv) a.x_part[blk * n16 + v0 / 16] = kept;
       }
     }
     // Z = dU + Y^T (beta dU); Y's row scale goes to the other factor
@@ -287,9 +309,10 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
 #pragma unroll
           for (int p = 0; p < 2; ++p)
             if (v0 + g + 8 * p < a.dv) {
-              const int64_t at = (blk * a.dv + v0 + g + 8 * p) * DR_C + col;
-              *reinterpret_cast<float2*>(a.keep_z + at) = make_float2(r[k][2 * p], r[k][2 * p + 1]);
-              const float2 e = *reinterpret_cast<const float2*>(a.keep_e + at);
+              *reinterpret_cast<float2*>(a.keep_z + (blk * a.dv + v0 + g + 8 * p) * DR_C + col) =
+                  make_float2(r[k][2 * p], r[k][2 * p + 1]);
+              const float2 e =
+                  *reinterpret_cast<const float2*>(etile + (warp * 16 + g + 8 * p) * DR_C + etile_col(g, col));
               ex += e.x * r[k][2 * p];
               ey += e.y * r[k][2 * p + 1];
             }
@@ -317,6 +340,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
         stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
       }
       __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[2]);  // E is read
       store_vtile(vbuf + buf * DR_VTILE, a.dV, a.ldv, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
     }
     // dS = e^{c_C} dS' + (e^c dO)^T Q - (e^c beta Z)^T K
@@ -382,50 +406,22 @@ __global__ void __launch_bounds__(256, 1) k_delta_reverse(const ReverseArgs a) {
         }
       }
     }
-    // <S, dS> of these channels
-    if constexpr (!SCAN) {
-      float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-      for (int k = 0; k < NT; ++k)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int rr = v0 + g + 8 * p, col = k * 8 + 2 * t;
-          if (rr < a.dv && col < a.dk) {
-            const float2 z = *reinterpret_cast<const float2*>(a.keep_s + (blk * a.dv + rr) * a.dk + col);
-            if (p) x1 += z.x * s[k][2] + z.y * s[k][3];
-            else x0 += z.x * s[k][0] + z.y * s[k][1];
-          }
-        }
-      float xx = x0 * inv0 + x1 * inv1;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) xx += __shfl_xor_sync(0xffffffffu, xx, m);
-      if (lane == 0 && v0 < a.dv) a.x_part[blk * n16 + v0 / 16] = xx;
-    }
-    __syncthreads();  // the stage is read; the next copy into it may start
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[buf]);  // this warp has read the stage and its tiles
   }
   // the gradient of the state before the sequence; in the scan, that at the end of the segment before the last or
   // what a segment adds
   float* to = a.dS0 && sq.seg == 0 ? a.dS0 + srow * a.dk : nullptr;
   if (SCAN) to = sq.seg == sq.nseg - 1 ? a.seg_ds + (grow - (int64_t)a.hv * a.dv) * a.dk : a.seg_n + grow * a.dk;
-  if (to) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int r = v0 + g + 8 * p, col = n * 8 + 2 * t;
-        const float i = p ? inv1 : inv0;
-        if (r < a.dv && col < a.dk)
-          *reinterpret_cast<float2*>(to + (int64_t)r * a.dk + col) = make_float2(s[n][2 * p] * i, s[n][2 * p + 1] * i);
-      }
-  }
+  if (to) store_rows<NT>(to + (int64_t)v0 * a.dk, s, inv0, inv1, a.dv - v0, a.dk, lane);
 }
 
 // ---------------------------------------------------------------------------
 // dQ, dK and the gates: one block per (chunk, query/key head), over the value
 // heads that share it.  What leaves here is rounded to bf16 (the gates' gradients
 // are sums of what the two passes kept), so the products take fp32 operands as
-// they lie in memory through TF32 (11 significant bits, no scaling), 64 value
-// channels at a time.
+// they lie in memory through TF32 (11 significant bits, no scaling).  32 value
+// channels at a time are copied in while the 32 before are multiplied.
 struct GradArgs {
   const __nv_bfloat16 *dO;
   int64_t ldo, ldq, ldk;
@@ -452,26 +448,31 @@ __device__ __forceinline__ uint32_t tf32(float x) {
   return r;
 }
 
-constexpr int GR_LDT = 72;  // floats per row of [dv][64] tiles: fragment reads k-major (4 rows x 8 columns) hit 32 banks
-constexpr int GR_LDA = 68;  // ... of [64][64] tiles read row-major (8 rows x 4 columns)
+constexpr int GR_V = 32;     // value channels of a tile
+constexpr int GR_LDT = 72;   // floats per row of [channels][64] tiles: fragment reads k-major (4 rows x 8 columns) hit 32 banks
+constexpr int GR_LDA = 68;   // ... of [64][64] tiles read row-major (8 rows x 4 columns)
+constexpr int GR_LDO = 40;   // bf16 per row of a dO tile [64][32]
+template <int DK>
+constexpr int grad_stage() {  // S, dS' | E, Z | dO
+  return (2 * GR_V * (DK + 8) + 2 * GR_V * GR_LDT) * 4 + DR_C * GR_LDO * 2;
+}
 template <int DK>
 constexpr int grad_smem() {
-  return (2 * DR_C * (DK + 8) + 2 * DR_C * GR_LDT + 3 * DR_C * GR_LDA + 5 * DR_C) * 4;
+  constexpr int stages = 2 * grad_stage<DK>(), kq = 2 * DR_C * (DK + 8) * 4;  // K~, Q~ take the stages' place
+  return (stages > kq ? stages : kq) + (2 * DR_C * GR_LDA + 5 * DR_C) * 4;
 }
 
 template <int DK>
 __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int LDS = DK + 8;
+  constexpr int LDS = DK + 8, STAGE = grad_stage<DK>();
+  constexpr int KQ_BYTES = 2 * DR_C * LDS * 4;
   constexpr int NH = DK / 16;  // n-tiles of a warp's half of the dk columns
-  float* Sm = reinterpret_cast<float*>(smem);  // S tile [64][LDS]; later K~
-  float* Dm = Sm + DR_C * LDS;                 // dS' tile; later Q~
-  float* Um = Dm + DR_C * LDS;                 // U^T tile [64 channels][GR_LDT]
-  float* Zm = Um + DR_C * GR_LDT;              // beta Z, the same
-  float* Om = Zm + DR_C * GR_LDT;              // dO tile [64 tokens][GR_LDA]
-  float* Fm = Om + DR_C * GR_LDA;              // F [64][GR_LDA]
-  float* Wm = Fm + DR_C * GR_LDA;              // W
-  float* vc = Wm + DR_C * GR_LDA;              // c, beta, e^c, e^{c_C - c} of the value head
+  float* Km = reinterpret_cast<float*>(smem);  // K~ [64][LDS] and Q~, once the tiles are done
+  float* Qm = Km + DR_C * LDS;
+  float* Fm = reinterpret_cast<float*>(smem + (2 * STAGE > KQ_BYTES ? 2 * STAGE : KQ_BYTES));  // F [64][GR_LDA]
+  float* Wm = Fm + DR_C * GR_LDA;                                                              // W
+  float* vc = Wm + DR_C * GR_LDA;  // c, beta, beta e^c, beta e^{c_C - c} of the value head
   float* red = vc + 4 * DR_C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -480,6 +481,40 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   pdl_wait();
   const DrChunk cu = a.chunks[ci];
   if (cu.len < 0) return;
+  const int ntiles = (a.dv + GR_V - 1) / GR_V;
+
+  // tile q (value head q / ntiles, channels 32 (q % ntiles)..) into stage q % 2, zero past dv, dk and the tokens
+  auto load_tile = [&](int q) {
+    const int h = hq * rep + q / ntiles, d0 = q % ntiles * GR_V;
+    const int64_t row0 = ((int64_t)ci * a.hv + h) * a.dv + d0;
+    const uint32_t st = smem_u32(smem + (q & 1) * STAGE);
+    const int rows = a.dv - d0;
+#pragma unroll
+    for (int i = tid; i < GR_V * (DK / 4); i += 256) {
+      const int r = i / (DK / 4), c = i % (DK / 4) * 4;
+      const bool live = r < rows && c < a.dk;
+      const int64_t at = live ? (row0 + r) * a.dk + c : 0;
+      cp_async16(st + (r * LDS + c) * 4, a.keep_s + at, live);
+      cp_async16(st + ((GR_V + r) * LDS + c) * 4, a.keep_ds + at, live);
+    }
+    const uint32_t et = st + 2 * GR_V * LDS * 4, zt = et + GR_V * GR_LDT * 4, ot = zt + GR_V * GR_LDT * 4;
+#pragma unroll
+    for (int i = tid; i < GR_V * 16; i += 256) {
+      const int r = i >> 4, c = i & 15;
+      const bool live = r < rows;
+      const int64_t at = live ? (row0 + r) * DR_C : 0;
+      // (the pairs of a kept E row are permuted in fours of tokens: 16-byte pieces stay whole)
+      cp_async16(et + (r * GR_LDT + c * 4) * 4, a.keep_e + at + (live ? (c ^ (((d0 + r) & 7) << 1)) * 4 : 0), live);
+      cp_async16(zt + (r * GR_LDT + c * 4) * 4, a.keep_z + at + (live ? c * 4 : 0), live);
+    }
+    {
+      const int r = tid >> 2, c = (tid & 3) * 8;
+      const bool live = r < cu.len && c < rows;
+      const __nv_bfloat16* src = live ? a.dO + (int64_t)(cu.tok + r) * a.ldo + (int64_t)h * a.dv + d0 + c : a.dO;
+      cp_async16(ot + (r * GR_LDO + c) * 2, src, live);
+    }
+    cp_commit();
+  };
 
   float q[NH][4], k[NH][4];  // dQ~ and dK~, rows 16 rg + {g, g + 8}, columns ch DK/2 + 8 n + {2t, 2t + 1}
 #pragma unroll
@@ -488,111 +523,78 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
     for (int j = 0; j < 4; ++j) q[n][j] = k[n][j] = 0.f;
   const int r0 = rg * 16 + g;
 
+  load_tile(0);
 #pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
     const int64_t blk = (int64_t)ci * a.hv + h;
     const float* vec = reinterpret_cast<const float*>(a.blk + blk * a.blk_bytes + 3 * DR_TILE);
-    __syncthreads();  // the head before is done with shared memory
+    // the gates' sums of the two passes, read ahead of the tiles
+    float w_sum = 0.f, b_sum = 0.f, x_sum = 0.f;
     if (tid < DR_C) {
-      const float c = vec[DV_C * DR_C + tid], G = vec[DV_C * DR_C + DR_C - 1];
+      const float c = vec[DV_C * DR_C + tid], G = vec[DV_C * DR_C + DR_C - 1], be = vec[DV_BETA * DR_C + tid];
       vc[tid] = c;
-      vc[DR_C + tid] = vec[DV_BETA * DR_C + tid];
-      vc[2 * DR_C + tid] = expf(c);
-      vc[3 * DR_C + tid] = expf(G - c);
-    }
-    // the gates: dbeta = E.Z, dg_t = <S, dS> - sum_{i < t} w_i
-    if (tid < DR_C) {
-      float w = 0.f, b = 0.f, x = 0.f;
+      vc[DR_C + tid] = be;
+      vc[2 * DR_C + tid] = be * expf(c);
+      vc[3 * DR_C + tid] = be * expf(G - c);
       for (int p = 0; p < n16; ++p) {
-        w += a.w_part[(blk * n16 + p) * DR_C + tid];
-        b += a.b_part[(blk * n16 + p) * DR_C + tid];
-        x += a.x_part[blk * n16 + p];
-      }
-      float sum = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      if (tid == 31) red[0] = sum;
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (tid >= 32) sum += red[0];
-      if (tid < cu.len) {
-        const int64_t at = (int64_t)(cu.tok + tid) * a.hv + h;
-        a.dg[at] = x - (sum - w);
-        a.dbeta[at] = b;
+        w_sum += a.w_part[(blk * n16 + p) * DR_C + tid];
+        b_sum += a.b_part[(blk * n16 + p) * DR_C + tid];
+        x_sum += a.x_part[blk * n16 + p];
       }
     }
-    float f[4][4], wm[4][4];
+    float f[4][4], wm[4][4], sd = 0.f;  // F, W; this thread's part of <S, dS'>
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[n][j] = wm[n][j] = 0.f;
     __syncthreads();
-    const float ec0 = vc[2 * DR_C + r0], ec1 = vc[2 * DR_C + r0 + 8];
-    const float el0 = vc[3 * DR_C + r0], el1 = vc[3 * DR_C + r0 + 8];
+    const float bc0 = -vc[2 * DR_C + r0], bc1 = -vc[2 * DR_C + r0 + 8];
+    const float bl0 = vc[3 * DR_C + r0], bl1 = vc[3 * DR_C + r0 + 8];
+    const float ec0 = expf(vc[r0]), ec1 = expf(vc[r0 + 8]);
 
 #pragma unroll 1
-    for (int d0 = 0; d0 < a.dv; d0 += DR_C) {
-      if (d0) __syncthreads();
-      // tiles of 64 value channels, zero past dv and dk
-      for (int i = tid; i < DR_C * (DK / 4); i += 256) {
-        const int r = i / (DK / 4), c = i % (DK / 4) * 4;
-        float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f), d4 = s4;
-        if (d0 + r < a.dv && c < a.dk) {
-          const int64_t at = (blk * a.dv + d0 + r) * a.dk + c;
-          s4 = *reinterpret_cast<const float4*>(a.keep_s + at);
-          d4 = *reinterpret_cast<const float4*>(a.keep_ds + at);
-        }
-        *reinterpret_cast<float4*>(Sm + r * LDS + c) = s4;
-        *reinterpret_cast<float4*>(Dm + r * LDS + c) = d4;
-      }
-      for (int i = tid; i < DR_C * 16; i += 256) {
-        const int r = i >> 4, c = (i & 15) * 4;
-        float4 e4 = make_float4(0.f, 0.f, 0.f, 0.f), z4 = e4;
-        if (d0 + r < a.dv) {
-          const int64_t at = (blk * a.dv + d0 + r) * DR_C + c;
-          e4 = *reinterpret_cast<const float4*>(a.keep_e + at);
-          z4 = *reinterpret_cast<const float4*>(a.keep_z + at);
-        }
-        const float4 be = *reinterpret_cast<const float4*>(vc + DR_C + c);
-        *reinterpret_cast<float4*>(Um + r * GR_LDT + c) = make_float4(e4.x * be.x, e4.y * be.y, e4.z * be.z, e4.w * be.w);
-        *reinterpret_cast<float4*>(Zm + r * GR_LDT + c) = make_float4(z4.x * be.x, z4.y * be.y, z4.z * be.z, z4.w * be.w);
-      }
-      for (int i = tid; i < DR_C * 8; i += 256) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < cu.len && d0 + c < a.dv)
-          x = *reinterpret_cast<const uint4*>(a.dO + (int64_t)(cu.tok + r) * a.ldo + (int64_t)h * a.dv + d0 + c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = (&x.x)[j];
-          Om[r * GR_LDA + c + 2 * j] = __uint_as_float(w << 16);
-          Om[r * GR_LDA + c + 2 * j + 1] = __uint_as_float(w & 0xffff0000u);
-        }
+    for (int tile = 0; tile < ntiles; ++tile) {
+      const int at = hr * ntiles + tile;
+      // (after a head's last tile K~ and Q~ take the stages' place, so the next head's first tile waits for them)
+      if (tile + 1 < ntiles) {
+        load_tile(at + 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
       }
       __syncthreads();
-#pragma unroll 2
-      for (int kk = 0; kk < DR_C; kk += 8) {
-        const float o0 = Om[r0 * GR_LDA + kk + t], o1 = Om[(r0 + 8) * GR_LDA + kk + t];
-        const float o2 = Om[r0 * GR_LDA + kk + t + 4], o3 = Om[(r0 + 8) * GR_LDA + kk + t + 4];
+      const float* Sm = reinterpret_cast<const float*>(smem + (at & 1) * STAGE);
+      const float *Dm = Sm + GR_V * LDS, *Em = Dm + GR_V * LDS, *Zm = Em + GR_V * GR_LDT;
+      const __nv_bfloat16* Om = reinterpret_cast<const __nv_bfloat16*>(Zm + GR_V * GR_LDT);
+#pragma unroll
+      for (int i = tid; i < GR_V * (DK / 4); i += 256) {
+        const int o = i / (DK / 4) * LDS + i % (DK / 4) * 4;
+        const float4 x = *reinterpret_cast<const float4*>(Sm + o), y = *reinterpret_cast<const float4*>(Dm + o);
+        sd += (x.x * y.x + x.y * y.y) + (x.z * y.z + x.w * y.w);
+      }
+#pragma unroll
+      for (int kk = 0; kk < GR_V; kk += 8) {
+        const float o0 = __bfloat162float(Om[r0 * GR_LDO + kk + t]), o1 = __bfloat162float(Om[(r0 + 8) * GR_LDO + kk + t]);
+        const float o2 = __bfloat162float(Om[r0 * GR_LDO + kk + t + 4]),
+                    o3 = __bfloat162float(Om[(r0 + 8) * GR_LDO + kk + t + 4]);
         const float z0 = Zm[(kk + t) * GR_LDT + r0], z1 = Zm[(kk + t) * GR_LDT + r0 + 8];
         const float z2 = Zm[(kk + t + 4) * GR_LDT + r0], z3 = Zm[(kk + t + 4) * GR_LDT + r0 + 8];
-        const float u0 = Um[(kk + t) * GR_LDT + r0], u1 = Um[(kk + t) * GR_LDT + r0 + 8];
-        const float u2 = Um[(kk + t + 4) * GR_LDT + r0], u3 = Um[(kk + t + 4) * GR_LDT + r0 + 8];
-        const uint32_t oa[4] = {tf32(o0), tf32(o1), tf32(o2), tf32(o3)};
+        const float u0 = Em[(kk + t) * GR_LDT + r0], u1 = Em[(kk + t) * GR_LDT + r0 + 8];
+        const float u2 = Em[(kk + t + 4) * GR_LDT + r0], u3 = Em[(kk + t + 4) * GR_LDT + r0 + 8];
+        const uint32_t oa[4] = {__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(o2), __float_as_uint(o3)};
         const uint32_t za[4] = {tf32(z0), tf32(z1), tf32(z2), tf32(z3)};
         const uint32_t oe[4] = {tf32(o0 * ec0), tf32(o1 * ec1), tf32(o2 * ec0), tf32(o3 * ec1)};
-        const uint32_t ze[4] = {tf32(-z0 * ec0), tf32(-z1 * ec1), tf32(-z2 * ec0), tf32(-z3 * ec1)};
-        const uint32_t ue[4] = {tf32(u0 * el0), tf32(u1 * el1), tf32(u2 * el0), tf32(u3 * el1)};
+        const uint32_t ze[4] = {tf32(z0 * bc0), tf32(z1 * bc1), tf32(z2 * bc0), tf32(z3 * bc1)};
+        const uint32_t ue[4] = {tf32(u0 * bl0), tf32(u1 * bl1), tf32(u2 * bl0), tf32(u3 * bl1)};
+        if (ch * 32 <= rg * 16 + 15) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {  // F, W: columns j = 32 ch + 8 n + g
-          const int j = ch * 32 + n * 8;
-          if (j > rg * 16 + 15) break;
-          const uint32_t b0 = tf32(Um[(kk + t) * GR_LDT + j + g]), b1 = tf32(Um[(kk + t + 4) * GR_LDT + j + g]);
-          mma_tf32(f[n], oa, b0, b1);
-          mma_tf32(wm[n], za, b0, b1);
+          for (int n = 0; n < 4; ++n) {  // F, W: columns j = 32 ch + 8 n + g
+            const int j = ch * 32 + n * 8 + g;
+            const uint32_t b0 = tf32(Em[(kk + t) * GR_LDT + j]), b1 = tf32(Em[(kk + t + 4) * GR_LDT + j]);
+            mma_tf32(f[n], oa, b0, b1);
+            mma_tf32(wm[n], za, b0, b1);
+          }
         }
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
@@ -604,29 +606,30 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
           mma_tf32(k[n], ue, e0, e1);
         }
       }
+      __syncthreads();  // the stage is read
     }
-    // F and W with their decays and masks
-    __syncthreads();
+    // F and W with their decays, gates and masks
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int j = ch * 32 + n * 8 + 2 * t;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p >> 1) * 8, jj = j + (p & 1);
-        const float d = jj <= i ? expf(vc[i] - vc[jj]) : 0.f;
+        const float d = jj <= i ? expf(vc[i] - vc[jj]) * vc[DR_C + jj] : 0.f;
         Fm[i * GR_LDA + jj] = jj <= i ? d * f[n][p] : 0.f;
-        Wm[i * GR_LDA + jj] = jj < i ? d * wm[n][p] : 0.f;
+        Wm[i * GR_LDA + jj] = jj < i ? d * vc[DR_C + i] * wm[n][p] : 0.f;
       }
     }
     // K~ = f_k K16, Q~ = f_q Q16
     const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
     const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
+#pragma unroll 4
     for (int i = tid; i < 2 * DR_C * (DK / 8); i += 256) {
       const int isq = i >= DR_C * (DK / 8), ii = i - isq * DR_C * (DK / 8);
       const int r = ii / (DK / 8), c = ii % (DK / 8);
       const uint4 x = *reinterpret_cast<const uint4*>(kq + isq * DR_C * DK * 2 + img_off(r, c, DK * 2));
       const float fs = tf[(isq ? TF_FQ : TF_FK) * DR_C + r];
-      float* dst = (isq ? Dm : Sm) + r * LDS + c * 8;
+      float* dst = (isq ? Qm : Km) + r * LDS + c * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 y = unpack_f16x2((&x.x)[j]);
@@ -634,7 +637,27 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
         dst[2 * j + 1] = y.y * fs;
       }
     }
+    // <S, dS'> of the block, for the gates: dg_t = <S', dS'> + sum_{i >= t} w_i, dbeta = E.Z
+#pragma unroll
+    for (int m = 16; m; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
+    if (lane == 0) red[warp] = sd;
+    float sum = w_sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (tid < DR_C && lane == 31) red[8 + warp] = sum;
     __syncthreads();
+    if (tid < cu.len) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d += red[i];
+      const float all = red[8] + red[9], before = (tid >= 32 ? red[8] : 0.f) + sum - w_sum;
+      const int64_t at = (int64_t)(cu.tok + tid) * a.hv + h;
+      a.dg[at] = expf(vc[DR_C - 1]) * d + x_sum + (all - before);
+      a.dbeta[at] = b_sum;
+    }
     // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~
 #pragma unroll 1
     for (int kk = 0; kk < DR_C; kk += 8) {
@@ -651,25 +674,26 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
         const int c = ch * (DK / 2) + n * 8 + g;
-        const uint32_t b0 = tf32(Sm[(kk + t) * LDS + c]), b1 = tf32(Sm[(kk + t + 4) * LDS + c]);
+        const uint32_t b0 = tf32(Km[(kk + t) * LDS + c]), b1 = tf32(Km[(kk + t + 4) * LDS + c]);
         if (lower) {
           mma_tf32(q[n], fa, b0, b1);
           mma_tf32(k[n], wa, b0, b1);
         }
         if (upper) {
           mma_tf32(k[n], wt, b0, b1);
-          const uint32_t e0 = tf32(Dm[(kk + t) * LDS + c]), e1 = tf32(Dm[(kk + t + 4) * LDS + c]);
+          const uint32_t e0 = tf32(Qm[(kk + t) * LDS + c]), e1 = tf32(Qm[(kk + t + 4) * LDS + c]);
           mma_tf32(k[n], ft, e0, e1);
         }
       }
     }
+    __syncthreads();  // shared memory is free for the next value head
+    if (hr + 1 < rep) load_tile((hr + 1) * ntiles);
   }
 
   // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)), the dot over both column halves
   const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
   const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
   float* dots = Fm;  // [2 halves][2][64]
-  __syncthreads();
 #pragma unroll
   for (int isq = 0; isq < 2; ++isq)
 #pragma unroll

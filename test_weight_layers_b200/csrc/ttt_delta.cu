@@ -162,10 +162,9 @@ constexpr int pass_warps(bool back) {
 }
 int pass_warps_for(int most, int dv) { return std::min(most, (dv + 15) / 16); }
 
-// Launches a pass over the chunks of each segment.  `rows`: rows of 16 that share a block of `warps`, per head.
+// Launches a pass over the chunks of each segment (`warps` with the one that copies).
 template <auto K, typename Args>
-int launch_pass(const Args& a, int segs, int64_t blocks_per_head, int warps, int smem,
-                cudaStream_t s) {
+int launch_pass(const Args& a, int segs, int64_t blocks_per_head, int warps, int smem, cudaStream_t s) {
   if (blocks_per_head * a.hv * segs > INT32_MAX) return TTT_ERR_UNSUPPORTED;
   TTT_TRY(smem_opt_in<K>());
   TTT_TRY(launch_pdl(K, dim3((unsigned)(blocks_per_head * a.hv * segs)), dim3(warps * 32), smem, s, a));
@@ -187,7 +186,7 @@ int run_scan(const StateArgs& sa, const DeltaWs& w, cudaStream_t s) {
   if (!w.seg_chunks) return TTT_OK;
   const int warps = pass_warps<DK>(false);
   TTT_TRY((launch_pass<k_delta_state<DK, PASS_SCAN>>(sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
-                      warps, state_smem<DK, false>(warps), s)));
+                                                   warps + 1, state_smem<DK, false>(warps), s)));
   return launch_join<DK, false>(sa, w.seg_s, w, s);
 }
 
@@ -204,22 +203,22 @@ int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream
   TTT_TRY((launch_prep<DK, false>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
   const int warps = pass_warps_for(pass_warps<DK>(false), sa.dv);
-  return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps), warps,
-                     state_smem<DK, false>(warps), s);
+  return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps), warps + 1,
+                                                  state_smem<DK, false>(warps), s);
 }
 
 template <int DK>
 int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, const DeltaWs& w, cudaStream_t s) {
   TTT_TRY((launch_prep<DK, true>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
-  const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps);
+  const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps, true);
   const int64_t blocks = blocks_of(sa.dv, warps);
-  TTT_TRY((launch_pass<k_delta_state<DK, PASS_BACK>>(sa, w.max_segs, blocks, warps, smem, s)));
+  TTT_TRY((launch_pass<k_delta_state<DK, PASS_BACK>>(sa, w.max_segs, blocks, warps + 1, smem, s)));
   if (w.seg_chunks) {  // the transitions are the state pass's, transposed
-    TTT_TRY((launch_pass<k_delta_reverse<DK, true>>(ra, w.max_segs, blocks, warps, smem, s)));
+    TTT_TRY((launch_pass<k_delta_reverse<DK, true>>(ra, w.max_segs, blocks, warps + 1, smem, s)));
     TTT_TRY((launch_join<DK, true>(sa, w.seg_s, w, s)));
   }
-  TTT_TRY((launch_pass<k_delta_reverse<DK, false>>(ra, w.max_segs, blocks, warps, smem, s)));
+  TTT_TRY((launch_pass<k_delta_reverse<DK, false>>(ra, w.max_segs, blocks, warps + 1, smem, s)));
   TTT_TRY(smem_opt_in<k_delta_grad<DK>>());
   TTT_TRY(launch_pdl(k_delta_grad<DK>, dim3((unsigned)w.max_chunks, ga.hk), dim3(256), grad_smem<DK>(), s, ga));
   TTT_LAUNCHED();
@@ -323,7 +322,6 @@ void pass_args(Args& a, const void* V, const ttt_delta_dims& d, const DeltaIo& x
   a.blk = w.blk;
   a.blk_bytes = w.blk_bytes;
   a.guard = Guard{w.status, wait_timeout_ns()};
-  a.keep_s = w.keep_s;
   a.keep_e = w.keep_e;
   a.w_part = w.w_part;
   a.seg_n = w.seg_n;
@@ -333,6 +331,7 @@ StateArgs state_args(const void* V, const float* S0, const ttt_delta_dims& d, co
   StateArgs a{};
   pass_args(a, V, d, x, w);
   a.S0 = S0;
+  a.keep_s = w.keep_s;
   a.seg_s = w.seg_s;
   a.phi = w.phi;
   a.phi_scale = w.phi_scale;
