@@ -192,7 +192,7 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 // TPR threads to a row, NV chunks of 8 columns to a thread; GROUPS: several means of y to a row.
 // Measured (131,072 x 768, bf16, all operands): NORM_F.
 template <typename T, int TPR, int NV, bool GROUPS, bool VEC>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm(const NormArgs<T> a) {
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV <= 3 ? 4 * 128 / (TPR > 128 ? TPR : 128) : 1) k_block_norm(const NormArgs<T> a) {
   constexpr int BLOCK = TPR > 128 ? TPR : 128;
   constexpr int RPB = BLOCK / TPR;  // rows per block
   __shared__ __align__(16) float red[2][TPR / 32];
@@ -202,17 +202,25 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_block_norm(const Norm
   const bool xr = a.X != nullptr, zr = a.Z != nullptr;
   const float inv_group = 1.f / (float)a.group, inv_d = 1.f / (float)a.D;
   const int64_t r0 = (int64_t)blockIdx.x * RPB + rb, step = (int64_t)gridDim.x * RPB;
-  RowAt at(r0, a.split);
+  RowAt at(r0, a.split), ahead = at;
   const RowAt by(step, a.split);
-  for (int64_t row = r0; row < a.rows; row += step, at.step(by, a.split)) {
-    Raw8<T> y[NV], x[NV], z[NV];
+  Raw8<T> ny[NV], nx[NV], nz[NV];  // the next row, in flight while one is worked on
+  auto load_row = [&] {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      y[i] = load8<VEC>(at.in(a.Y, a.ldy, a.D), col, a.D);
-      if (zr) z[i] = load8<VEC>(at.in(a.Z, a.ldz, a.D), col, a.D);
-      if (xr) x[i] = load8<VEC>(at.in(a.X, a.ldx, a.D), col, a.D);
+      ny[i] = load8<VEC>(ahead.in(a.Y, a.ldy, a.D), col, a.D);
+      if (zr) nz[i] = load8<VEC>(ahead.in(a.Z, a.ldz, a.D), col, a.D);
+      if (xr) nx[i] = load8<VEC>(ahead.in(a.X, a.ldx, a.D), col, a.D);
     }
+    ahead.step(by, a.split);
+  };
+  if (r0 < a.rows) load_row();
+  for (int64_t row = r0; row < a.rows; row += step, at.step(by, a.split)) {
+    Raw8<T> y[NV], x[NV], z[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) y[i] = ny[i], x[i] = nx[i], z[i] = nz[i];
+    if (row + step < a.rows) load_row();
     float sy[NV], s1[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
