@@ -62,6 +62,33 @@ __device__ __forceinline__ Raw8<float> pack8(const float (&x)[8], float) {
   return r;
 }
 
+// Two fp32 operations in one instruction (the gradient is bound by its instructions otherwise).
+__device__ __forceinline__ unsigned long long bits(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
+__device__ __forceinline__ float2 from_bits(unsigned long long v) { return *reinterpret_cast<float2*>(&v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return from_bits(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return from_bits(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void unpack2(const Raw8<__nv_bfloat16>& r, float2 (&x)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w = (&r.q[0].x)[j];
+    x[j] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void unpack2(const Raw8<float>& r, float2 (&x)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x[j] = make_float2(__uint_as_float((&r.q[j >> 1].x)[2 * (j & 1)]), __uint_as_float((&r.q[j >> 1].x)[2 * (j & 1) + 1]));
+}
+
 // Columns [col, col + 8) of a row, zero past D.  VEC: rows and weights are 16-byte aligned, D a multiple of 8.
 // Plain loads: an output may be one of the inputs.
 template <bool VEC, typename T>
@@ -78,6 +105,13 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int col, int D) {
     r = pack8(x, T());
   }
   return r;
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* p, int col, int D, const float (&x)[8]);
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* p, int col, int D, const float2 (&x)[4]) {
+  const float y[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+  store8<VEC>(p, col, D, y);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store8(T* p, int col, int D, const float (&x)[8]) {
@@ -110,6 +144,14 @@ __device__ __forceinline__ void weight8(const float* w, int col, int n, float (&
     for (int j = 0; j < 8; ++j)
       if (col + j < n) x[j] = __ldg(w + col + j);
   }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void weight8(const float* w, int col, int n, float2 (&x)[4]) {
+  float y[8];
+  weight8<VEC>(w, col, n, y);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = make_float2(y[2 * j], y[2 * j + 1]);
 }
 
 // Sums over the TPR threads of a row (TPR = 32: a warp; else the whole block).  The sums of a row have a buffer
@@ -295,8 +337,8 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
   float* buf = gbuf + rb * ((a.D + 7) / 8);
   const bool xr = a.X != nullptr, zr = a.Z != nullptr, gr = a.dXo != nullptr, nr = a.dN != nullptr;
   const float inv_group = 1.f / (float)a.group, inv_d = 1.f / (float)a.D;
-  float c_post[NV][8], c_lam[NV][8], c_pre[NV][8];  // this thread's column sums
-  float wq[NV][8], lm[NV][8], wp[NV][8];            // and its columns' weights
+  float2 c_post[NV][4], c_lam[NV][4], c_pre[NV][4];  // this thread's column sums
+  float2 wq[NV][4], lm[NV][4], wp[NV][4];            // and its columns' weights
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = (i * TPR + t) * 8;
@@ -304,7 +346,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
     weight8<VEC>(a.lam, col, a.D, lm[i]);
     weight8<VEC>(a.w_pre, col, a.D, wp[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c_post[i][j] = c_lam[i][j] = c_pre[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) c_post[i][j] = c_lam[i][j] = c_pre[i][j] = both(0.f);
   }
   const int64_t r0 = (int64_t)blockIdx.x * RPB + rb, step = (int64_t)gridDim.x * RPB;
   RowAt at(r0, a.split), ahead = at;
@@ -327,53 +369,57 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
   if (r0 < a.rows) load_row();
   for (int64_t row = r0; row < a.rows; row += step, at.step(by, a.split)) {
     Raw8<T> x[NV], z[NV], gx[NV], gn[NV];
-    float yh[NV][8];
+    float2 yh[NV][4];
     float sy[NV], s1[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      unpack8(ny[i], yh[i]);
+      unpack2(ny[i], yh[i]);
       x[i] = nx[i], z[i] = nz[i], gx[i] = ngx[i], gn[i] = ngn[i];
-      sy[i] = 0.f;
+      float2 q = both(0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sy[i] += yh[i][j] * yh[i][j];
+      for (int j = 0; j < 4; ++j) q = fma2(yh[i][j], yh[i][j], q);
+      sy[i] = q.x + q.y;
       s1[0] += sy[i];
     }
     if (row + step < a.rows) load_row();
     if constexpr (GROUPS) group_sum<TPR>(sy, t, a.D, a.group, buf);
     else row_sum<TPR>(s1, red);
     // s(z), s'(z), x' again, and the two sums of its norm
-    float sl[NV][8], ds[NV][8], xo[NV][8], ry[NV];
-    float s2[2] = {0.f, 0.f};  // sum x'^2, sum t x'
+    float2 sl[NV][4], ds[NV][4], xo[NV][4];
+    float ry[NV], s2[2] = {0.f, 0.f};  // sum x'^2, sum t x'
     const float ry1 = rsqrtf(s1[0] * inv_group + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       ry[i] = GROUPS ? rsqrtf(sy[i] * inv_group + a.eps) : ry1;
-      float v[8];
+      float2 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) yh[i][j] *= ry[i], sl[i][j] = 1.f, ds[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) yh[i][j] = mul2(yh[i][j], both(ry[i])), sl[i][j] = both(1.f), ds[i][j] = both(0.f);
       if (zr) {
-        unpack8(z[i], v);
+        unpack2(z[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float sg = sigmoid_f<T>(v[j]);
-          sl[i][j] = v[j] * sg;
-          ds[i][j] = sg + sl[i][j] * (1.f - sg);
+        for (int j = 0; j < 4; ++j) {
+          const float2 sg = make_float2(sigmoid_f<T>(v[j].x), sigmoid_f<T>(v[j].y));
+          sl[i][j] = mul2(v[j], sg);
+          ds[i][j] = fma2(sl[i][j], fma2(sg, both(-1.f), both(1.f)), sg);
         }
       }
       if (nr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xo[i][j] = lm[i][j] * (yh[i][j] * sl[i][j] * wq[i][j]);
+        for (int j = 0; j < 4; ++j) xo[i][j] = mul2(mul2(yh[i][j], sl[i][j]), mul2(lm[i][j], wq[i][j]));
         if (xr) {
-          unpack8(x[i], v);
+          unpack2(x[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) xo[i][j] += v[j];
+          for (int j = 0; j < 4; ++j) xo[i][j] = fma2(v[j], both(1.f), xo[i][j]);
         }
-        unpack8(gn[i], v);
+        unpack2(gn[i], v);
+        float2 q0 = both(0.f), q1 = q0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s2[0] += xo[i][j] * xo[i][j];
-          s2[1] += v[j] * wp[i][j] * xo[i][j];
+        for (int j = 0; j < 4; ++j) {
+          q0 = fma2(xo[i][j], xo[i][j], q0);
+          q1 = fma2(mul2(v[j], wp[i][j]), xo[i][j], q1);
         }
+        s2[0] += q0.x + q0.y;
+        s2[1] += q1.x + q1.y;
       }
     }
     float r = 0.f, m = 0.f;
@@ -383,33 +429,35 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
       m = r * r * (s2[1] * inv_d);
     }
     // column sums, dx, dz and the sums of u y r_y
-    float u[NV][8], su[NV], s3[1] = {0.f};
+    float2 u[NV][4];
+    float su[NV], s3[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = (i * TPR + t) * 8;
-      float d[8], v[8];
+      float2 d[4], v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = 0.f;
-      if (gr) unpack8(gx[i], d);
+      for (int j = 0; j < 4; ++j) d[j] = both(0.f);
+      if (gr) unpack2(gx[i], d);
       if (nr) {
-        unpack8(gn[i], v);
+        unpack2(gn[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          c_pre[i][j] += v[j] * (xo[i][j] * r);
-          d[j] += r * (v[j] * wp[i][j] - xo[i][j] * m);
+        for (int j = 0; j < 4; ++j) {
+          c_pre[i][j] = fma2(v[j], mul2(xo[i][j], both(r)), c_pre[i][j]);
+          const float2 e = fma2(xo[i][j], both(-m), mul2(v[j], wp[i][j]));
+          d[j] = fma2(e, both(r), d[j]);
         }
       }
-      su[i] = 0.f;
-      float dz[8];
+      float2 q = both(0.f), dz[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float ys = yh[i][j] * sl[i][j], dp = d[j] * lm[i][j], dw = dp * wq[i][j];
-        c_lam[i][j] += d[j] * (ys * wq[i][j]);
-        c_post[i][j] += dp * ys;
-        dz[j] = dw * yh[i][j] * ds[i][j];
-        u[i][j] = dw * sl[i][j];
-        su[i] += u[i][j] * yh[i][j];
+      for (int j = 0; j < 4; ++j) {
+        const float2 ys = mul2(yh[i][j], sl[i][j]), dp = mul2(d[j], lm[i][j]), dw = mul2(dp, wq[i][j]);
+        c_lam[i][j] = fma2(d[j], mul2(ys, wq[i][j]), c_lam[i][j]);
+        c_post[i][j] = fma2(dp, ys, c_post[i][j]);
+        dz[j] = mul2(mul2(dw, yh[i][j]), ds[i][j]);
+        u[i][j] = mul2(dw, sl[i][j]);
+        q = fma2(u[i][j], yh[i][j], q);
       }
+      su[i] = q.x + q.y;
       s3[0] += su[i];
       if (a.dX) store8<VEC>(at.in(a.dX, a.ldx, a.D), col, a.D, d);
       if (zr && a.dZ) store8<VEC>(at.in(a.dZ, a.ldz, a.D), col, a.D, dz);
@@ -421,9 +469,9 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
       for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + t) * 8;
         const float mu = (GROUPS ? su[i] : s3[0]) * inv_group;
-        float v[8];
+        float2 v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ry[i] * (u[i][j] - yh[i][j] * mu);
+        for (int j = 0; j < 4; ++j) v[j] = mul2(fma2(yh[i][j], both(-mu), u[i][j]), both(ry[i]));
         store8<VEC>(at.in(a.dY, a.ldy, a.D), col, a.D, v);
       }
     } else if (TPR > 32 && !GROUPS && !nr) {
@@ -446,7 +494,8 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV == 1 ? (TPR > 128 ? 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int col = (i * TPR + t) * 8 + j;
-              const float v = q == 0 ? c_post[i][j] : q == 1 ? c_lam[i][j] : c_pre[i][j];
+              const float2 v2 = q == 0 ? c_post[i][j / 2] : q == 1 ? c_lam[i][j / 2] : c_pre[i][j / 2];
+              const float v = j % 2 ? v2.y : v2.x;
               if (col < a.D) sum[col] = b ? sum[col] + v : v;
             }
         if constexpr (RPB > 1) __syncthreads();

@@ -28,7 +28,7 @@ NormShape norm_shape(const ttt_norm_cfg& c, bool row_wide, bool back, int64_t T)
   s.D = c.D / s.split;
   s.groups = c.group < s.D;
   const int chunks = (s.D + 7) / 8;
-  if (back) s.tpr = chunks <= 64 ? 32 : chunks <= 128 ? 128 : chunks <= 512 ? 256 : 512;
+  if (back) s.tpr = chunks <= 64 ? 32 : chunks <= 256 ? 128 : chunks <= 512 ? 256 : 512;
   else if (T * s.split <= 4 * kNormSms) s.tpr = chunks <= 32 ? 32 : chunks <= 128 ? 128 : chunks <= 256 ? 256 : 512;
   else s.tpr = chunks <= 128 ? 32 : chunks <= 512 ? 128 : 256;
   s.nv = (chunks + s.tpr - 1) / s.tpr;
@@ -180,7 +180,7 @@ int ttt_block_norm(const void* X, const void* Y, const void* Z, const float* w_p
   cudaStream_t s = (cudaStream_t)stream;
   const NormShape sh = norm_shape(*cfg, N || res_scale, false, T);
   const int block = std::max(128, sh.tpr), rpb = block / sh.tpr;
-  const int64_t blocks = std::min<int64_t>((T * sh.split + rpb - 1) / rpb, (int64_t)kNormSms * (2048 / block));
+  const int64_t blocks = std::min<int64_t>((T * sh.split + rpb - 1) / rpb, (int64_t)kNormSms * (512 / block));
   ProfScope ps(TTT_PROF_BNORM, s);
   if (dtype == TTT_FP32) return run_norm(norm_args<float>(c, *cfg, sh, ld, T), sh, vec != 0, false, blocks, s);
   return run_norm(norm_args<__nv_bfloat16>(c, *cfg, sh, ld, T), sh, vec != 0, false, blocks, s);
