@@ -420,8 +420,11 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
 // dQ, dK and the gates: one block per (chunk, query/key head), over the value
 // heads that share it.  What leaves here is rounded to bf16 (the gates' gradients
 // are sums of what the two passes kept), so the products take fp32 operands as
-// they lie in memory through TF32 (11 significant bits, no scaling).  32 value
-// channels at a time are copied in while the 32 before are multiplied.
+// they lie in memory through TF32 (11 significant bits, no scaling): A operands
+// and the intra-chunk tiles rounded, S, dS' and E, whose conversion would be a
+// quarter of the instructions, cut off by the hardware (4e-4 at most on average,
+// against 2e-3 for the outputs' rounding).  32 value channels at a time are
+// copied in while the 32 before are multiplied.
 struct GradArgs {
   const __nv_bfloat16 *dO;
   int64_t ldo, ldq, ldk;
@@ -459,7 +462,7 @@ constexpr int grad_stage() {  // S, dS' | E, Z | dO
 template <int DK>
 constexpr int grad_smem() {
   constexpr int stages = 2 * grad_stage<DK>(), kq = 2 * DR_C * (DK + 8) * 4;  // K~, Q~ take the stages' place
-  return (stages > kq ? stages : kq) + (2 * DR_C * GR_LDA + 5 * DR_C) * 4;
+  return (stages > kq ? stages : kq) + (2 * DR_C * GR_LDA + 4 * DR_C + 16 + 8 * DR_C + TF_N * DR_C) * 4;
 }
 
 template <int DK>
@@ -473,7 +476,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   float* Fm = reinterpret_cast<float*>(smem + (2 * STAGE > KQ_BYTES ? 2 * STAGE : KQ_BYTES));  // F [64][GR_LDA]
   float* Wm = Fm + DR_C * GR_LDA;                                                              // W
   float* vc = Wm + DR_C * GR_LDA;  // c, beta, beta e^c, beta e^{c_C - c} of the value head
-  float* red = vc + 4 * DR_C;
+  float* red = vc + 4 * DR_C;        // [16]
+  float* part = red + 16;            // [2][4][64] partial sums of w and E.Z
+  float* tfs = part + 8 * DR_C;      // the token factors (TF_*)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rg = warp >> 1, ch = warp & 1;  // this warp's 16 token rows and half of the columns
@@ -524,24 +529,34 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   const int r0 = rg * 16 + g;
 
   load_tile(0);
+  for (int i = tid; i < TF_N * DR_C; i += 256) tfs[i] = a.tok[((int64_t)ci * a.hk + hq) * TF_N * DR_C + i];
 #pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
     const int64_t blk = (int64_t)ci * a.hv + h;
     const float* vec = reinterpret_cast<const float*>(a.blk + blk * a.blk_bytes + 3 * DR_TILE);
-    // the gates' sums of the two passes, read ahead of the tiles
-    float w_sum = 0.f, b_sum = 0.f, x_sum = 0.f;
+    // the gates' sums of the two passes: a quarter of the channel slices to each 64 threads
+    {
+      const int tok = tid & (DR_C - 1), grp = tid >> 6;
+      float w = 0.f, b = 0.f;
+#pragma unroll 4
+      for (int p = grp; p < n16; p += 4) {
+        w += a.w_part[(blk * n16 + p) * DR_C + tok];
+        b += a.b_part[(blk * n16 + p) * DR_C + tok];
+      }
+      part[grp * DR_C + tok] = w;
+      part[(4 + grp) * DR_C + tok] = b;
+    }
+    float x_sum = 0.f;
+    for (int p = lane; p < n16; p += 32) x_sum += a.x_part[blk * n16 + p];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x_sum += __shfl_xor_sync(0xffffffffu, x_sum, o);
     if (tid < DR_C) {
       const float c = vec[DV_C * DR_C + tid], G = vec[DV_C * DR_C + DR_C - 1], be = vec[DV_BETA * DR_C + tid];
       vc[tid] = c;
       vc[DR_C + tid] = be;
       vc[2 * DR_C + tid] = be * expf(c);
       vc[3 * DR_C + tid] = be * expf(G - c);
-      for (int p = 0; p < n16; ++p) {
-        w_sum += a.w_part[(blk * n16 + p) * DR_C + tid];
-        b_sum += a.b_part[(blk * n16 + p) * DR_C + tid];
-        x_sum += a.x_part[blk * n16 + p];
-      }
     }
     float f[4][4], wm[4][4], sd = 0.f;  // F, W; this thread's part of <S, dS'>
 #pragma unroll
@@ -591,7 +606,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
 #pragma unroll
           for (int n = 0; n < 4; ++n) {  // F, W: columns j = 32 ch + 8 n + g
             const int j = ch * 32 + n * 8 + g;
-            const uint32_t b0 = tf32(Em[(kk + t) * GR_LDT + j]), b1 = tf32(Em[(kk + t + 4) * GR_LDT + j]);
+            const uint32_t b0 = __float_as_uint(Em[(kk + t) * GR_LDT + j]), b1 = __float_as_uint(Em[(kk + t + 4) * GR_LDT + j]);
             mma_tf32(f[n], oa, b0, b1);
             mma_tf32(wm[n], za, b0, b1);
           }
@@ -599,8 +614,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
           const int c = ch * (DK / 2) + n * 8 + g;
-          const uint32_t b0 = tf32(Sm[(kk + t) * LDS + c]), b1 = tf32(Sm[(kk + t + 4) * LDS + c]);
-          const uint32_t e0 = tf32(Dm[(kk + t) * LDS + c]), e1 = tf32(Dm[(kk + t + 4) * LDS + c]);
+          const uint32_t b0 = __float_as_uint(Sm[(kk + t) * LDS + c]), b1 = __float_as_uint(Sm[(kk + t + 4) * LDS + c]);
+          const uint32_t e0 = __float_as_uint(Dm[(kk + t) * LDS + c]), e1 = __float_as_uint(Dm[(kk + t + 4) * LDS + c]);
           mma_tf32(q[n], oe, b0, b1);
           mma_tf32(k[n], ze, b0, b1);
           mma_tf32(k[n], ue, e0, e1);
@@ -608,7 +623,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       }
       __syncthreads();  // the stage is read
     }
-    // F and W with their decays, gates and masks
+    // F and -W with their decays, gates and masks, rounded for the products
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int j = ch * 32 + n * 8 + 2 * t;
@@ -616,31 +631,38 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p >> 1) * 8, jj = j + (p & 1);
         const float d = jj <= i ? expf(vc[i] - vc[jj]) * vc[DR_C + jj] : 0.f;
-        Fm[i * GR_LDA + jj] = jj <= i ? d * f[n][p] : 0.f;
-        Wm[i * GR_LDA + jj] = jj < i ? d * vc[DR_C + i] * wm[n][p] : 0.f;
+        Fm[i * GR_LDA + jj] = __uint_as_float(tf32(jj <= i ? d * f[n][p] : 0.f));
+        Wm[i * GR_LDA + jj] = __uint_as_float(tf32(jj < i ? -d * vc[DR_C + i] * wm[n][p] : 0.f));
       }
     }
     // K~ = f_k K16, Q~ = f_q Q16
     const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
-    const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
 #pragma unroll 4
     for (int i = tid; i < 2 * DR_C * (DK / 8); i += 256) {
       const int isq = i >= DR_C * (DK / 8), ii = i - isq * DR_C * (DK / 8);
       const int r = ii / (DK / 8), c = ii % (DK / 8);
       const uint4 x = *reinterpret_cast<const uint4*>(kq + isq * DR_C * DK * 2 + img_off(r, c, DK * 2));
-      const float fs = tf[(isq ? TF_FQ : TF_FK) * DR_C + r];
+      const float fs = tfs[(isq ? TF_FQ : TF_FK) * DR_C + r];
       float* dst = (isq ? Qm : Km) + r * LDS + c * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 y = unpack_f16x2((&x.x)[j]);
-        dst[2 * j] = y.x * fs;
-        dst[2 * j + 1] = y.y * fs;
+        *reinterpret_cast<float2*>(dst + 2 * j) =
+            make_float2(__uint_as_float(tf32(y.x * fs)), __uint_as_float(tf32(y.y * fs)));
       }
     }
     // <S, dS'> of the block, for the gates: dg_t = <S', dS'> + sum_{i >= t} w_i, dbeta = E.Z
 #pragma unroll
     for (int m = 16; m; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
     if (lane == 0) red[warp] = sd;
+    float w_sum = 0.f, b_sum = 0.f;
+    if (tid < DR_C) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w_sum += part[i * DR_C + tid];
+        b_sum += part[(4 + i) * DR_C + tid];
+      }
+    }
     float sum = w_sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -659,30 +681,33 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       a.dbeta[at] = b_sum;
     }
     // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~
-#pragma unroll 1
+    auto bits = [](float x) { return __float_as_uint(x); };
+#pragma unroll 2
     for (int kk = 0; kk < DR_C; kk += 8) {
       const bool lower = kk <= rg * 16 + 15, upper = kk + 7 >= rg * 16;  // tiles of F, W and of their transposes
       uint32_t fa[4], wa[4], ft[4], wt[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p & 1) * 8, j = kk + t + (p >> 1) * 4;
-        fa[p] = tf32(Fm[i * GR_LDA + j]);
-        wa[p] = tf32(-Wm[i * GR_LDA + j]);
-        ft[p] = tf32(Fm[j * GR_LDA + i]);
-        wt[p] = tf32(-Wm[j * GR_LDA + i]);
+        fa[p] = bits(Fm[i * GR_LDA + j]);
+        wa[p] = bits(Wm[i * GR_LDA + j]);
+        ft[p] = bits(Fm[j * GR_LDA + i]);
+        wt[p] = bits(Wm[j * GR_LDA + i]);
       }
+      const float *k0 = Km + (kk + t) * LDS + ch * (DK / 2) + g, *q0 = Qm + (kk + t) * LDS + ch * (DK / 2) + g;
+      if (lower) {
 #pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        const int c = ch * (DK / 2) + n * 8 + g;
-        const uint32_t b0 = tf32(Km[(kk + t) * LDS + c]), b1 = tf32(Km[(kk + t + 4) * LDS + c]);
-        if (lower) {
+        for (int n = 0; n < NH; ++n) {
+          const uint32_t b0 = bits(k0[n * 8]), b1 = bits(k0[n * 8 + 4 * LDS]);
           mma_tf32(q[n], fa, b0, b1);
           mma_tf32(k[n], wa, b0, b1);
         }
-        if (upper) {
-          mma_tf32(k[n], wt, b0, b1);
-          const uint32_t e0 = tf32(Qm[(kk + t) * LDS + c]), e1 = tf32(Qm[(kk + t + 4) * LDS + c]);
-          mma_tf32(k[n], ft, e0, e1);
+      }
+      if (upper) {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          mma_tf32(k[n], wt, bits(k0[n * 8]), bits(k0[n * 8 + 4 * LDS]));
+          mma_tf32(k[n], ft, bits(q0[n * 8]), bits(q0[n * 8 + 4 * LDS]));
         }
       }
     }
@@ -690,22 +715,22 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
     if (hr + 1 < rep) load_tile((hr + 1) * ntiles);
   }
 
-  // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)), the dot over both column halves
-  const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
-  const float* tf = a.tok + ((int64_t)ci * a.hk + hq) * TF_N * DR_C;
-  float* dots = Fm;  // [2 halves][2][64]
+  // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)) with K16 = K~ / f_k (p_k = 0 for a zero row), the dot
+  // over both column halves; the rows leave through shared memory, 16 bytes a store
+  float* dots = part;  // [2 halves][2][64]
+  __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(Fm);
+  constexpr int LDR = DK + 8;
 #pragma unroll
   for (int isq = 0; isq < 2; ++isq)
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int row = r0 + 8 * p;
+      const float* x = (isq ? Qm : Km) + row * LDS + ch * (DK / 2) + 2 * t;
       float s = 0.f;
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
-        const int c = ch * (DK / 2) + n * 8 + 2 * t;
-        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(kq + isq * DR_C * DK * 2 +
-                                                                       img_off(row, c >> 3, DK * 2) + (c & 7) * 2));
-        s += x.x * (isq ? q[n][2 * p] : k[n][2 * p]) + x.y * (isq ? q[n][2 * p + 1] : k[n][2 * p + 1]);
+        const float2 y = *reinterpret_cast<const float2*>(x + n * 8);
+        s += y.x * (isq ? q[n][2 * p] : k[n][2 * p]) + y.y * (isq ? q[n][2 * p + 1] : k[n][2 * p + 1]);
       }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
@@ -713,26 +738,33 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
     }
   __syncthreads();
 #pragma unroll
-  for (int isq = 0; isq < 2; ++isq)
+  for (int isq = 0; isq < 2; ++isq) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int row = r0 + 8 * p;
-      if (row >= cu.len) continue;
-      const float dot = (dots[isq * DR_C + row] + dots[(2 + isq) * DR_C + row]) * tf[(isq ? TF_PQ : TF_PK) * DR_C + row];
-      const float hs = tf[(isq ? TF_HQ : TF_HK) * DR_C + row];
-      __nv_bfloat16* out =
-          (isq ? a.dQ + (int64_t)(cu.tok + row) * a.ldq : a.dK + (int64_t)(cu.tok + row) * a.ldk) + (int64_t)hq * a.dk;
+      const float f = tfs[(isq ? TF_FQ : TF_FK) * DR_C + row], hs = tfs[(isq ? TF_HQ : TF_HK) * DR_C + row];
+      const float pf = f != 0.f ? tfs[(isq ? TF_PQ : TF_PK) * DR_C + row] / f / f : 0.f;
+      const float dot = (dots[isq * DR_C + row] + dots[(2 + isq) * DR_C + row]) * pf;
+      const float* x = (isq ? Qm : Km) + row * LDS + ch * (DK / 2) + 2 * t;
+      __nv_bfloat16* out = rows + row * LDR + ch * (DK / 2) + 2 * t;
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
-        const int c = ch * (DK / 2) + n * 8 + 2 * t;
-        if (c >= a.dk) continue;
-        const float2 x = unpack_f16x2(*reinterpret_cast<const uint32_t*>(kq + isq * DR_C * DK * 2 +
-                                                                       img_off(row, c >> 3, DK * 2) + (c & 7) * 2));
-        const float y0 = hs * ((isq ? q[n][2 * p] : k[n][2 * p]) - x.x * dot);
-        const float y1 = hs * ((isq ? q[n][2 * p + 1] : k[n][2 * p + 1]) - x.y * dot);
-        *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(y0, y1);
+        const float2 y = *reinterpret_cast<const float2*>(x + n * 8);
+        *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16x2(hs * ((isq ? q[n][2 * p] : k[n][2 * p]) - y.x * dot),
+                                                                hs * ((isq ? q[n][2 * p + 1] : k[n][2 * p + 1]) - y.y * dot));
       }
     }
+    __syncthreads();
+    __nv_bfloat16* out = (isq ? a.dQ + (int64_t)cu.tok * a.ldq : a.dK + (int64_t)cu.tok * a.ldk) + (int64_t)hq * a.dk;
+    const int64_t ld = isq ? a.ldq : a.ldk;
+#pragma unroll
+    for (int i = tid; i < DR_C * (DK / 8); i += 256) {
+      const int r = i / (DK / 8), c = i % (DK / 8) * 8;
+      if (r < cu.len && c < a.dk)
+        *reinterpret_cast<uint4*>(out + r * ld + c) = *reinterpret_cast<const uint4*>(rows + r * LDR + c);
+    }
+    if (!isq) __syncthreads();
+  }
 }
 
 }  // namespace ttt
