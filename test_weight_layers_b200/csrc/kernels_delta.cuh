@@ -910,24 +910,32 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
       const float d0 = eg * inv0 * w0, d1 = eg * inv1 * w1;
       inv0 = pow2i(-f0);
       inv1 = pow2i(-f1);
+      uint32_t hi[4][4], lo[4][4];
 #pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        s[k][0] *= d0;
-        s[k][1] *= d0;
-        s[k][2] *= d1;
-        s[k][3] *= d1;
-      }
+      for (int kt = 0; kt < 4; ++kt) split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi[kt], lo[kt]);
+      // The products have accumulators of their own: the tensor cores cut off what falls below the sum, and S, which
+      // is carried over all chunks, takes the result with one rounding to nearest.
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
-        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
+      for (int np = 0; np < DK / 16; np += 2) {
+        float acc[4][4];
 #pragma unroll
-        for (int np = 0; np < DK / 16; np += 2) {
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[k][j] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
           uint32_t b[2][4];
           ldsm4t(b[0], addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
           ldsm4t(b[1], addr_bk(kb, lane, kt * 16, np * 2 + 2, DK * 2));
-          mma_f16x4(s + 2 * np, hi, b);
-          mma_f16x4(s + 2 * np, lo, b);
+          mma_f16x4(acc, lo[kt], b);
+          mma_f16x4(acc, hi[kt], b);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[2 * np + k][0] = fmaf(s[2 * np + k][0], d0, acc[k][0]);
+          s[2 * np + k][1] = fmaf(s[2 * np + k][1], d0, acc[k][1]);
+          s[2 * np + k][2] = fmaf(s[2 * np + k][2], d1, acc[k][2]);
+          s[2 * np + k][3] = fmaf(s[2 * np + k][3], d1, acc[k][3]);
         }
       }
     }

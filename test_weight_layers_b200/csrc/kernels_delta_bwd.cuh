@@ -368,17 +368,10 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
       const float d0 = eg * inv0 * w0, d1 = eg * inv1 * w1;
       inv0 = pow2i(-f0);
       inv1 = pow2i(-f1);
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        s[k][0] *= d0;
-        s[k][1] *= d0;
-        s[k][2] *= d1;
-        s[k][3] *= d1;
-      }
+      uint32_t hi[4][4], lo[4][4], ho[4][4], lp[4][4];
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4], ho[4], lp[4];
-        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
+        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi[kt], lo[kt]);
         float b[2][4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -389,20 +382,34 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
           b[q][2] = ao.x * __uint_as_float(a1 << 16);
           b[q][3] = ao.y * __uint_as_float(a1 & 0xffff0000u);
         }
-        split_a(b[0], b[1], w0, w1, ho, lp);
+        split_a(b[0], b[1], w0, w1, ho[kt], lp[kt]);
+      }
+      // (accumulators of their own, as in the state pass)
 #pragma unroll
-        for (int np = 0; np < DK / 16; ++np) {
-          uint32_t b4[4];
-          ldsm4t(b4, addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
-          mma_f16(s[2 * np], hi, b4[0], b4[1]);
-          mma_f16(s[2 * np + 1], hi, b4[2], b4[3]);
-          mma_f16(s[2 * np], lo, b4[0], b4[1]);
-          mma_f16(s[2 * np + 1], lo, b4[2], b4[3]);
-          ldsm4t(b4, addr_bk(qb, lane, kt * 16, np * 2, DK * 2));
-          mma_f16(s[2 * np], ho, b4[0], b4[1]);
-          mma_f16(s[2 * np + 1], ho, b4[2], b4[3]);
-          mma_f16(s[2 * np], lp, b4[0], b4[1]);
-          mma_f16(s[2 * np + 1], lp, b4[2], b4[3]);
+      for (int np = 0; np < DK / 16; np += 2) {
+        float acc[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[k][j] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          uint32_t b[2][4], c[2][4];
+          ldsm4t(b[0], addr_bk(kb, lane, kt * 16, np * 2, DK * 2));
+          ldsm4t(b[1], addr_bk(kb, lane, kt * 16, np * 2 + 2, DK * 2));
+          ldsm4t(c[0], addr_bk(qb, lane, kt * 16, np * 2, DK * 2));
+          ldsm4t(c[1], addr_bk(qb, lane, kt * 16, np * 2 + 2, DK * 2));
+          mma_f16x4(acc, lo[kt], b);
+          mma_f16x4(acc, lp[kt], c);
+          mma_f16x4(acc, hi[kt], b);
+          mma_f16x4(acc, ho[kt], c);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[2 * np + k][0] = fmaf(s[2 * np + k][0], d0, acc[k][0]);
+          s[2 * np + k][1] = fmaf(s[2 * np + k][1], d0, acc[k][1]);
+          s[2 * np + k][2] = fmaf(s[2 * np + k][2], d1, acc[k][2]);
+          s[2 * np + k][3] = fmaf(s[2 * np + k][3], d1, acc[k][3]);
         }
       }
     }
