@@ -539,10 +539,28 @@ template <bool BACK>
 constexpr int state_warp_smem() {
   return (BACK ? 4 : 2) * DR_VTILE;
 }
+// Outputs of their own warps (dk <= 192, where shared memory holds the hand-over): per warp S's and U's leading
+// parts as A fragments, their row scales, and a tile for O.
+template <int DK, int PASS>
+constexpr bool state_split() {
+  return PASS == PASS_OUT && DK <= 192;
+}
+template <int DK>
+constexpr int state_hand() {
+  return DK / 16 * 512 + 4 * 512 + 2 * 256 + DR_VTILE;
+}
 constexpr int DR_ETILE = 16 * DR_C * 4;  // a warp's E rows (reverse pass)
 template <int DK, bool BACK>
 constexpr int state_smem(int warps, bool etile = false) {
   return 2 * state_stage<DK, BACK>() + warps * (state_warp_smem<BACK>() + (etile ? DR_ETILE : 0)) + 64;
+}
+template <int DK>
+constexpr int state_out_smem(int warps) {
+  return state_smem<DK, false>(warps) + (state_split<DK, PASS_OUT>() ? warps * (state_hand<DK>() + 32) : 0);
+}
+template <int DK, int PASS>
+constexpr int state_threads() {  // at most four warps of rows, and as many for their outputs or one that copies
+  return state_split<DK, PASS>() ? 256 : 160;  // (a ninth warp would leave 168 registers)
 }
 
 // A warp's 64 x 16 tile of token rows `p` (first channel v0 of head h), zero outside the sequence and the head.
@@ -574,6 +592,27 @@ __device__ __forceinline__ uint32_t vtile_addr(uint32_t base, int lane, int n0) 
   return base + vtile_off(n0 + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
 }
 
+// O's tile in the accumulator layout, o (Q S^T at scales is) and x (P U at scales iu), to the rows of a tile.
+__device__ __forceinline__ void store_o(const float (&o)[8][4], const float (&x)[8][4], float is0, float is1, float iu0,
+                                        float iu1, const float* vec, uint32_t tile, int lane) {
+  const int t = lane & 3;
+#pragma unroll
+  for (int np = 0; np < 4; ++np) {
+    uint32_t y[4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int k = 2 * np + q, col = k * 8 + 2 * t;
+      const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
+      const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
+      y[2 * q] = pack_bf16x2(ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * iu0),
+                             ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * iu0));
+      y[2 * q + 1] = pack_bf16x2(ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * iu1),
+                                 ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * iu1));
+    }
+    stsm4t(vtile_addr(tile, lane, np * 16), y[0], y[1], y[2], y[3]);
+  }
+}
+
 // A warp's 16 rows of dk floats, rows scaled back, to `out`; `rows` of them exist.
 template <int NT>
 __device__ __forceinline__ void store_rows(float* out, const float (&s)[NT][4], float i0, float i1, int rows, int dk,
@@ -594,19 +633,28 @@ __device__ __forceinline__ void store_rows(float* out, const float (&s)[NT][4], 
 __device__ __forceinline__ int etile_col(int row, int col) { return (((col >> 1) ^ ((row & 7) << 2)) << 1) | (col & 1); }
 
 template <int DK, int PASS>
-__global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
+__global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(const StateArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr bool BACK = PASS == PASS_BACK, SCAN = PASS == PASS_SCAN;
+  constexpr bool BACK = PASS == PASS_BACK, SCAN = PASS == PASS_SCAN, SPLIT = state_split<DK, PASS>();
   constexpr int STAGE = state_stage<DK, BACK>();
   constexpr int KQ = 2 * DR_C * DK * 2;
   constexpr int HB = STAGE - KQ;
   constexpr int WSM = state_warp_smem<BACK>();
   constexpr int NT = DK / 8;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = (blockDim.x >> 5) - 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int nwarp = SPLIT ? blockDim.x >> 6 : (blockDim.x >> 5) - 1;  // warps that own rows
+  const bool outer = SPLIT && tid >> 5 >= nwarp;
+  const int warp = outer ? (tid >> 5) - nwarp : tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);  // [2] stage and tiles have landed
   uint64_t* empty = full + 2;                                                    // [2] every warp has read them
+  // hand-over from a row warp to its output warp: S parts written, read, U parts written, read
+  uint64_t* hand = empty + 2 + 4 * warp;
+  uint8_t* hbuf = smem + state_smem<DK, false>(nwarp) + nwarp * 32 + warp * state_hand<DK>();
+  uint4 *h_s = reinterpret_cast<uint4*>(hbuf), *h_u = h_s + DK / 16 * 32;
+  float2 *h_ss = reinterpret_cast<float2*>(h_u + 4 * 32), *h_us = h_ss + 32;
+  uint8_t* obuf = reinterpret_cast<uint8_t*>(h_us + 32);
   const int nblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
   const int vblocks = nblocks + (SCAN ? (DK + nwarp * 16 - 1) / (nwarp * 16) : 0);
   const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
@@ -617,9 +665,11 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
   const int dv_in = phi ? 0 : a.dv;  // the transition's rows take no values
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 33);  // the bulk copies, and each lane's tile copies
-      mbar_init(&empty[i], nwarp);
+      mbar_init(&full[i], 1 + 32 * (SPLIT ? nwarp : 1));  // the bulk copies, and each copying lane's tile copies
+      mbar_init(&empty[i], nwarp * (SPLIT ? 2 : 1));
     }
+    if (SPLIT)
+      for (int i = 0; i < 4 * nwarp; ++i) mbar_init(&empty[2 + i], 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -631,36 +681,104 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
   if (SCAN && (sq.seg == sq.nseg - 1 || (phi && sq.seg == 0))) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
-  if (warp == nwarp) {  // the last warp brings the chunks, two ahead at most
+  auto load_stage = [&](int n) {  // one thread: the chunk's shared operands
+    uint64_t* bar = &full[n & 1];
+    const int64_t ci = sq.chunk0 + n;
+    uint8_t* st = smem + (n & 1) * STAGE;
+    const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
+    const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
+    if constexpr (SCAN) {  // without Q16 and P
+      mbar_expect_tx(bar, KQ / 2 + HB - DR_TILE);
+      bulk_load(st, kq, KQ / 2, bar);
+      bulk_load(st + KQ, blk, 2 * DR_TILE, bar);
+      bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, bar);
+    } else {
+      mbar_expect_tx(bar, KQ + HB);
+      bulk_load(st, kq, KQ, bar);
+      bulk_load(st + KQ, blk, HB, bar);
+    }
+  };
+  auto load_tiles = [&](int n, int w) {  // one warp: row warp w's tiles
+    const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + (n & 1) * DR_VTILE);
+    load_vtile(dst, a.V, a.ldv, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
+    if constexpr (BACK) load_vtile(dst + 2 * DR_VTILE, a.dO, a.ldo, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
+  };
+  if (!SPLIT && warp == nwarp) {  // the last warp brings the chunks, two ahead at most
 #pragma unroll 1
     for (int n = 0; n < nchunk; ++n) {
-      uint64_t* bar = &full[n & 1];
       if (n >= 2) mbar_wait(&empty[n & 1], ((n >> 1) - 1) & 1, a.guard);
-      if (lane == 0) {
-        const int64_t ci = sq.chunk0 + n;
-        uint8_t* st = smem + (n & 1) * STAGE;
-        const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
-        const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
-        if constexpr (SCAN) {  // without Q16 and P
-          mbar_expect_tx(bar, KQ / 2 + HB - DR_TILE);
-          bulk_load(st, kq, KQ / 2, bar);
-          bulk_load(st + KQ, blk, 2 * DR_TILE, bar);
-          bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, bar);
-        } else {
-          mbar_expect_tx(bar, KQ + HB);
-          bulk_load(st, kq, KQ, bar);
-          bulk_load(st + KQ, blk, HB, bar);
-        }
-      }
-      for (int w = 0; w < nwarp; ++w) {
-        const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + (n & 1) * DR_VTILE);
-        load_vtile(dst, a.V, a.ldv, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
-        if constexpr (BACK)
-          load_vtile(dst + 2 * DR_VTILE, a.dO, a.ldo, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
-      }
-      cp_arrive(bar);
+      if (lane == 0) load_stage(n);
+      for (int w = 0; w < nwarp; ++w) load_tiles(n, w);
+      cp_arrive(&full[n & 1]);
     }
     return;
+  }
+
+  if constexpr (SPLIT) {
+    if (outer) {
+      // O = e^c Q S^T + P U from the row warp's leading parts (2^-12, enough for a bf16 output), beside its chain;
+      // and the next chunk's copies, once every warp is done with the stage
+      auto copy = [&](int n) {
+        if (warp == 0 && lane == 0) load_stage(n);
+        load_tiles(n, warp);
+        cp_arrive(&full[n & 1]);
+      };
+      if (nchunk > 0) copy(0);
+#pragma unroll 1
+      for (int n = 0; n < nchunk; ++n) {
+        if (n + 1 < nchunk) {
+          if (n > 0) mbar_wait(&empty[(n + 1) & 1], ((n - 1) >> 1) & 1, a.guard);
+          copy(n + 1);
+        }
+        mbar_wait(&full[n & 1], (n >> 1) & 1, a.guard);
+        const uint32_t st = smem_u32(smem + (n & 1) * STAGE);
+        const uint32_t qb = st + DR_C * DK * 2, pb = st + KQ + 2 * DR_TILE;
+        const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + KQ + 3 * DR_TILE);
+        float o[8][4], x[8][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[k][j] = x[k][j] = 0.f;
+        mbar_wait(&hand[0], n & 1, a.guard);
+        const float2 is = h_ss[lane];
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt) {
+          const uint4 v = h_s[kt * 32 + lane];
+          const uint32_t hi[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int np = 0; np < 4; np += 2) {
+            uint32_t c[2][4];
+            ldsm4(c[0], addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
+            ldsm4(c[1], addr_bn(qb, lane, np * 16 + 16, kt * 2, DK * 2));
+            mma_f16x4(o + 2 * np, hi, c);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hand[1]);
+        mbar_wait(&hand[2], n & 1, a.guard);
+        const float2 iu = h_us[lane];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const uint4 v = h_u[kt * 32 + lane];
+          const uint32_t hi[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int np = kt; np < 4; ++np) {
+            uint32_t p[4];
+            ldsm4(p, addr_bn(pb, lane, np * 16, kt * 2, 128));
+            mma_f16(x[2 * np], hi, p[0], p[1]);
+            mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hand[3]);
+        store_o(o, x, is.x, is.y, iu.x, iu.y, vec, smem_u32(obuf), lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[n & 1]);
+        store_vtile(obuf, a.O, a.ldo, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
+        __syncwarp();  // the tile is read
+      }
+      return;
+    }
   }
 
   float s[NT][4];
@@ -710,17 +828,19 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
     for (int k = 0; k < 8; ++k)
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[k][j] = o[k][j] = 0.f;
+    if (SPLIT && n > 0) mbar_wait(&hand[1], (n - 1) & 1, a.guard);  // the output warp has read the S before
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt) {
       uint32_t hi[4], lo[4];
       split_a(s[2 * kt], s[2 * kt + 1], sc0, sc1, hi, lo);
+      if constexpr (SPLIT) h_s[kt * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
       for (int np = 0; np < 4; np += 2) {
         uint32_t b[2][4], c[2][4];
         ldsm4(b[0], addr_bn(kb, lane, np * 16, kt * 2, DK * 2));
         ldsm4(b[1], addr_bn(kb, lane, np * 16 + 16, kt * 2, DK * 2));
         mma_f16x4(r + 2 * np, hi, b);
-        if constexpr (!SCAN) {
+        if constexpr (!SCAN && !SPLIT) {
           // the outputs are rounded to bf16: S's hi part alone (2^-12) is enough for them
           ldsm4(c[0], addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
           ldsm4(c[1], addr_bn(qb, lane, np * 16 + 16, kt * 2, DK * 2));
@@ -732,6 +852,11 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
     }
     // R = V - e^c K S^T, then the scale of beta R
     const float is0 = inv0 * pow2i(-e0), is1 = inv1 * pow2i(-e1);
+    if constexpr (SPLIT) {
+      h_ss[lane] = make_float2(is0, is1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hand[0]);
+    }
     m0 = m1 = 0.f;
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
@@ -808,8 +933,28 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
         r[k][3] *= be.y;
       }
     }
+    if constexpr (SPLIT) {  // U's leading parts for the output warp
+      m0 = m1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m0 = max_abs2(m0, r[k][0], r[k][1]);
+        m1 = max_abs2(m1, r[k][2], r[k][3]);
+      }
+      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+      const float w0 = pow2i(f0), w1 = pow2i(f1);
+      if (n > 0) mbar_wait(&hand[3], (n - 1) & 1, a.guard);
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt)
+        h_u[kt * 32 + lane] = make_uint4(pack_f16x2(r[2 * kt][0] * w0, r[2 * kt][1] * w0),
+                                         pack_f16x2(r[2 * kt][2] * w1, r[2 * kt][3] * w1),
+                                         pack_f16x2(r[2 * kt + 1][0] * w0, r[2 * kt + 1][1] * w0),
+                                         pack_f16x2(r[2 * kt + 1][2] * w1, r[2 * kt + 1][3] * w1));
+      h_us[lane] = make_float2(pow2i(-f0), pow2i(-f1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hand[2]);
+    }
     // O = e^c Q S^T + P U, accumulated in U's scale over P's row scales
-    if constexpr (!SCAN) {
+    if constexpr (!SCAN && !SPLIT) {
       m0 = m1 = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -870,21 +1015,7 @@ __global__ void __launch_bounds__(160, 1) k_delta_state(const StateArgs a) {
         }
       } else {
         __syncwarp();  // every lane has read its V tile; O takes its place
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t y[4];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int k = 2 * np + q, col = k * 8 + 2 * t;
-            const float2 ao = *reinterpret_cast<const float2*>(vec + DV_AO * DR_C + col);
-            const float2 ps = *reinterpret_cast<const float2*>(vec + DV_PS * DR_C + col);
-            y[2 * q] = pack_bf16x2(ao.x * (o[k][0] * is0) + ps.x * (x[k][0] * i0),
-                                   ao.y * (o[k][1] * is0) + ps.y * (x[k][1] * i0));
-            y[2 * q + 1] = pack_bf16x2(ao.x * (o[k][2] * is1) + ps.x * (x[k][2] * i1),
-                                       ao.y * (o[k][3] * is1) + ps.y * (x[k][3] * i1));
-          }
-          stsm4t(vtile_addr(vb, lane, np * 16), y[0], y[1], y[2], y[3]);
-        }
+        store_o(o, x, is0, is1, i0, i1, vec, vb, lane);
         __syncwarp();
         store_vtile(vbuf + (n & 1) * DR_VTILE, a.O, a.ldo, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
       }

@@ -203,8 +203,9 @@ int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream
   TTT_TRY((launch_prep<DK, false>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
   const int warps = pass_warps_for(pass_warps<DK>(false), sa.dv);
-  return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps), warps + 1,
-                                                  state_smem<DK, false>(warps), s);
+  return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps),
+                                                  state_split<DK, PASS_OUT>() ? 2 * warps : warps + 1,
+                                                  state_out_smem<DK>(warps), s);
 }
 
 template <int DK>
