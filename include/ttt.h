@@ -288,17 +288,22 @@ int ttt_layer_host(ttt_weights W, const void* hQ, const void* hK, const void* hV
  *    is a multiple of heads_qk.  Q, K: [T][ld] with head h in columns [h*dk,
  *    (h+1)*dk); V, O: head h in columns [h*dv, (h+1)*dv); the ld_* of
  *    ttt_io_cfg, 0 meaning heads*d.
- *  - g (log decay, usually <= 0; g > 0 grows the state and is allowed while
- *    exp of its sums stays finite), beta: float [T][heads_v], contiguous.
+ *  - g (log decay, usually <= 0; -inf forgets the state; g > 0 grows it and is
+ *    allowed while exp of its sums stays finite), beta: float [T][heads_v],
+ *    contiguous.
  *  - States are float [..][heads_v][dv][dk], contiguous; they are never rounded
  *    to fewer bits.
  *  - dk, dv multiples of 8, dk <= 256, dv <= 1024; heads_v <= 4096; other
  *    shapes return TTT_ERR_UNSUPPORTED.  Token rows and pointers are 16-byte
  *    aligned (TTT_ERR_ALIGN), g and beta 4-byte.
- *  - A non-finite token, gate or state makes undefined the outputs of its chunk
+ *  - The L2 norms of single tokens (ttt_delta_step, TTT_FP32) are summed in fp32:
+ *    rows of norm above 1.8e19 count as zero there.  The chunked bf16 form scales
+ *    each row first and takes any finite one.
+ *  - A non-finite token, gate (other than g = -inf) or state makes undefined the outputs of its chunk
  *    of 64 tokens (earlier tokens of that chunk too) and of all later tokens of
  *    its sequence and head; other sequences are not touched by it.
- *  - Outputs may not overlap inputs or each other, except S with S0. */
+ *  - Outputs may not overlap inputs or each other, except that S may be S0.
+ *  - All buffers are on the current device. */
 typedef struct { int heads_qk, heads_v, dk, dv; } ttt_delta_dims;
 
 /* Workspace bytes for ttt_delta_chunked (backward = 0) or both it and

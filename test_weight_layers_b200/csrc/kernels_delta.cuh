@@ -181,7 +181,7 @@ __device__ __forceinline__ void store_half_row(const float* p, int i, int half, 
 // forward substitution, a thread to a column; then, by their distance from the diagonal,
 //     Y_ij = T + Y_ii beta_i T,   T = -L_ij - sum_{j <= k < i} L_ik beta_k Y_kj
 // since (I + L_ii beta_i)^-1 = I + Y_ii beta_i.  Substitution over all 64 rows at once is a chain four times
-// as long that only half of the threads share: 8.8 us a block against 1.6 us.
+// as long that only half of the threads share: 16,700 cycles a block against 6,700.
 __device__ __forceinline__ void solve_y(const float* Lm, float* Ym, const float* bet, int tid) {
   if (tid < DR_C) {
     const int b0 = tid & ~15, cc = tid & 15;
@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
     uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * a.blk_bytes;
     float* vec = reinterpret_cast<float*>(blk + 3 * DR_TILE);
     // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
-    double s = (double)g_next;
+    // exp of less than -110 is zero in fp32: lower values (-inf: a reset) are taken as that, so that the sums of the
+    // tokens behind them keep their digits
+    double s = g_next < -110.f ? -110.0 : (double)g_next;
     const float b_now = b_next;
     if (tid < ch.len && hr + 1 < rep) {
       g_next = __ldg(a.g + gate0 + hr + 1);
@@ -783,8 +785,11 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
 
   float s[NT][4];
   const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
-  // a first segment starts from S0; the others from the join's state, or in the scan from zero or the unit matrix
-  const float* from = sq.seg == 0 ? (a.S0 ? a.S0 + srow * a.dk : nullptr) : SCAN ? nullptr : a.seg_s + grow * a.dk;
+  // a first segment starts from S0 (which the scan keeps: S may be S0, and a last segment may end before the first one
+  // starts), the others from the join's state, or in the scan from zero or the unit matrix
+  const float* from = sq.nseg > 1 && !SCAN ? a.seg_s + grow * a.dk
+                      : sq.seg == 0        ? (a.S0 ? a.S0 + srow * a.dk : nullptr)
+                                           : nullptr;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -800,6 +805,7 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
       s[n][2 * p + 1] = x.y;
     }
   float inv0 = 1.f, inv1 = 1.f;  // S = s * inv: rows g and g + 8 carry a power of two
+  if (SCAN && sq.seg == 0) store_rows<NT>(a.seg_s + (grow + v0) * a.dk, s, 1.f, 1.f, a.dv - v0, a.dk, lane);
 
 #pragma unroll 1
   for (int n = 0; n < nchunk; ++n) {

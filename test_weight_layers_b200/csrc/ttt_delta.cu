@@ -28,6 +28,8 @@ struct DeltaWs {
   size_t total;
 };
 
+constexpr int kDeltaMaxSeqs = 1 << 24;
+
 int dk_pad(int dk) { return (dk + 63) / 64 * 64; }
 
 bool delta_dims_ok(const ttt_delta_dims& d) {
@@ -44,8 +46,9 @@ int64_t pass_blocks(const ttt_delta_dims& d) { return (int64_t)d.heads_v * ((d.d
 // Segments.  Uncut, the passes have n_seq * pass_blocks blocks, each on its own SM for the length of a sequence.
 // Cut into k segments a sequence costs 2.6 times the products on k times the blocks, and a chain of k joins, so it is
 // cut where at least 3 segments fit on the card's 148 SMs and the sequences are long enough: 131,072 tokens, 4 heads
-// of 192: 10.1 ms uncut, 2.4 ms in 12 segments; 1,374 tokens: 117 us and 66 us.  Eight sequences of 16 heads leave
-// no SM idle and stay whole.  The length that goes into the rule is the mean one; the device cuts each by its own.
+// of 192: the passes take 10.1 ms uncut, 2.1 ms in 12 segments; 1,374 tokens: 117 us, and 78 us in 6.  Eight sequences
+// of 16 heads leave no SM idle and stay whole.  The length that goes into the rule is the mean one; the device cuts
+// each sequence by its own.
 constexpr int kDeltaSms = 148;
 int seg_chunks(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
   if (dt != TTT_BF16 || n_seq < 1) return 0;
@@ -152,10 +155,10 @@ int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaS
   return TTT_OK;
 }
 
-// Warps of a pass block (16 value channels each): four, one to a sub-partition of the SM.  A warp's chain of products
-// is bound by its own latency, so eight share an SM at 0.6 of the speed each (packed prompts of 16 heads: 435 us
-// with 8, 260 with 4, 353 with 2, which share a staged copy of the operands with fewer); two where shared memory
-// holds no more (dk = 256 on the way back).
+// Row warps of a pass block (16 value channels each): four, one to a sub-partition of the SM.  A warp's chain of
+// products is bound by its own latency, so eight on an SM run at 0.6 of the speed each (state pass of packed prompts
+// of 16 heads: 435 us with 8, 260 with 4; with 2, which share a staged copy of the operands with fewer, 353); two where
+// shared memory holds no more (dk = 256 on the way back).
 template <int DK>
 constexpr int pass_warps(bool back) {
   return back && DK > 192 ? 2 : 4;
@@ -342,7 +345,7 @@ StateArgs state_args(const void* V, const float* S0, const ttt_delta_dims& d, co
 int delta_check_call(const ttt_delta_dims& d, ttt_dtype dt, int64_t T, int n_seq, bool packed, const ttt_io_cfg* io,
                      bool backward, void* ws, size_t ws_bytes) {
   if ((dt != TTT_FP32 && dt != TTT_BF16) || !delta_dims_ok(d) || T < 0 || n_seq < 0 || !io) return TTT_ERR_INVALID;
-  if (!delta_dims_supported(d) || T > INT32_MAX - DR_C) return TTT_ERR_UNSUPPORTED;
+  if (!delta_dims_supported(d) || T > INT32_MAX - DR_C || n_seq > kDeltaMaxSeqs) return TTT_ERR_UNSUPPORTED;
   if (n_seq == 0 ? T > 0 && !packed : !packed && T % n_seq) return TTT_ERR_INVALID;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return TTT_ERR_WORKSPACE;
   return ws_bytes < delta_carve(nullptr, d, T, n_seq, dt, backward).total ? TTT_ERR_WORKSPACE : TTT_OK;
@@ -354,7 +357,7 @@ extern "C" {
 
 size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_dtype dtype, int backward) {
   if ((dtype != TTT_FP32 && dtype != TTT_BF16) || !delta_dims_ok(dims) || !delta_dims_supported(dims) || T < 0 ||
-      T > INT32_MAX - DR_C || n_seq < 0)
+      T > INT32_MAX - DR_C || n_seq < 0 || n_seq > kDeltaMaxSeqs)
     return 0;
   return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0).total;
 }
@@ -402,6 +405,7 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
   for (const void* p : {(const void*)S0, (const void*)dS, (const void*)dS0})
     if (!aligned16(p)) return TTT_ERR_ALIGN;
   if (!aligned4(cu_seqlens) || !aligned4(dg) || !aligned4(dbeta)) return TTT_ERR_ALIGN;
+  if (dS0 && (dS0 == dS || dS0 == S0)) return TTT_ERR_INVALID;
   if (any) {
     TTT_TRY(check_rows(dQ, x.ldq, (int64_t)dims.heads_qk * dims.dk, dtype));
     TTT_TRY(check_rows(dK, x.ldk, (int64_t)dims.heads_qk * dims.dk, dtype));

@@ -62,6 +62,10 @@ def test_delta_arguments(lib):
     assert _fwd(lib, cu=None, n_seq=3) == INV                 # 256 tokens in 3 equal sequences
     assert _fwd(lib, cu=None, n_seq=0) == INV
     assert _fwd(lib, n_seq=0, T_=256) == OK                   # offsets of no sequence: nothing to do
+    assert _fwd(lib, n_seq=(1 << 24) + 1) == UNS
+    assert lib.ttt_delta_chunked_backward(*FAKE[:5], None, FAKE[5], FAKE[6], FAKE[8], FAKE[12], FAKE[13], FAKE[9],
+                                          FAKE[14], FAKE[6], FAKE[10], 2, 256, 1.0, T.delta_dims(2, 4, 128, 64),
+                                          ctypes.byref(T.io_cfg()), T.TTT_BF16, FAKE[11], 1 << 40, None) == INV  # dS0 = dS
     assert _bwd(lib, dQ=None) == INV and _bwd(lib, dg=None) == INV and _bwd(lib, dQ=FAKE[0]) == INV
     assert _step(lib, slots=None, B_=9) == INV                # more rows than slots
     assert _step(lib, S=None) == INV and _step(lib, O=FAKE[0]) == INV and _step(lib, B_=-1) == INV

@@ -219,6 +219,57 @@ def test_large_state_with_small_writes():
     c.check_forward(*c.forward()[:2])
 
 
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min, -1e6])
+def test_gates_that_forget(low):
+    # a reset inside a chunk, at its border, twice in a row; the tokens behind it keep their own decays
+    c = Seqs([200, 70], 1, 2, 64, 64, seed=25)
+    for t in (0, 10, 11, 63, 64, 130, 205):
+        c.g[t] = low
+    c.check_forward(*c.forward()[:2])
+    out, _ = c.backward()
+    c.check_backward(out)
+    pool, O = c.S0.clone(), torch.zeros((2, 128), dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 205], device="cuda")
+    d = Seqs([1, 1], 1, 2, 64, 64, seed=25)
+    d.Q, d.K, d.V, d.g, d.beta = (t[rows].contiguous() for t in (c.Q, c.K, c.V, c.g, c.beta))
+    d.S0 = c.S0
+    T.ttt_delta_step(d.Q, d.K, d.V, d.g, d.beta, pool, O, 2, d.dm, d.io, scale=d.scale)
+    d.check_forward(O, pool)
+
+
+def test_long_sequence_in_place():
+    # cut into segments: the last one may end before the first has read the state that it overwrites
+    c = Seqs([20000], 1, 1, 64, 64, seed=26)
+    O, S, _ = c.forward()
+    state = c.S0.clone()
+    O2, _, ws = c.forward(S=state, S0=state)
+    assert T.ttt_poll_status(ws) == T.TTT_OK
+    assert torch.equal(O, O2) and torch.equal(S, state)
+
+
+def test_gradients_of_zero_and_tiny_rows():
+    # x / max(||x||, 1e-12): a zero row passes 1e12 times the gradient, a tiny one 1 / ||x|| times its part across x
+    c = Seqs([80], 1, 1, 64, 64, seed=27)
+    c.K[5] = 0
+    c.Q[70] = 0
+    c.K[40] = (c.K[40].float() * 1e-9).bfloat16()
+    out, _ = c.backward()
+    at, args = c._seq(0)
+    ref = D.delta_rule_grad(*args, f64(c.dO), f64(c.dS[0]), 1, 1, c.scale)
+    for k, tol in (("dq", TOL_QK), ("dk", TOL_QK)):
+        for rows in ([5], [40], [70], [i for i in range(80) if i not in (5, 40, 70)]):
+            assert rel_fro(f64(out[k][rows]), ref[k][rows]) < tol, (k, rows)
+    assert rel_fro(f64(out["dg"]), ref["dg"]) < TOL_G and rel_fro(f64(out["dbeta"]), ref["dbeta"]) < TOL_G
+
+
+def test_many_sequences():
+    # more than the chunk table sorts, lengths of 0 to 3
+    lens = [i % 4 for i in range(1500)]
+    c = Seqs(lens, 1, 1, 64, 64, seed=28)
+    c.check_forward(*c.forward()[:2])
+    c.check_backward(c.backward()[0])
+
+
 def test_growing_gate():
     c = Seqs([100], 1, 1, 64, 64, seed=8)
     c.g = c.g.abs() * 0.3
