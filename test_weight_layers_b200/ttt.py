@@ -271,7 +271,7 @@ def ttt_layer_host(W: Weights, hQ, hK, hV, hEta, hO, T, chunk, order, steps, ns:
 
 def _queue(stream, *tensors):
     """The stream to queue on, after checking that all given tensors are on the current CUDA device."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
@@ -284,12 +284,16 @@ def _at(t):
 
 def _rows(name, t, rows, width, ld, dtype):
     """A token matrix of at least `rows` rows of `width` columns, stored with row stride ld (0: width)."""
-    size, step = t.shape, t.stride()
-    if (t.dtype is dtype and len(size) == 2 and size[0] >= rows and size[1] >= width and (step[1] == 1 or width == 1)
-            and (step[0] == (ld or width) or rows < 2)):
-        return
+    if t.dtype is dtype:
+        size = t.shape
+        if size == (rows, width) and (not ld or ld == width) and t.is_contiguous():
+            return
+        step = t.stride()
+        if (len(size) == 2 and size[0] >= rows and size[1] >= width and (step[1] == 1 or width == 1)
+                and (step[0] == (ld or width) or rows < 2)):
+            return
     raise ValueError(f"{name} must be {dtype} [{rows}][{width}] with strides ({ld or width}, 1), got {t.dtype} "
-                     f"{list(size)} with strides {step}")
+                     f"{list(t.shape)} with strides {t.stride()}")
 
 
 def _dense(name, t, shape, dtype=torch.float32):
@@ -387,13 +391,15 @@ def norm_workspace(T: int, cfg: NormCfg, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _norm_check(T, cfg, dtype, rows, weights):
-    for name, t, ld in rows:
+def _norm_check(T, cfg, dtype, names, rows, lds, weights):
+    """`rows` (token matrices) have the strides `lds`; `weights` are [group], [D], [D] and again so."""
+    D = cfg.D
+    for i, t in enumerate(rows):
         if t is not None:
-            _rows(name, t, T, cfg.D, ld, dtype)
-    for name, t, n in weights:
+            _rows(names[i], t, T, D, lds[i], dtype)
+    for i, t in enumerate(weights):
         if t is not None:
-            _dense(name, t, (n,))
+            _dense(names[len(rows) + i], t, (D if i % 3 else cfg.group,))
 
 
 def ttt_block_norm(Y, Xout, T, cfg: NormCfg, X=None, Z=None, w_post=None, res_scale=None, w_pre=None, N=None,
@@ -401,9 +407,8 @@ def ttt_block_norm(Y, Xout, T, cfg: NormCfg, X=None, Z=None, w_post=None, res_sc
     """Xout = X + res_scale * RMSNorm(Y) * w_post * SiLU(Z) and N = RMSNorm(Xout) * w_pre per row (either output may
     be None)."""
     queue = _queue(stream, Y, Xout, X, Z, w_post, res_scale, w_pre, N)
-    _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
-                                  ("Xout", Xout, cfg.ld_xout), ("N", N, cfg.ld_n)),
-                (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D)))
+    _norm_check(T, cfg, Y.dtype, ("X", "Y", "Z", "Xout", "N", "w_post", "res_scale", "w_pre"), (X, Y, Z, Xout, N),
+                (cfg.ld_x, cfg.ld_y, cfg.ld_z, cfg.ld_xout, cfg.ld_n), (w_post, res_scale, w_pre))
     _check("ttt_block_norm", lib().ttt_block_norm(
         _at(X), _at(Y), _at(Z), _at(w_post), _at(res_scale), _at(w_pre), _at(Xout), _at(N), T,
         ctypes.byref(cfg), dtype_code(Y.dtype), queue))
@@ -413,11 +418,10 @@ def ttt_block_norm_backward(Y, dXout, dY, T, cfg: NormCfg, ws, X=None, Z=None, w
                             dN=None, dX=None, dZ=None, dw_post=None, dres_scale=None, dw_pre=None, stream=None):
     """The gradient of ttt_block_norm from dXout and dN (None: zero); outputs that are None are not written."""
     queue = _queue(stream, Y, dXout, dY, ws, X, Z, w_post, res_scale, w_pre, dN, dX, dZ, dw_post, dres_scale, dw_pre)
-    _norm_check(T, cfg, Y.dtype, (("X", X, cfg.ld_x), ("Y", Y, cfg.ld_y), ("Z", Z, cfg.ld_z),
-                                  ("dXout", dXout, cfg.ld_xout), ("dN", dN, cfg.ld_n), ("dX", dX, cfg.ld_x),
-                                  ("dY", dY, cfg.ld_y), ("dZ", dZ, cfg.ld_z)),
-                (("w_post", w_post, cfg.group), ("res_scale", res_scale, cfg.D), ("w_pre", w_pre, cfg.D),
-                 ("dw_post", dw_post, cfg.group), ("dres_scale", dres_scale, cfg.D), ("dw_pre", dw_pre, cfg.D)))
+    _norm_check(T, cfg, Y.dtype, ("X", "Y", "Z", "dXout", "dN", "dX", "dY", "dZ", "w_post", "res_scale", "w_pre",
+                                  "dw_post", "dres_scale", "dw_pre"), (X, Y, Z, dXout, dN, dX, dY, dZ),
+                (cfg.ld_x, cfg.ld_y, cfg.ld_z, cfg.ld_xout, cfg.ld_n, cfg.ld_x, cfg.ld_y, cfg.ld_z),
+                (w_post, res_scale, w_pre, dw_post, dres_scale, dw_pre))
     _check("ttt_block_norm_backward", lib().ttt_block_norm_backward(
         _at(X), _at(Y), _at(Z), _at(w_post), _at(res_scale), _at(w_pre), _at(dXout), _at(dN), _at(dX),
         _at(dY), _at(dZ), _at(dw_post), _at(dres_scale), _at(dw_pre), T, ctypes.byref(cfg), dtype_code(Y.dtype),
