@@ -296,9 +296,9 @@ int ttt_layer_host(ttt_weights W, const void* hQ, const void* hK, const void* hV
  *  - dk, dv multiples of 8, dk <= 256, dv <= 1024; heads_v <= 4096; other
  *    shapes return TTT_ERR_UNSUPPORTED.  Token rows and pointers are 16-byte
  *    aligned (TTT_ERR_ALIGN), g and beta 4-byte.
- *  - The L2 norms of single tokens (ttt_delta_step, TTT_FP32) are summed in fp32:
- *    rows of norm above 1.8e19 count as zero there.  The chunked bf16 form scales
- *    each row first and takes any finite one.
+ *  - Token by token (ttt_delta_step, TTT_FP32, bf16 calls of up to 40 tokens) the
+ *    L2 norms are summed in fp32: rows of norm above 1.8e19 count as zero there.
+ *    The chunked bf16 form scales each row first and takes any finite one.
  *  - A non-finite token, gate (other than g = -inf) or state makes undefined the outputs of its chunk
  *    of 64 tokens (earlier tokens of that chunk too) and of all later tokens of
  *    its sequence and head; other sequences are not touched by it.
@@ -325,8 +325,9 @@ size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_
  *    S: state after each (a sequence of length 0 keeps S0), may be S0 itself
  *    or NULL.  Passing S as the next call's S0 resumes the sequences.
  *  - TTT_BF16: bf16 Q, K, V, O on the tensor cores, with fp32-precise products
- *    (operands split in two fp16 parts); TTT_FP32: float Q, K, V, O, token by
- *    token on the CUDA cores (the precision check, and short sequences).
+ *    (operands split in two fp16 parts; calls of up to 40 tokens on the CUDA
+ *    cores); TTT_FP32: float Q, K, V, O, token by token on the CUDA cores (the
+ *    precision check, and short sequences).
  *  - T up to 2^31 - 1. */
 int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
                       float* S, void* O, const int32_t* cu_seqlens, int n_seq, int64_t T, float scale,

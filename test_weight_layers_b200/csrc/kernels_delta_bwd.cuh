@@ -536,35 +536,47 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   const int r0 = rg * 16 + g;
 
   load_tile(0);
-  for (int i = tid; i < TF_N * DR_C; i += 256) tfs[i] = a.tok[((int64_t)ci * a.hk + hq) * TF_N * DR_C + i];
+  float tf_in[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (tid + i * 256 < TF_N * DR_C) tf_in[i] = a.tok[((int64_t)ci * a.hk + hq) * TF_N * DR_C + tid + i * 256];
 #pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
     const int64_t blk = (int64_t)ci * a.hv + h;
     const float* vec = reinterpret_cast<const float*>(a.blk + blk * a.blk_bytes + 3 * DR_TILE);
-    // the gates' sums of the two passes: a quarter of the channel slices to each 64 threads
-    {
-      const int tok = tid & (DR_C - 1), grp = tid >> 6;
-      float w = 0.f, b = 0.f;
-#pragma unroll 4
-      for (int p = grp; p < n16; p += 4) {
-        w += a.w_part[(blk * n16 + p) * DR_C + tok];
-        b += a.b_part[(blk * n16 + p) * DR_C + tok];
-      }
-      part[grp * DR_C + tok] = w;
-      part[(4 + grp) * DR_C + tok] = b;
+    // the gates' sums of the two passes (a quarter of the channel slices to each 64 threads) and the head's vectors:
+    // every load is issued before the first is waited for
+    const int tok = tid & (DR_C - 1), grp = tid >> 6;
+    float w4[4], b4[4], x_sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = grp + 4 * i;
+      w4[i] = p < n16 ? a.w_part[(blk * n16 + p) * DR_C + tok] : 0.f;
+      b4[i] = p < n16 ? a.b_part[(blk * n16 + p) * DR_C + tok] : 0.f;
     }
-    float x_sum = 0.f;
-    for (int p = lane; p < n16; p += 32) x_sum += a.x_part[blk * n16 + p];
+    if (lane < n16) x_sum = a.x_part[blk * n16 + lane];
+    const float c_in = vec[DV_C * DR_C + tok], G = vec[DV_C * DR_C + DR_C - 1], be = vec[DV_BETA * DR_C + tok];
+    float w = (w4[0] + w4[1]) + (w4[2] + w4[3]), b = (b4[0] + b4[1]) + (b4[2] + b4[3]);
+    for (int p = grp + 16; p < n16; p += 4) {
+      w += a.w_part[(blk * n16 + p) * DR_C + tok];
+      b += a.b_part[(blk * n16 + p) * DR_C + tok];
+    }
+    for (int p = lane + 32; p < n16; p += 32) x_sum += a.x_part[blk * n16 + p];
 #pragma unroll
     for (int o = 16; o; o >>= 1) x_sum += __shfl_xor_sync(0xffffffffu, x_sum, o);
+    part[grp * DR_C + tok] = w;
+    part[(4 + grp) * DR_C + tok] = b;
     if (tid < DR_C) {
-      const float c = vec[DV_C * DR_C + tid], G = vec[DV_C * DR_C + DR_C - 1], be = vec[DV_BETA * DR_C + tid];
-      vc[tid] = c;
+      vc[tid] = c_in;
       vc[DR_C + tid] = be;
-      vc[2 * DR_C + tid] = be * expf(c);
-      vc[3 * DR_C + tid] = be * expf(G - c);
+      vc[2 * DR_C + tid] = be * expf(c_in);
+      vc[3 * DR_C + tid] = be * expf(G - c_in);
     }
+    if (hr == 0)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (tid + i * 256 < TF_N * DR_C) tfs[tid + i * 256] = tf_in[i];
     float f[4][4], wm[4][4], sd = 0.f;  // F, W; this thread's part of <S, dS'>
 #pragma unroll
     for (int n = 0; n < 4; ++n)
@@ -644,18 +656,22 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
     }
     // K~ = f_k K16, Q~ = f_q Q16
     const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
-#pragma unroll 4
-    for (int i = tid; i < 2 * DR_C * (DK / 8); i += 256) {
-      const int isq = i >= DR_C * (DK / 8), ii = i - isq * DR_C * (DK / 8);
-      const int r = ii / (DK / 8), c = ii % (DK / 8);
-      const uint4 x = *reinterpret_cast<const uint4*>(kq + isq * DR_C * DK * 2 + img_off(r, c, DK * 2));
-      const float fs = tfs[(isq ? TF_FQ : TF_FK) * DR_C + r];
-      float* dst = (isq ? Qm : Km) + r * LDS + c * 8;
+    {
+      uint4 raw[DK / 16];  // 2 x 64 rows of DK / 8 pieces, all in flight
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 y = unpack_f16x2((&x.x)[j]);
-        *reinterpret_cast<float2*>(dst + 2 * j) =
-            make_float2(__uint_as_float(tf32(y.x * fs)), __uint_as_float(tf32(y.y * fs)));
+      for (int n = 0; n < DK / 16; ++n) raw[n] = __ldg(reinterpret_cast<const uint4*>(kq) + tid + n * 256);
+#pragma unroll
+      for (int n = 0; n < DK / 16; ++n) {
+        const int i = tid + n * 256, isq = n >= DK / 32;  // pieces as they lie: swizzled within the row
+        const int r = i / (DK / 8) - isq * DR_C, c = (i % (DK / 8)) ^ (r & 7);
+        const float fs = tfs[(isq ? TF_FQ : TF_FK) * DR_C + r];
+        float* dst = (isq ? Qm : Km) + r * LDS + c * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = unpack_f16x2((&raw[n].x)[j]);
+          *reinterpret_cast<float2*>(dst + 2 * j) =
+              make_float2(__uint_as_float(tf32(y.x * fs)), __uint_as_float(tf32(y.y * fs)));
+        }
       }
     }
     // <S, dS'> of the block, for the gates: dg_t = <S', dS'> + sum_{i >= t} w_i, dbeta = E.Z

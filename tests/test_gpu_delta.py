@@ -137,6 +137,9 @@ SHAPES = [
     ([70], 1, 1, 8, 8, 1, True, False),
     ([300], 1, 1, 64, 264, 1, False, False),     # more value channels than keys, past four blocks of 64
     ([0, 0], 1, 1, 64, 64, 1, True, False),
+    ([40], 2, 4, 192, 128, 1, True, True),       # the longest call that runs token by token, and the next
+    ([41], 2, 4, 192, 128, 1, True, True),
+    ([7, 0, 1, 20], 1, 3, 256, 40, 0, True, False),
     ([5000], 1, 1, 64, 64, 1, True, False),      # few heads and long: cut into segments
     ([1500, 0, 2100, 30, 1], 1, 1, 192, 192, 1, True, True),
     ([1000, 1], 1, 2, 256, 64, 1, True, False),
