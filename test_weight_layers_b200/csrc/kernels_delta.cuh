@@ -488,11 +488,14 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
 // ---------------------------------------------------------------------------
 // State pass: the recurrence over the chunks of a sequence.  The rows of S
 // (value channels) do not meet, so a warp owns 16 of them and keeps them in
-// registers for the whole sequence, S^T-free: S [16][dk] as accumulators is at
-// once the A operand of S K^T, the errors R^T [16][64] that of (beta R)^T Y^T,
-// the writes U^T that of U^T K and U^T P^T.  No warp waits for another inside
-// a chunk; shared memory holds only what all warps read (K16, Q16, Y, P),
-// brought by bulk copies one chunk ahead.
+// registers for the whole sequence: S [16][dk] as accumulators is at once the A
+// operand of S K^T, the errors R^T [16][64] that of (beta R)^T Y^T, the writes U^T
+// that of U^T K and U^T P^T.  No row warp waits for another inside a chunk; shared
+// memory holds only what all of them read (K16, Q16, Y, P), brought one to two
+// chunks ahead by a warp of its own, or by the warps that make the outputs beside
+// the chain (forward; they take S's and U's leading parts from the row warps).
+// Bound by the chain's latency: 6,200 cycles a chunk at dk = 128, 8,100 at 192, of
+// which the row warp's and its output warp's 400 and 560 products are 3,200 and 4,500.
 //
 // Few heads leave most SMs idle while a long sequence runs chunk by chunk.  S' is linear in S, so the sequence is
 // then cut into segments: the scan pass runs each from a zero state (N, its end) and from the unit matrix without
