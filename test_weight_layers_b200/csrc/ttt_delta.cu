@@ -64,7 +64,25 @@ int seg_chunks(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
   return (int)k;
 }
 
-DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward) {
+// The most segments of any call with up to T tokens in up to n_seq sequences: a workspace for (T, n_seq) serves fewer
+// and shorter sequences too, and few sequences are cut where many are not.  With k chunks to a segment, n sequences have
+// at most n + (T / 64 + n) / k segments; k >= chunks / most, 2 k^2 >= chunks and chunks >= 12 bound that by
+// n + 13/12 n min(most, sqrt(2 chunks)).
+int64_t seg_cap(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
+  int64_t cap = 0;
+  for (int64_t n = 1; dt == TTT_BF16 && n <= n_seq; ++n) {
+    const int64_t most = kDeltaSms / (pass_blocks(d) * n), chunks = (T / n + DR_C - 1) / DR_C;
+    if (most < 3 || chunks < 12) break;
+    int64_t root = 1;
+    while (root < most && root * root < 2 * chunks) ++root;
+    cap = std::max(cap, n + n * root * 13 / 12 + 1);
+  }
+  return cap;
+}
+
+// `cap`: room for so many segments (the workspace query), else for this call's.
+DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward,
+                    int64_t cap = -1) {
   DeltaWs w{};
   uint8_t* b = static_cast<uint8_t*>(base);
   size_t off = 0;
@@ -78,14 +96,15 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
   w.seg_chunks = seg_chunks(d, T, n_seq, dt);
   w.max_segs = n_seq + (w.seg_chunks ? (int)(w.max_chunks / w.seg_chunks) : 0);
   w.status = reinterpret_cast<unsigned int*>(take(256));
-  w.seqs = reinterpret_cast<DrSeq*>(take((size_t)std::max(w.max_segs, 1) * sizeof(DrSeq)));
+  const size_t segs_room = cap >= 0 ? cap : w.seg_chunks ? w.max_segs : 0;
+  w.seqs = reinterpret_cast<DrSeq*>(take((n_seq + segs_room + 1) * sizeof(DrSeq)));
   w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
   if (dt == TTT_BF16) {
     w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
     w.blk = take((size_t)w.max_chunks * d.heads_v * w.blk_bytes);
   }
-  if (w.seg_chunks) {
-    const size_t segs = (size_t)w.max_segs * d.heads_v, dkp = dk_pad(d.dk);
+  if (segs_room) {
+    const size_t segs = segs_room * d.heads_v, dkp = dk_pad(d.dk);
     w.seg_s = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
     w.seg_n = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
     w.phi = take(segs * 2 * dkp * dkp * 2);
@@ -215,7 +234,8 @@ int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream
 }
 
 template <int DK>
-int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, const DeltaWs& w, cudaStream_t s) {
+int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra, const GradArgs& ga, const DeltaWs& w,
+                  cudaStream_t s) {
   TTT_TRY((launch_prep<DK, true>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
   const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps, true);
@@ -361,7 +381,7 @@ size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_
   if ((dtype != TTT_FP32 && dtype != TTT_BF16) || !delta_dims_ok(dims) || !delta_dims_supported(dims) || T < 0 ||
       T > INT32_MAX - DR_C || n_seq < 0 || n_seq > kDeltaMaxSeqs)
     return 0;
-  return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0).total;
+  return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0, seg_cap(dims, T, n_seq, dtype)).total;
 }
 
 int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,

@@ -83,6 +83,22 @@ def test_delta_workspace(lib):
     assert _fwd(lib, ws=None) == WS and _fwd(lib, ws=ctypes.c_void_p((1 << 24) + 128)) == WS
 
 
+def test_delta_workspace_serves_every_smaller_call(lib):
+    # long sequences of few heads are cut, which takes room that more or shorter ones do not need
+    for dims in ((4, 4, 192, 192), (1, 1, 64, 64), (8, 16, 128, 128), (2, 2, 256, 40)):
+        dm = T.delta_dims(*dims)
+        for back in (0, 1):
+            size = lambda t, n: lib.ttt_delta_workspace_bytes(dm, t, n, T.TTT_BF16, back)  # noqa: E731, B023
+            grid = [(t, n) for t in (0, 40, 700, 705, 768, 1374, 5000, 9999, 40000, 131072) for n in (1, 2, 3, 7, 16, 50, 400)]
+            for t, n in grid:
+                assert all(size(t, n) >= size(u, m) for u, m in grid if u <= t and m <= n), (dims, t, n)
+            # ... and each call's own need is within its query
+            for t, n in grid:
+                if t:
+                    rc = _fwd(lib, dm, T_=t, n_seq=n, ws_bytes=size(t, n), Q=ctypes.c_void_p((1 << 24) + 2))
+                    assert rc == AL, (dims, t, n)  # past the workspace check, stopped at Q's alignment
+
+
 def _norm(lib, cfg, dt=T.TTT_BF16, Y=FAKE[0], Xo=FAKE[1], N=FAKE[2], X=FAKE[3], T_=8, w=FAKE[4]):
     return lib.ttt_block_norm(X, Y, None, w, None, None, Xo, N, T_, ctypes.byref(cfg), dt, None)
 

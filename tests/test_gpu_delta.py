@@ -250,6 +250,20 @@ def test_long_sequence_in_place():
     assert torch.equal(O, O2) and torch.equal(S, state)
 
 
+def test_workspace_of_a_larger_call():
+    # sized for 16 sequences that are not cut, used for one that is
+    big, c = Seqs([250] * 16, 4, 4, 64, 64, seed=29), Seqs([4000], 4, 4, 64, 64, seed=30)
+    want, want_s, _ = c.forward()
+    ws, wsb = big.workspace(), big.workspace(True)
+    big.forward(ws=ws)
+    O, S, _ = c.forward(ws=ws)
+    assert torch.equal(O, want) and torch.equal(S, want_s)
+    big.backward(ws=wsb)
+    out, _ = c.backward(ws=wsb)
+    ref, _ = c.backward()
+    assert T.ttt_poll_status(wsb) == T.TTT_OK and all(torch.equal(out[k], ref[k]) for k in out)
+
+
 def test_gradients_of_zero_and_tiny_rows():
     # x / max(||x||, 1e-12): a zero row passes 1e12 times the gradient, a tiny one 1 / ||x|| times its part across x
     c = Seqs([80], 1, 1, 64, 64, seed=27)
