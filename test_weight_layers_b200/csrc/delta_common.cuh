@@ -40,8 +40,10 @@ enum {
   DV_C = 7,     // c_j
   DR_NVEC = 8
 };
-// Bytes of a value head's chunk block: Y hi | Y lo | P hi | vectors (| P lo, for the backward pass)
-constexpr int DR_HBLK = 3 * DR_TILE + DR_NVEC * DR_C * 4;
+// A value head's chunk block: Y hi | Y lo | vectors | P hi | P lo.  The scan takes what stands before P.
+constexpr int DR_VEC = 2 * DR_TILE;                          // byte offset of the vectors
+constexpr int DR_P = DR_VEC + DR_NVEC * DR_C * 4;            // ... and of P
+constexpr int DR_BLK = DR_P + 2 * DR_TILE;
 
 // A sequence, or a segment of one: first token, tokens in it (-1: nothing to do), first chunk, the sequence's
 // number, the segment's number in it and how many it has.

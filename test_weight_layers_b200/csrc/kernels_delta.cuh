@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
 // Chunk preparation: one block per (chunk, query/key head), for all value heads
 // that share it.  Writes K16 and Q16 (the token rows, exact in fp16, as
 // shared-memory images for the next kernels' bulk copies) and per value head
-// Y (hi, lo), P and the chunk vectors.
+// Y and P (hi, lo) and the chunk vectors.
 struct PrepArgs {
   const __nv_bfloat16 *Q, *K;
   const float *g, *beta;  // [T][heads_v]
@@ -130,8 +130,7 @@ struct PrepArgs {
   float scale;
   const DrChunk* chunks;
   uint8_t* kq;   // [chunk][hk][K16 | Q16]
-  uint8_t* blk;  // [chunk][hv][blk_bytes]
-  int blk_bytes;
+  uint8_t* blk;  // [chunk][hv][DR_BLK]
   float* tok;    // [chunk][hk][6][64] token factors (TF_*), backward pass only
 };
 
@@ -173,7 +172,7 @@ __device__ __forceinline__ void store_half_row(const float* p, int i, int half, 
     split2(b.z * s, b.w * s, h.w, l.w);
     const uint32_t off = img_off(i, half * 4 + ch, 128);
     *reinterpret_cast<uint4*>(hi + off) = h;
-    if (lo) *reinterpret_cast<uint4*>(lo + off) = l;
+    *reinterpret_cast<uint4*>(lo + off) = l;
   }
 }
 
@@ -402,8 +401,8 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
 #pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
-    uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * a.blk_bytes;
-    float* vec = reinterpret_cast<float*>(blk + 3 * DR_TILE);
+    uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * DR_BLK;
+    float* vec = reinterpret_cast<float*>(blk + DR_VEC);
     // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
     // exp of less than -110 is zero in fp32: lower values (-inf: a reset) are taken as that, so that the sums of the
     // tokens behind them keep their digits
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
     {
       const float* P = Ym + i * PREP_LD;
       const int e = half_row_exp(P, half);
-      store_half_row(P, i, half, pow2i(e), blk + 2 * DR_TILE, BACK ? blk + DR_HBLK : nullptr);
+      store_half_row(P, i, half, pow2i(e), blk + DR_P, blk + DR_P + DR_TILE);
       if (!half) {
         const double G = c[DR_C - 1] + c31, cii = c[i] + (i >= 32 ? c31 : 0.0);
         const float ec = expf((float)cii), el = expf((float)(G - cii));
@@ -493,9 +492,12 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
 // that of U^T K and U^T P^T.  No row warp waits for another inside a chunk; shared
 // memory holds only what all of them read (K16, Q16, Y, P), brought one to two
 // chunks ahead by a warp of its own, or by the warps that make the outputs beside
-// the chain (forward; they take S's and U's leading parts from the row warps).
-// Bound by the chain's latency: 6,200 cycles a chunk at dk = 128, 8,100 at 192, of
-// which the row warp's and its output warp's 400 and 560 products are 3,200 and 4,500.
+// the chain (forward; they take S's parts and U from the row warps).
+// Bound by the chain's latency: 6,900 cycles a chunk at dk = 128, 9,500 at 192, of
+// which the row warp's and its output warp's 504 and 696 products are 4,000 and 5,600.
+// (The outputs' share with one part of S, U and P each was 104 and 136 products fewer and
+// the pass a tenth faster, 239 us for 265 of packed prompts; but an output whose terms cancel,
+// as where a key is written again, then keeps 2^-11 of the terms instead of its own bits.)
 //
 // Few heads leave most SMs idle while a long sequence runs chunk by chunk.  S' is linear in S, so the sequence is
 // then cut into segments: the scan pass runs each from a zero state (N, its end) and from the unit matrix without
@@ -512,7 +514,6 @@ struct StateArgs {
   const DrSeq* seqs;
   const uint8_t* kq;
   const uint8_t* blk;
-  int blk_bytes;
   Guard guard;
   // segments: [segment][hv][dv][dk] states at their starts and scan results, [segment][hv] transitions (fp16 hi
   // and lo images [DK][DK], rows scaled) and their rows' inverse scales [segment][hv][DK]
@@ -535,33 +536,36 @@ __device__ __forceinline__ uint32_t vtile_off(int row, int half) {
 
 enum { PASS_OUT = 0, PASS_BACK = 1, PASS_SCAN = 2 };  // what a state pass is for
 
-template <int DK, bool BACK>
-constexpr int state_stage() {
-  return 2 * DR_C * DK * 2 + DR_HBLK + (BACK ? DR_TILE : 0);
-}
-// per warp two V tiles, and two dO tiles for the backward pass
-template <bool BACK>
-constexpr int state_warp_smem() {
-  return (BACK ? 4 : 2) * DR_VTILE;
-}
-// Outputs of their own warps (dk <= 192, where shared memory holds the hand-over): per warp S's and U's leading
-// parts as A fragments, their row scales, and a tile for O.
+// Outputs of their own warps where shared memory holds the hand-over (dk <= 192): per warp S's parts as A
+// fragments with their row scales, U, and a tile for O.
 template <int DK, int PASS>
 constexpr bool state_split() {
   return PASS == PASS_OUT && DK <= 192;
 }
 template <int DK>
 constexpr int state_hand() {
-  return DK / 16 * 512 + 4 * 512 + 2 * 256 + DR_VTILE;
+  return DK / 16 * 1024 + 256 + 4096 + DR_VTILE;
+}
+// A stage (two of them): K16, Q16 and the chunk's block; without Q16 and P in the scan, which has no outputs, and
+// where the output warps keep those in one buffer of their own (they have the row warps' state update to refill it).
+template <int DK, int PASS>
+constexpr int state_stage() {
+  return PASS == PASS_SCAN || state_split<DK, PASS>() ? DR_C * DK * 2 + DR_P : 2 * DR_C * DK * 2 + DR_BLK;
+}
+template <int DK, int PASS>
+constexpr int state_obuf() {
+  return state_split<DK, PASS>() ? DR_C * DK * 2 + 2 * DR_TILE : 0;
+}
+// per warp two V tiles, and two dO tiles for the backward pass
+template <int PASS>
+constexpr int state_warp_smem() {
+  return (PASS == PASS_BACK ? 4 : 2) * DR_VTILE;
 }
 constexpr int DR_ETILE = 16 * DR_C * 4;  // a warp's E rows (reverse pass)
-template <int DK, bool BACK>
+template <int DK, int PASS>
 constexpr int state_smem(int warps, bool etile = false) {
-  return 2 * state_stage<DK, BACK>() + warps * (state_warp_smem<BACK>() + (etile ? DR_ETILE : 0)) + 64;
-}
-template <int DK>
-constexpr int state_out_smem(int warps) {
-  return state_smem<DK, false>(warps) + (state_split<DK, PASS_OUT>() ? warps * (state_hand<DK>() + 32) : 0);
+  return 2 * state_stage<DK, PASS>() + state_obuf<DK, PASS>() + 64 +
+         warps * (state_warp_smem<PASS>() + (etile ? DR_ETILE : 0) + (state_split<DK, PASS>() ? state_hand<DK>() + 32 : 0));
 }
 template <int DK, int PASS>
 constexpr int state_threads() {  // at most four warps of rows, and as many for their outputs or one that copies
@@ -595,6 +599,28 @@ __device__ __forceinline__ void store_vtile(const uint8_t* src, __nv_bfloat16* p
 // read with .trans it gives the accumulator layout of two neighbouring 8-token tiles (rows = channels).
 __device__ __forceinline__ uint32_t vtile_addr(uint32_t base, int lane, int n0) {
   return base + vtile_off(n0 + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
+}
+
+// x += P U in the accumulator layout (rows of U^T = r at scales w0, w1), all parts.
+__device__ __forceinline__ void mul_pu(float (&x)[8][4], const float (&r)[8][4], float w0, float w1, uint32_t ph,
+                                       uint32_t pl, int lane) {
+#pragma unroll
+  for (int kt = 0; kt < 4; ++kt) {
+    uint32_t hi[4], lo[4];
+    split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
+#pragma unroll
+    for (int np = kt; np < 4; ++np) {
+      uint32_t p[4];
+      ldsm4(p, addr_bn(ph, lane, np * 16, kt * 2, 128));
+      mma_f16(x[2 * np], hi, p[0], p[1]);
+      mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+      mma_f16(x[2 * np], lo, p[0], p[1]);
+      mma_f16(x[2 * np + 1], lo, p[2], p[3]);
+      ldsm4(p, addr_bn(pl, lane, np * 16, kt * 2, 128));
+      mma_f16(x[2 * np], hi, p[0], p[1]);
+      mma_f16(x[2 * np + 1], hi, p[2], p[3]);
+    }
+  }
 }
 
 // O's tile in the accumulator layout, o (Q S^T at scales is) and x (P U at scales iu), to the rows of a tile.
@@ -641,25 +667,28 @@ template <int DK, int PASS>
 __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(const StateArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr bool BACK = PASS == PASS_BACK, SCAN = PASS == PASS_SCAN, SPLIT = state_split<DK, PASS>();
-  constexpr int STAGE = state_stage<DK, BACK>();
-  constexpr int KQ = 2 * DR_C * DK * 2;
-  constexpr int HB = STAGE - KQ;
-  constexpr int WSM = state_warp_smem<BACK>();
+  constexpr int STAGE = state_stage<DK, PASS>();
+  constexpr int KB = DR_C * DK * 2;                  // bytes of K16, and of Q16
+  constexpr int YB = SPLIT || SCAN ? KB : 2 * KB;    // offset of Y in a stage
+  constexpr int TILES = 2 * STAGE + state_obuf<DK, PASS>();  // offset of the warps' tiles
+  constexpr int WSM = state_warp_smem<PASS>();
   constexpr int NT = DK / 8;
   const int tid = threadIdx.x, lane = tid & 31;
   const int nwarp = SPLIT ? blockDim.x >> 6 : (blockDim.x >> 5) - 1;  // warps that own rows
   const bool outer = SPLIT && tid >> 5 >= nwarp;
   const int warp = outer ? (tid >> 5) - nwarp : tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* vbuf = smem + 2 * STAGE + warp * WSM;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * STAGE + nwarp * WSM);  // [2] stage and tiles have landed
-  uint64_t* empty = full + 2;                                                    // [2] every warp has read them
-  // hand-over from a row warp to its output warp: S parts written, read, U parts written, read
-  uint64_t* hand = empty + 2 + 4 * warp;
-  uint8_t* hbuf = smem + state_smem<DK, false>(nwarp) + nwarp * 32 + warp * state_hand<DK>();
-  uint4 *h_s = reinterpret_cast<uint4*>(hbuf), *h_u = h_s + DK / 16 * 32;
-  float2 *h_ss = reinterpret_cast<float2*>(h_u + 4 * 32), *h_us = h_ss + 32;
-  uint8_t* obuf = reinterpret_cast<uint8_t*>(h_us + 32);
+  uint8_t* vbuf = smem + TILES + warp * WSM;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + TILES + nwarp * WSM);  // [2] stage and tiles have landed
+  uint64_t* empty = full + 2;                                                // [2] every warp has read them
+  uint64_t *ofull = full + 4, *oempty = full + 5;  // the output warps' Q16 and P have landed, every one has read them
+  // hand-over from a row warp to its output warp: S's parts written, read, U written, read
+  uint64_t* hand = full + 6 + 4 * warp;
+  uint8_t* hbuf = smem + TILES + nwarp * (WSM + 32) + 64 + warp * state_hand<DK>();
+  uint4* h_s = reinterpret_cast<uint4*>(hbuf);  // [dk / 16][hi, lo][32]
+  float4* h_u = reinterpret_cast<float4*>(h_s + DK / 16 * 64);
+  float2* h_ss = reinterpret_cast<float2*>(h_u + 8 * 32);
+  uint8_t* obuf = reinterpret_cast<uint8_t*>(h_ss + 32);
   const int nblocks = (a.dv + nwarp * 16 - 1) / (nwarp * 16);
   const int vblocks = nblocks + (SCAN ? (DK + nwarp * 16 - 1) / (nwarp * 16) : 0);
   const int h = blockIdx.x / vblocks % a.hv, hq = h / (a.hv / a.hk);
@@ -673,8 +702,11 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
       mbar_init(&full[i], 1 + 32 * (SPLIT ? nwarp : 1));  // the bulk copies, and each copying lane's tile copies
       mbar_init(&empty[i], nwarp * (SPLIT ? 2 : 1));
     }
-    if (SPLIT)
-      for (int i = 0; i < 4 * nwarp; ++i) mbar_init(&empty[2 + i], 1);
+    if (SPLIT) {
+      mbar_init(ofull, 1);
+      mbar_init(oempty, nwarp);
+      for (int i = 0; i < 4 * nwarp; ++i) mbar_init(&full[6 + i], 1);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -690,21 +722,12 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
     uint64_t* bar = &full[n & 1];
     const int64_t ci = sq.chunk0 + n;
     uint8_t* st = smem + (n & 1) * STAGE;
-    const uint8_t* kq = a.kq + (ci * a.hk + hq) * KQ;
-    const uint8_t* blk = a.blk + (ci * a.hv + h) * a.blk_bytes;
-    if constexpr (SCAN) {  // without Q16 and P
-      mbar_expect_tx(bar, KQ / 2 + HB - DR_TILE);
-      bulk_load(st, kq, KQ / 2, bar);
-      bulk_load(st + KQ, blk, 2 * DR_TILE, bar);
-      bulk_load(st + KQ + 3 * DR_TILE, blk + 3 * DR_TILE, HB - 3 * DR_TILE, bar);
-    } else {
-      mbar_expect_tx(bar, KQ + HB);
-      bulk_load(st, kq, KQ, bar);
-      bulk_load(st + KQ, blk, HB, bar);
-    }
+    mbar_expect_tx(bar, STAGE);
+    bulk_load(st, a.kq + (ci * a.hk + hq) * 2 * KB, YB, bar);
+    bulk_load(st + YB, a.blk + (ci * a.hv + h) * DR_BLK, STAGE - YB, bar);
   };
   auto load_tiles = [&](int n, int w) {  // one warp: row warp w's tiles
-    const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + (n & 1) * DR_VTILE);
+    const uint32_t dst = smem_u32(smem + TILES + w * WSM + (n & 1) * DR_VTILE);
     load_vtile(dst, a.V, a.ldv, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
     if constexpr (BACK) load_vtile(dst + 2 * DR_VTILE, a.dO, a.ldo, sq, n, h * a.dv, vfirst + w * 16, dv_in, lane);
   };
@@ -721,24 +744,38 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
 
   if constexpr (SPLIT) {
     if (outer) {
-      // O = e^c Q S^T + P U from the row warp's leading parts (2^-12, enough for a bf16 output), beside its chain;
-      // and the next chunk's copies, once every warp is done with the stage
+      // O = e^c Q S^T + P U beside the row warp's chain, from both parts of S, U and P: what is read from the state and
+      // what is written over it can cancel; and the next chunk's copies, once every warp is done with the stage
       auto copy = [&](int n) {
         if (warp == 0 && lane == 0) load_stage(n);
         load_tiles(n, warp);
         cp_arrive(&full[n & 1]);
       };
-      if (nchunk > 0) copy(0);
+      uint8_t* ob = smem + 2 * STAGE;
+      const uint32_t qb = smem_u32(ob), ph = qb + KB, pl = ph + DR_TILE;
+      auto copy_o = [&](int n) {
+        const int64_t ci = sq.chunk0 + n;
+        mbar_expect_tx(ofull, KB + 2 * DR_TILE);
+        bulk_load(ob, a.kq + (ci * a.hk + hq) * 2 * KB + KB, KB, ofull);
+        bulk_load(ob + KB, a.blk + (ci * a.hv + h) * DR_BLK + DR_P, 2 * DR_TILE, ofull);
+      };
+      if (nchunk > 0) {
+        copy(0);
+        if (warp == 0 && lane == 0) copy_o(0);
+      }
 #pragma unroll 1
       for (int n = 0; n < nchunk; ++n) {
+        if (warp == 0 && n > 0) {
+          mbar_wait(oempty, (n - 1) & 1, a.guard);
+          if (lane == 0) copy_o(n);
+        }
         if (n + 1 < nchunk) {
           if (n > 0) mbar_wait(&empty[(n + 1) & 1], ((n - 1) >> 1) & 1, a.guard);
           copy(n + 1);
         }
         mbar_wait(&full[n & 1], (n >> 1) & 1, a.guard);
-        const uint32_t st = smem_u32(smem + (n & 1) * STAGE);
-        const uint32_t qb = st + DR_C * DK * 2, pb = st + KQ + 2 * DR_TILE;
-        const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + KQ + 3 * DR_TILE);
+        mbar_wait(ofull, n & 1, a.guard);
+        const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + YB + DR_VEC);
         float o[8][4], x[8][4];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -748,35 +785,38 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
         const float2 is = h_ss[lane];
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt) {
-          const uint4 v = h_s[kt * 32 + lane];
-          const uint32_t hi[4] = {v.x, v.y, v.z, v.w};
+          const uint4 v = h_s[kt * 64 + lane], w = h_s[kt * 64 + 32 + lane];
+          const uint32_t hi[4] = {v.x, v.y, v.z, v.w}, lo[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int np = 0; np < 4; np += 2) {
             uint32_t c[2][4];
             ldsm4(c[0], addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
             ldsm4(c[1], addr_bn(qb, lane, np * 16 + 16, kt * 2, DK * 2));
             mma_f16x4(o + 2 * np, hi, c);
+            mma_f16x4(o + 2 * np, lo, c);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&hand[1]);
         mbar_wait(&hand[2], n & 1, a.guard);
-        const float2 iu = h_us[lane];
+        float r[8][4], m0 = 0.f, m1 = 0.f;
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-          const uint4 v = h_u[kt * 32 + lane];
-          const uint32_t hi[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int np = kt; np < 4; ++np) {
-            uint32_t p[4];
-            ldsm4(p, addr_bn(pb, lane, np * 16, kt * 2, 128));
-            mma_f16(x[2 * np], hi, p[0], p[1]);
-            mma_f16(x[2 * np + 1], hi, p[2], p[3]);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const float4 v = h_u[k * 32 + lane];
+          r[k][0] = v.x, r[k][1] = v.y, r[k][2] = v.z, r[k][3] = v.w;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&hand[3]);
-        store_o(o, x, is.x, is.y, iu.x, iu.y, vec, smem_u32(obuf), lane);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m0 = max_abs2(m0, r[k][0], r[k][1]);
+          m1 = max_abs2(m1, r[k][2], r[k][3]);
+        }
+        const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
+        mul_pu(x, r, pow2i(f0), pow2i(f1), ph, pl, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(oempty);
+        store_o(o, x, is.x, is.y, pow2i(-f0), pow2i(-f1), vec, smem_u32(obuf), lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[n & 1]);
         store_vtile(obuf, a.O, a.ldo, sq, n, (int64_t)h * a.dv, v0, a.dv, lane);
@@ -815,8 +855,8 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
     // a wait that gives up records the error; the pass then runs on (bounded) with what the stage holds
     mbar_wait(&full[n & 1], (n >> 1) & 1, a.guard);
     const uint32_t st = smem_u32(smem + (n & 1) * STAGE);
-    const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, pb = yl + DR_TILE;
-    const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + KQ + 3 * DR_TILE);
+    const uint32_t kb = st, qb = st + KB, yh = st + YB, yl = yh + DR_TILE, ph = yh + DR_P, pl = ph + DR_TILE;
+    const float* vec = reinterpret_cast<const float*>(smem + (n & 1) * STAGE + YB + DR_VEC);
     const uint32_t vb = smem_u32(vbuf + (n & 1) * DR_VTILE);
     const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;  // this chunk's block of the kept arrays
 
@@ -842,7 +882,10 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
     for (int kt = 0; kt < DK / 16; ++kt) {
       uint32_t hi[4], lo[4];
       split_a(s[2 * kt], s[2 * kt + 1], sc0, sc1, hi, lo);
-      if constexpr (SPLIT) h_s[kt * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (SPLIT) {
+        h_s[kt * 64 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        h_s[kt * 64 + 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
 #pragma unroll
       for (int np = 0; np < 4; np += 2) {
         uint32_t b[2][4], c[2][4];
@@ -850,13 +893,12 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
         ldsm4(b[1], addr_bn(kb, lane, np * 16 + 16, kt * 2, DK * 2));
         mma_f16x4(r + 2 * np, hi, b);
         if constexpr (!SCAN && !SPLIT) {
-          // the outputs are rounded to bf16: S's hi part alone (2^-12) is enough for them
           ldsm4(c[0], addr_bn(qb, lane, np * 16, kt * 2, DK * 2));
           ldsm4(c[1], addr_bn(qb, lane, np * 16 + 16, kt * 2, DK * 2));
           mma_f16x4(o + 2 * np, hi, c);
         }
         mma_f16x4(r + 2 * np, lo, b);
-        if constexpr (BACK) mma_f16x4(o + 2 * np, lo, c);  // the gates' gradients are sums of dO . O in fp32
+        if constexpr (!SCAN && !SPLIT) mma_f16x4(o + 2 * np, lo, c);
       }
     }
     // R = V - e^c K S^T, then the scale of beta R
@@ -942,23 +984,10 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
         r[k][3] *= be.y;
       }
     }
-    if constexpr (SPLIT) {  // U's leading parts for the output warp
-      m0 = m1 = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m0 = max_abs2(m0, r[k][0], r[k][1]);
-        m1 = max_abs2(m1, r[k][2], r[k][3]);
-      }
-      const int f0 = row_exp(quad_max(m0), DR_ROW_EXP), f1 = row_exp(quad_max(m1), DR_ROW_EXP);
-      const float w0 = pow2i(f0), w1 = pow2i(f1);
+    if constexpr (SPLIT) {  // U for the output warp
       if (n > 0) mbar_wait(&hand[3], (n - 1) & 1, a.guard);
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt)
-        h_u[kt * 32 + lane] = make_uint4(pack_f16x2(r[2 * kt][0] * w0, r[2 * kt][1] * w0),
-                                         pack_f16x2(r[2 * kt][2] * w1, r[2 * kt][3] * w1),
-                                         pack_f16x2(r[2 * kt + 1][0] * w0, r[2 * kt + 1][1] * w0),
-                                         pack_f16x2(r[2 * kt + 1][2] * w1, r[2 * kt + 1][3] * w1));
-      h_us[lane] = make_float2(pow2i(-f0), pow2i(-f1));
+      for (int k = 0; k < 8; ++k) h_u[k * 32 + lane] = make_float4(r[k][0], r[k][1], r[k][2], r[k][3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&hand[2]);
     }
@@ -977,25 +1006,7 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
       for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[k][j] = 0.f;
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
-        split_a(r[2 * kt], r[2 * kt + 1], w0, w1, hi, lo);
-#pragma unroll
-        for (int np = kt; np < 4; ++np) {
-          uint32_t p[4];
-          ldsm4(p, addr_bn(pb, lane, np * 16, kt * 2, 128));
-          mma_f16(x[2 * np], hi, p[0], p[1]);
-          mma_f16(x[2 * np + 1], hi, p[2], p[3]);
-          if constexpr (BACK) {
-            mma_f16(x[2 * np], lo, p[0], p[1]);
-            mma_f16(x[2 * np + 1], lo, p[2], p[3]);
-            ldsm4(p, addr_bn(yh + DR_HBLK, lane, np * 16, kt * 2, 128));
-            mma_f16(x[2 * np], hi, p[0], p[1]);
-            mma_f16(x[2 * np + 1], hi, p[2], p[3]);
-          }
-        }
-      }
+      mul_pu(x, r, w0, w1, ph, pl, lane);
       if constexpr (BACK) {  // this warp's part of dO . O for each token
         const uint32_t db = smem_u32(vbuf + (2 + (n & 1)) * DR_VTILE);
 #pragma unroll

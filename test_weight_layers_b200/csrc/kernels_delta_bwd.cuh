@@ -32,7 +32,6 @@ struct ReverseArgs {
   const DrSeq* seqs;
   const uint8_t* kq;
   const uint8_t* blk;
-  int blk_bytes;
   Guard guard;
   const float* keep_e;
   float* keep_ds;  // [chunk][hv][dv][dk] dS'
@@ -49,10 +48,9 @@ struct ReverseArgs {
 template <int DK, bool SCAN>
 __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int STAGE = state_stage<DK, true>();
+  constexpr int STAGE = state_stage<DK, PASS_BACK>();
   constexpr int KQ = 2 * DR_C * DK * 2;
-  constexpr int HB = STAGE - KQ;
-  constexpr int WSM = state_warp_smem<true>();
+  constexpr int WSM = state_warp_smem<PASS_BACK>();
   constexpr int NT = DK / 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = (blockDim.x >> 5) - 1;
   const int g = lane >> 2, t = lane & 3;
@@ -87,9 +85,9 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
       if (it >= 2) mbar_wait(&empty[buf], ((it >> 1) - 1) & 1, a.guard);
       if (lane == 0) {
         uint8_t* st = smem + buf * STAGE;
-        mbar_expect_tx(bar, KQ + HB);
+        mbar_expect_tx(bar, STAGE);
         bulk_load(st, a.kq + (ci * a.hk + hq) * KQ, KQ, bar);
-        bulk_load(st + KQ, a.blk + (ci * a.hv + h) * a.blk_bytes, HB, bar);
+        bulk_load(st + KQ, a.blk + (ci * a.hv + h) * DR_BLK, DR_BLK, bar);
       }
       for (int w = 0; w < nwarp; ++w) {
         const uint32_t dst = smem_u32(smem + 2 * STAGE + w * WSM + buf * DR_VTILE);
@@ -130,9 +128,8 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
     const int n = nchunk - 1 - it, buf = it & 1;
     mbar_wait(&full[buf], (it >> 1) & 1, a.guard);  // (as in the state pass)
     const uint32_t st = smem_u32(smem + buf * STAGE);
-    const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, ph = yl + DR_TILE;
-    const uint32_t pl = yh + DR_HBLK;
-    const float* vec = reinterpret_cast<const float*>(smem + buf * STAGE + KQ + 3 * DR_TILE);
+    const uint32_t kb = st, qb = st + DR_C * DK * 2, yh = st + KQ, yl = yh + DR_TILE, ph = yh + DR_P, pl = ph + DR_TILE;
+    const float* vec = reinterpret_cast<const float*>(smem + buf * STAGE + KQ + DR_VEC);
     const uint32_t vb = smem_u32(vbuf + buf * DR_VTILE), db = smem_u32(vbuf + (2 + buf) * DR_VTILE);
     const int64_t blk = (int64_t)(sq.chunk0 + n) * a.hv + h;
 
@@ -441,7 +438,6 @@ struct GradArgs {
   const DrChunk* chunks;
   const uint8_t* kq;
   const uint8_t* blk;
-  int blk_bytes;
   const float* tok;
   const float *keep_s, *keep_e, *keep_ds, *keep_z, *w_part, *b_part, *x_part;
 };
@@ -544,7 +540,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   for (int hr = 0; hr < rep; ++hr) {
     const int h = hq * rep + hr;
     const int64_t blk = (int64_t)ci * a.hv + h;
-    const float* vec = reinterpret_cast<const float*>(a.blk + blk * a.blk_bytes + 3 * DR_TILE);
+    const float* vec = reinterpret_cast<const float*>(a.blk + blk * DR_BLK + DR_VEC);
     // the gates' sums of the two passes (a quarter of the channel slices to each 64 threads) and the head's vectors:
     // every load is issued before the first is waited for
     const int tok = tid & (DR_C - 1), grp = tid >> 6;

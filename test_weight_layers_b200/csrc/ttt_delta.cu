@@ -18,7 +18,6 @@ struct DeltaWs {
   DrChunk* chunks;
   uint8_t* kq;
   uint8_t* blk;
-  int blk_bytes;
   int64_t max_chunks;
   int seg_chunks, max_segs;  // chunks of a segment (0: sequences are not cut)
   float *seg_s, *seg_n, *phi_scale;
@@ -92,7 +91,6 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
     return p;
   };
   w.max_chunks = T / DR_C + n_seq;
-  w.blk_bytes = DR_HBLK + (backward ? DR_TILE : 0);
   w.seg_chunks = seg_chunks(d, T, n_seq, dt);
   w.max_segs = n_seq + (w.seg_chunks ? (int)(w.max_chunks / w.seg_chunks) : 0);
   w.status = reinterpret_cast<unsigned int*>(take(256));
@@ -101,7 +99,7 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
   w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
   if (dt == TTT_BF16) {
     w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
-    w.blk = take((size_t)w.max_chunks * d.heads_v * w.blk_bytes);
+    w.blk = take((size_t)w.max_chunks * d.heads_v * DR_BLK);
   }
   if (segs_room) {
     const size_t segs = segs_room * d.heads_v, dkp = dk_pad(d.dk);
@@ -211,7 +209,7 @@ int run_scan(const StateArgs& sa, const DeltaWs& w, cudaStream_t s) {
   if (!w.seg_chunks) return TTT_OK;
   const int warps = pass_warps<DK>(false);
   TTT_TRY((launch_pass<k_delta_state<DK, PASS_SCAN>>(sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
-                                                   warps + 1, state_smem<DK, false>(warps), s)));
+                                                   warps + 1, state_smem<DK, PASS_SCAN>(warps), s)));
   return launch_join<DK, false>(sa, w.seg_s, w, s);
 }
 
@@ -230,7 +228,7 @@ int run_delta_fwd(const PrepArgs& pa, StateArgs sa, const DeltaWs& w, cudaStream
   const int warps = pass_warps_for(pass_warps<DK>(false), sa.dv);
   return launch_pass<k_delta_state<DK, PASS_OUT>>(sa, w.max_segs, blocks_of(sa.dv, warps),
                                                   state_split<DK, PASS_OUT>() ? 2 * warps : warps + 1,
-                                                  state_out_smem<DK>(warps), s);
+                                                  state_smem<DK, PASS_OUT>(warps), s);
 }
 
 template <int DK>
@@ -238,7 +236,7 @@ int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra
                   cudaStream_t s) {
   TTT_TRY((launch_prep<DK, true>(pa, w, s)));
   TTT_TRY(run_scan<DK>(sa, w, s));
-  const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, true>(warps, true);
+  const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, PASS_BACK>(warps, true);
   const int64_t blocks = blocks_of(sa.dv, warps);
   TTT_TRY((launch_pass<k_delta_state<DK, PASS_BACK>>(sa, w.max_segs, blocks, warps + 1, smem, s)));
   if (w.seg_chunks) {  // the transitions are the state pass's, transposed
@@ -328,7 +326,6 @@ PrepArgs prep_args(const void* Q, const void* K, const float* g, const float* be
   a.chunks = w.chunks;
   a.kq = w.kq;
   a.blk = w.blk;
-  a.blk_bytes = w.blk_bytes;
   a.tok = w.tok;
   return a;
 }
@@ -346,7 +343,6 @@ void pass_args(Args& a, const void* V, const ttt_delta_dims& d, const DeltaIo& x
   a.seqs = w.seqs;
   a.kq = w.kq;
   a.blk = w.blk;
-  a.blk_bytes = w.blk_bytes;
   a.guard = Guard{w.status, wait_timeout_ns()};
   a.keep_e = w.keep_e;
   a.w_part = w.w_part;
@@ -474,7 +470,6 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
   ga.chunks = w.chunks;
   ga.kq = w.kq;
   ga.blk = w.blk;
-  ga.blk_bytes = w.blk_bytes;
   ga.tok = w.tok;
   ga.keep_s = w.keep_s;
   ga.keep_e = w.keep_e;

@@ -1,0 +1,103 @@
+"""What the chunked gated delta rule keeps of its operands' precision, on the GPU against the fp64 oracle.
+
+Tolerances, from the arithmetic (c terms of a sum, M the sum of their magnitudes):
+  - a product of split operands drops 2^-22 of an operand twice and the product of the low parts once, and its sum
+    loses 2^-24 per term: SUM(c) = 3 * 2^-22 + c * 2^-24, relative to M; a bf16 output adds half a step, 2^-8.
+  - a value off by d before it is rounded to bf16 is rounded to another one with probability |d| / step, and is then
+    off by a step of 2^-7 of the value at most: against the rounded oracle the relative Frobenius error is
+    sqrt(2^-7 * d).  Outputs that keep 11 bits of their operands are at 1e-3 there.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import delta_oracle as D
+from test_gpu_delta import TOL_S, Seqs
+from test_weight_layers_b200 import ttt as T
+
+from _gpu import f64, need_gpu, rel_fro
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def SUM(c):
+    return 3 * 2 ** -22 + c * 2 ** -24
+
+
+def flip(d):
+    return (2 ** -7 * d) ** 0.5
+
+
+def rounded(x):
+    return f64(torch.from_numpy(np.ascontiguousarray(x)).bfloat16())
+
+
+def overwritten(n, dk, dv, seed):
+    """One key, written again and again: a large value first, then values of about one."""
+    c = Seqs([n], 1, 1, dk, dv, seed=seed, s0=False, decay=0.0)
+    c.K[:] = c.K[0].clone()
+    c.V[:] = c.V.float().sign().bfloat16()
+    c.V[0] *= 1000
+    c.beta[:] = 0.9983
+    c.scale = 1.0
+    return c
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 40), (192, 64), (256, 64)])
+@pytest.mark.parametrize("n", [40, 41, 200])
+def test_output_of_an_overwritten_key(n, dk, dv):
+    # o = P U: two writes of about 1000 of opposite signs, then what is left of them
+    c = overwritten(n, dk, dv, dk)
+    c.Q = c.K.clone()
+    O, S, _ = c.forward()
+    at, args = c._seq(0)
+    o, _ = D.delta_rule(*args, 1, 1, c.scale)
+    assert np.all(np.abs(f64(O) - o) <= 2 ** -8 * np.abs(o) + SUM(64 + dk) * 2100)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (192, 64), (256, 64)])
+@pytest.mark.parametrize("n", [40, 41, 200])
+def test_output_where_a_large_state_is_overwritten(n, dk, dv):
+    # o = e^c S q + P U: the state's read of about 1000 against the write that replaces it
+    c = overwritten(n, dk, dv, dk + 1)
+    c.Q = c.K.clone()
+    c.V[0] /= 1000
+    k = c.K[0].float()
+    c.S0 = (1000 * k / k.norm()).expand(1, 1, dv, dk).contiguous()
+    O, S, _ = c.forward()
+    at, args = c._seq(0)
+    o, _ = D.delta_rule(*args, 1, 1, c.scale)
+    assert np.all(np.abs(f64(O) - o) <= 2 ** -8 * np.abs(o) + SUM(64 + dk) * 2100)
+
+
+# lens, heads_qk, heads_v, dk, dv
+ROUNDED = [([300, 41], 1, 2, 64, 64), ([200], 2, 4, 128, 128), ([200, 77], 1, 1, 192, 192), ([150], 1, 2, 256, 72),
+           ([5000], 1, 1, 64, 64), ([90], 1, 1, 40, 24)]
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", ROUNDED)
+def test_outputs_are_the_rounded_ones(lens, hk, hv, dk, dv):
+    c = Seqs(lens, hk, hv, dk, dv, seed=dk + 7)
+    O, S, _ = c.forward()
+    ref = np.concatenate([D.delta_rule(*c._seq(i)[1], hk, hv, c.scale)[0] for i in range(c.N)])
+    assert rel_fro(f64(O), rounded(ref)) < flip(TOL_S / 3)
+
+
+def test_states_and_gates_keep_what_is_stated():
+    # dk = dv = 128: eight steps of 16 terms twice (leading and low parts) for each of a chunk's three products, each
+    # step cutting off 2^-24 of the sum: 48 * 2^-24, and the operands' 3 * 2^-22 a product
+    c = Seqs([640, 333], 2, 4, 128, 128, seed=33)
+    tol = 48 * 2 ** -24 + 9 * 2 ** -22
+    _, S, _ = c.forward()
+    ref = np.stack([D.delta_rule(*c._seq(i)[1], 2, 4, c.scale)[1] for i in range(2)])
+    assert rel_fro(f64(S), ref) < tol
+    out, _ = c.backward()
+    refs = [D.delta_rule_grad(*c._seq(i)[1], f64(c.dO[c._seq(i)[0]]), f64(c.dS[i]), 2, 4, c.scale) for i in range(2)]
+    assert rel_fro(f64(out["dS0"]), np.stack([r["dS0"] for r in refs])) < tol
+    for k in ("dg", "dbeta"):
+        assert rel_fro(f64(out[k]), np.concatenate([r[k] for r in refs])) < 2 * tol, k
