@@ -16,7 +16,8 @@
 // lo = fp16(x - hi), after its row is scaled by a power of two to [2^12, 2^13):
 // what is dropped is below 2^-22 of an element and 2^-36 of the row.  A token operand
 // times an fp32 one takes 2 products (hi, lo), two fp32 ones 3 (hi hi, lo hi,
-// hi lo).  bf16 pieces would need 3 and 6 for the same precision.
+// hi lo).  bf16 pieces would need 3 and 6 for the same precision.  The per-chunk
+// gradients, which have no scales at hand, take TF32 parts in the same way.
 #pragma once
 
 #include "common.cuh"

@@ -422,13 +422,15 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
 
 // ---------------------------------------------------------------------------
 // dQ, dK and the gates: one block per (chunk, query/key head), over the value
-// heads that share it.  What leaves here is rounded to bf16 (the gates' gradients
-// are sums of what the two passes kept), so the products take fp32 operands as
-// they lie in memory through TF32 (11 significant bits, no scaling): A operands
-// and the intra-chunk tiles rounded, S, dS' and E, whose conversion would be a
-// quarter of the instructions, cut off by the hardware (4e-4 at most on average,
-// against 2e-3 for the outputs' rounding).  32 value channels at a time are
-// copied in while the 32 before are multiplied.
+// heads that share it.  The products take fp32 operands as they lie in memory in
+// two TF32 parts (no scaling: TF32 has fp32's range), three products for each,
+// two where an operand is exact (dO, K16, Q16); the factors of token rows go to
+// the other operand.  One part each is 2.5 times fewer products (packed
+// documents 279 us instead of 440), but keeps 2^-11 of the terms where they
+// cancel, as behind a key that is written again.  32 value channels at a time
+// are copied in while the 32 before are multiplied.
+// Bound by the tensor cores and one block's phases on an SM (252 registers):
+// 56% tensor pipe, 0.31 issue slots.
 struct GradArgs {
   const __nv_bfloat16 *dO;
   int64_t ldo, ldq, ldk;
@@ -447,11 +449,23 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// fp32 -> TF32, rounded to nearest
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
+// x = hi + lo in two TF32 parts (what the products drop of lo is below 2^-21 of x)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void split_tf32(float x0, float x1, float x2, float x3, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split_tf32(x0, hi[0], lo[0]);
+  split_tf32(x1, hi[1], lo[1]);
+  split_tf32(x2, hi[2], lo[2]);
+  split_tf32(x3, hi[3], lo[3]);
+}
+// A in two parts times B in two parts (h0, h1), (l0, l1)
+__device__ __forceinline__ void mma_tf32x3(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t h0,
+                                           uint32_t h1, uint32_t l0, uint32_t l1) {
+  mma_tf32(c, lo, h0, h1);
+  mma_tf32(c, hi, l0, l1);
+  mma_tf32(c, hi, h0, h1);
 }
 
 constexpr int GR_V = 32;     // value channels of a tile
@@ -474,7 +488,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   constexpr int LDS = DK + 8, STAGE = grad_stage<DK>();
   constexpr int KQ_BYTES = 2 * DR_C * LDS * 4;
   constexpr int NH = DK / 16;  // n-tiles of a warp's half of the dk columns
-  float* Km = reinterpret_cast<float*>(smem);  // K~ [64][LDS] and Q~, once the tiles are done
+  float* Km = reinterpret_cast<float*>(smem);  // K16 [64][LDS] and Q16, once the tiles are done
   float* Qm = Km + DR_C * LDS;
   float* Fm = reinterpret_cast<float*>(smem + (2 * STAGE > KQ_BYTES ? 2 * STAGE : KQ_BYTES));  // F [64][GR_LDA]
   float* Wm = Fm + DR_C * GR_LDA;                                                              // W
@@ -612,33 +626,40 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
         const float z2 = Zm[(kk + t + 4) * GR_LDT + r0], z3 = Zm[(kk + t + 4) * GR_LDT + r0 + 8];
         const float u0 = Em[(kk + t) * GR_LDT + r0], u1 = Em[(kk + t) * GR_LDT + r0 + 8];
         const float u2 = Em[(kk + t + 4) * GR_LDT + r0], u3 = Em[(kk + t + 4) * GR_LDT + r0 + 8];
-        const uint32_t oa[4] = {__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(o2), __float_as_uint(o3)};
-        const uint32_t za[4] = {tf32(z0), tf32(z1), tf32(z2), tf32(z3)};
-        const uint32_t oe[4] = {tf32(o0 * ec0), tf32(o1 * ec1), tf32(o2 * ec0), tf32(o3 * ec1)};
-        const uint32_t ze[4] = {tf32(z0 * bc0), tf32(z1 * bc1), tf32(z2 * bc0), tf32(z3 * bc1)};
-        const uint32_t ue[4] = {tf32(u0 * bl0), tf32(u1 * bl1), tf32(u2 * bl0), tf32(u3 * bl1)};
+        uint32_t h0, h1, l0, l1;
         if (ch * 32 <= rg * 16 + 15) {
+          const uint32_t oa[4] = {__float_as_uint(o0), __float_as_uint(o1), __float_as_uint(o2), __float_as_uint(o3)};
+          uint32_t zh[4], zl[4];
+          split_tf32(z0, z1, z2, z3, zh, zl);
 #pragma unroll
           for (int n = 0; n < 4; ++n) {  // F, W: columns j = 32 ch + 8 n + g
             const int j = ch * 32 + n * 8 + g;
-            const uint32_t b0 = __float_as_uint(Em[(kk + t) * GR_LDT + j]), b1 = __float_as_uint(Em[(kk + t + 4) * GR_LDT + j]);
-            mma_tf32(f[n], oa, b0, b1);
-            mma_tf32(wm[n], za, b0, b1);
+            split_tf32(Em[(kk + t) * GR_LDT + j], h0, l0);
+            split_tf32(Em[(kk + t + 4) * GR_LDT + j], h1, l1);
+            mma_tf32(f[n], oa, l0, l1);  // (dO is exact)
+            mma_tf32x3(wm[n], zh, zl, h0, h1, l0, l1);
+            mma_tf32(f[n], oa, h0, h1);
           }
         }
+        uint32_t oh[4], ol[4], zh[4], zl[4], uh[4], ul[4];
+        split_tf32(o0 * ec0, o1 * ec1, o2 * ec0, o3 * ec1, oh, ol);
+        split_tf32(z0 * bc0, z1 * bc1, z2 * bc0, z3 * bc1, zh, zl);
+        split_tf32(u0 * bl0, u1 * bl1, u2 * bl0, u3 * bl1, uh, ul);
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
           const int c = ch * (DK / 2) + n * 8 + g;
-          const uint32_t b0 = __float_as_uint(Sm[(kk + t) * LDS + c]), b1 = __float_as_uint(Sm[(kk + t + 4) * LDS + c]);
-          const uint32_t e0 = __float_as_uint(Dm[(kk + t) * LDS + c]), e1 = __float_as_uint(Dm[(kk + t + 4) * LDS + c]);
-          mma_tf32(q[n], oe, b0, b1);
-          mma_tf32(k[n], ze, b0, b1);
-          mma_tf32(k[n], ue, e0, e1);
+          split_tf32(Sm[(kk + t) * LDS + c], h0, l0);
+          split_tf32(Sm[(kk + t + 4) * LDS + c], h1, l1);
+          mma_tf32x3(q[n], oh, ol, h0, h1, l0, l1);
+          mma_tf32x3(k[n], zh, zl, h0, h1, l0, l1);
+          split_tf32(Dm[(kk + t) * LDS + c], h0, l0);
+          split_tf32(Dm[(kk + t + 4) * LDS + c], h1, l1);
+          mma_tf32x3(k[n], uh, ul, h0, h1, l0, l1);
         }
       }
       __syncthreads();  // the stage is read
     }
-    // F and -W with their decays, gates and masks, rounded for the products
+    // F and -W with their decays, gates and masks
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int j = ch * 32 + n * 8 + 2 * t;
@@ -646,11 +667,11 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p >> 1) * 8, jj = j + (p & 1);
         const float d = jj <= i ? expf(vc[i] - vc[jj]) * vc[DR_C + jj] : 0.f;
-        Fm[i * GR_LDA + jj] = __uint_as_float(tf32(jj <= i ? d * f[n][p] : 0.f));
-        Wm[i * GR_LDA + jj] = __uint_as_float(tf32(jj < i ? -d * vc[DR_C + i] * wm[n][p] : 0.f));
+        Fm[i * GR_LDA + jj] = jj <= i ? d * f[n][p] : 0.f;
+        Wm[i * GR_LDA + jj] = jj < i ? -d * vc[DR_C + i] * wm[n][p] : 0.f;
       }
     }
-    // K~ = f_k K16, Q~ = f_q Q16
+    // K16, Q16 (exact; their rows' factors go to the other operand)
     const uint8_t* kq = a.kq + ((int64_t)ci * a.hk + hq) * (2 * DR_C * DK * 2);
     {
       uint4 raw[DK / 16];  // 2 x 64 rows of DK / 8 pieces, all in flight
@@ -660,13 +681,10 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       for (int n = 0; n < DK / 16; ++n) {
         const int i = tid + n * 256, isq = n >= DK / 32;  // pieces as they lie: swizzled within the row
         const int r = i / (DK / 8) - isq * DR_C, c = (i % (DK / 8)) ^ (r & 7);
-        const float fs = tfs[(isq ? TF_FQ : TF_FK) * DR_C + r];
         float* dst = (isq ? Qm : Km) + r * LDS + c * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 y = unpack_f16x2((&raw[n].x)[j]);
-          *reinterpret_cast<float2*>(dst + 2 * j) =
-              make_float2(__uint_as_float(tf32(y.x * fs)), __uint_as_float(tf32(y.y * fs)));
+          *reinterpret_cast<float2*>(dst + 2 * j) = unpack_f16x2((&raw[n].x)[j]);
         }
       }
     }
@@ -699,34 +717,39 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       a.dg[at] = expf(vc[DR_C - 1]) * d + x_sum + (all - before);
       a.dbeta[at] = b_sum;
     }
-    // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~
+    // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~ with K~_j = f_k(j) K16_j, Q~_j = f_q(j) Q16_j
     auto bits = [](float x) { return __float_as_uint(x); };
+    auto mma2 = [](float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t b0, uint32_t b1) {
+      mma_tf32(c, lo, b0, b1);
+      mma_tf32(c, hi, b0, b1);
+    };
 #pragma unroll 2
     for (int kk = 0; kk < DR_C; kk += 8) {
       const bool lower = kk <= rg * 16 + 15, upper = kk + 7 >= rg * 16;  // tiles of F, W and of their transposes
-      uint32_t fa[4], wa[4], ft[4], wt[4];
+      uint32_t fa[4], wa[4], ft[4], wt[4], fal[4], wal[4], ftl[4], wtl[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p & 1) * 8, j = kk + t + (p >> 1) * 4;
-        fa[p] = bits(Fm[i * GR_LDA + j]);
-        wa[p] = bits(Wm[i * GR_LDA + j]);
-        ft[p] = bits(Fm[j * GR_LDA + i]);
-        wt[p] = bits(Wm[j * GR_LDA + i]);
+        const float fk = tfs[TF_FK * DR_C + j], fq = tfs[TF_FQ * DR_C + j];
+        split_tf32(Fm[i * GR_LDA + j] * fk, fa[p], fal[p]);
+        split_tf32(Wm[i * GR_LDA + j] * fk, wa[p], wal[p]);
+        split_tf32(Fm[j * GR_LDA + i] * fq, ft[p], ftl[p]);
+        split_tf32(Wm[j * GR_LDA + i] * fk, wt[p], wtl[p]);
       }
       const float *k0 = Km + (kk + t) * LDS + ch * (DK / 2) + g, *q0 = Qm + (kk + t) * LDS + ch * (DK / 2) + g;
       if (lower) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
           const uint32_t b0 = bits(k0[n * 8]), b1 = bits(k0[n * 8 + 4 * LDS]);
-          mma_tf32(q[n], fa, b0, b1);
-          mma_tf32(k[n], wa, b0, b1);
+          mma2(q[n], fa, fal, b0, b1);
+          mma2(k[n], wa, wal, b0, b1);
         }
       }
       if (upper) {
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-          mma_tf32(k[n], wt, bits(k0[n * 8]), bits(k0[n * 8 + 4 * LDS]));
-          mma_tf32(k[n], ft, bits(q0[n * 8]), bits(q0[n * 8 + 4 * LDS]));
+          mma2(k[n], wt, wtl, bits(k0[n * 8]), bits(k0[n * 8 + 4 * LDS]));
+          mma2(k[n], ft, ftl, bits(q0[n * 8]), bits(q0[n * 8 + 4 * LDS]));
         }
       }
     }
@@ -734,7 +757,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
     if (hr + 1 < rep) load_tile((hr + 1) * ntiles);
   }
 
-  // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)) with K16 = K~ / f_k (p_k = 0 for a zero row), the dot
+  // back through the norms: dk = h_k (dk~ - p_k K16 (K16 . dk~)) (p_k = 0 where nothing is normalised), the dot
   // over both column halves; the rows leave through shared memory, 16 bytes a store
   float* dots = part;  // [2 halves][2][64]
   __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(Fm);
@@ -761,9 +784,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const int row = r0 + 8 * p;
-      const float f = tfs[(isq ? TF_FQ : TF_FK) * DR_C + row], hs = tfs[(isq ? TF_HQ : TF_HK) * DR_C + row];
-      const float pf = f != 0.f ? tfs[(isq ? TF_PQ : TF_PK) * DR_C + row] / f / f : 0.f;
-      const float dot = (dots[isq * DR_C + row] + dots[(2 + isq) * DR_C + row]) * pf;
+      const float hs = tfs[(isq ? TF_HQ : TF_HK) * DR_C + row];
+      const float dot = (dots[isq * DR_C + row] + dots[(2 + isq) * DR_C + row]) * tfs[(isq ? TF_PQ : TF_PK) * DR_C + row];
       const float* x = (isq ? Qm : Km) + row * LDS + ch * (DK / 2) + 2 * t;
       __nv_bfloat16* out = rows + row * LDR + ch * (DK / 2) + 2 * t;
 #pragma unroll

@@ -75,6 +75,25 @@ def test_output_where_a_large_state_is_overwritten(n, dk, dv):
     assert np.all(np.abs(f64(O) - o) <= 2 ** -8 * np.abs(o) + SUM(64 + dk) * 2100)
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (192, 72), (256, 64)])
+def test_gradients_of_an_overwritten_key(dk, dv):
+    # dq = scale S^T dO with S = the sum of writes of about 1000 that leave about one; the same sums are in dk
+    c = overwritten(200, dk, dv, dk + 2)
+    c.l2 = c.io.qk_l2norm = 0
+    c.K /= c.K[0].float().norm()
+    c.Q /= 8
+    out, _ = c.backward()
+    at, args = c._seq(0)
+    z = f64(c.dS[0])
+    ref = D.delta_rule_grad(*args, f64(c.dO), z, 1, 1, c.scale, False)
+    # terms: sums of |U| of 2100 at most per channel, times |dO| in dq; in dk also times |dS|, which reaches every token
+    of_do = np.abs(f64(c.dO)).sum(-1, keepdims=True)
+    for name, size in (("dq", of_do), ("dk", of_do + of_do.max() + np.abs(z).sum())):
+        err = np.linalg.norm(f64(out[name]) - ref[name], axis=-1, keepdims=True)
+        most = 2 ** -8 * np.linalg.norm(ref[name], axis=-1, keepdims=True) + SUM(64 + dv) * 2100 * size
+        assert np.all(err <= most), (name, float((err / most).max()))
+
+
 # lens, heads_qk, heads_v, dk, dv
 ROUNDED = [([300, 41], 1, 2, 64, 64), ([200], 2, 4, 128, 128), ([200, 77], 1, 1, 192, 192), ([150], 1, 2, 256, 72),
            ([5000], 1, 1, 64, 64), ([90], 1, 1, 40, 24)]
@@ -86,6 +105,17 @@ def test_outputs_are_the_rounded_ones(lens, hk, hv, dk, dv):
     O, S, _ = c.forward()
     ref = np.concatenate([D.delta_rule(*c._seq(i)[1], hk, hv, c.scale)[0] for i in range(c.N)])
     assert rel_fro(f64(O), rounded(ref)) < flip(TOL_S / 3)
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", ROUNDED)
+def test_gradients_are_the_rounded_ones(lens, hk, hv, dk, dv):
+    # dq, dk: two more products in a row than the states' three give
+    c = Seqs(lens, hk, hv, dk, dv, seed=dk + 8)
+    out, _ = c.backward()
+    refs = [D.delta_rule_grad(*c._seq(i)[1], f64(c.dO[c._seq(i)[0]]), f64(c.dS[i]), hk, hv, c.scale)
+            for i in range(c.N)]
+    for k in ("dq", "dk", "dv"):
+        assert rel_fro(f64(out[k]), rounded(np.concatenate([r[k] for r in refs]))) < flip(TOL_S), k
 
 
 def test_states_and_gates_keep_what_is_stated():
