@@ -38,8 +38,9 @@ enum {
   DV_PS = 4,    // inverse row scale of P
   DV_AK = 5,    // e^{c_C - c_j} f_k : factor of U in S'
   DV_EG = 6,    // e^{c_C} (64 times)
-  DV_C = 7,     // c_j
-  DR_NVEC = 8
+  DV_C = 7,     // c_j, and what fp32 leaves of it (differences of far-off c's keep their digits)
+  DV_CLO = 8,
+  DR_NVEC = 9
 };
 // A value head's chunk block: Y hi | Y lo | vectors | P hi | P lo.  The scan takes what stands before P.
 constexpr int DR_VEC = 2 * DR_TILE;                          // byte offset of the vectors

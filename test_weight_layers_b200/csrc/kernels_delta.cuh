@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
         vec[DV_AK * DR_C + i] = el * fki;
         vec[DV_EG * DR_C + i] = expf((float)G);
         vec[DV_C * DR_C + i] = (float)cii;
+        vec[DV_CLO * DR_C + i] = (float)(cii - (double)(float)cii);
       }
     }
     __syncthreads();

@@ -479,7 +479,7 @@ constexpr int grad_stage() {  // S, dS' | E, Z | dO
 template <int DK>
 constexpr int grad_smem() {
   constexpr int stages = 2 * grad_stage<DK>(), kq = 2 * DR_C * (DK + 8) * 4;  // K~, Q~ take the stages' place
-  return (stages > kq ? stages : kq) + (2 * DR_C * GR_LDA + 4 * DR_C + 16 + 8 * DR_C + TF_N * DR_C) * 4;
+  return (stages > kq ? stages : kq) + (2 * DR_C * GR_LDA + 5 * DR_C + 16 + 8 * DR_C + TF_N * DR_C) * 4;
 }
 
 template <int DK>
@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
   float* Qm = Km + DR_C * LDS;
   float* Fm = reinterpret_cast<float*>(smem + (2 * STAGE > KQ_BYTES ? 2 * STAGE : KQ_BYTES));  // F [64][GR_LDA]
   float* Wm = Fm + DR_C * GR_LDA;                                                              // W
-  float* vc = Wm + DR_C * GR_LDA;  // c, beta, beta e^c, beta e^{c_C - c} of the value head
-  float* red = vc + 4 * DR_C;        // [16]
+  float* vc = Wm + DR_C * GR_LDA;  // c, beta, beta e^c, beta e^{c_C - c} of the value head, c's low part
+  float* red = vc + 5 * DR_C;        // [16]
   float* part = red + 16;            // [2][4][64] partial sums of w and E.Z
   float* tfs = part + 8 * DR_C;      // the token factors (TF_*)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       b4[i] = p < n16 ? a.b_part[(blk * n16 + p) * DR_C + tok] : 0.f;
     }
     if (lane < n16) x_sum = a.x_part[blk * n16 + lane];
-    const float c_in = vec[DV_C * DR_C + tok], G = vec[DV_C * DR_C + DR_C - 1], be = vec[DV_BETA * DR_C + tok];
+    const float c_in = vec[DV_C * DR_C + tok], c_lo = vec[DV_CLO * DR_C + tok], be = vec[DV_BETA * DR_C + tok];
+    const float G = vec[DV_C * DR_C + DR_C - 1], G_lo = vec[DV_CLO * DR_C + DR_C - 1];
     float w = (w4[0] + w4[1]) + (w4[2] + w4[3]), b = (b4[0] + b4[1]) + (b4[2] + b4[3]);
     for (int p = grp + 16; p < n16; p += 4) {
       w += a.w_part[(blk * n16 + p) * DR_C + tok];
@@ -581,7 +582,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       vc[tid] = c_in;
       vc[DR_C + tid] = be;
       vc[2 * DR_C + tid] = be * expf(c_in);
-      vc[3 * DR_C + tid] = be * expf(G - c_in);
+      vc[3 * DR_C + tid] = be * expf((G - c_in) + (G_lo - c_lo));
+      vc[4 * DR_C + tid] = c_lo;
     }
     if (hr == 0)
 #pragma unroll
@@ -666,7 +668,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int i = r0 + (p >> 1) * 8, jj = j + (p & 1);
-        const float d = jj <= i ? expf(vc[i] - vc[jj]) * vc[DR_C + jj] : 0.f;
+        const float d =
+            jj <= i ? expf((vc[i] - vc[jj]) + (vc[4 * DR_C + i] - vc[4 * DR_C + jj])) * vc[DR_C + jj] : 0.f;
         Fm[i * GR_LDA + jj] = jj <= i ? d * f[n][p] : 0.f;
         Wm[i * GR_LDA + jj] = jj < i ? -d * vc[DR_C + i] * wm[n][p] : 0.f;
       }

@@ -118,6 +118,19 @@ def test_gradients_are_the_rounded_ones(lens, hk, hv, dk, dv):
         assert rel_fro(f64(out[k]), rounded(np.concatenate([r[k] for r in refs]))) < flip(TOL_S), k
 
 
+@pytest.mark.parametrize("dk", [64, 256])
+def test_gradients_behind_many_resets(dk):
+    # the tokens behind 48 resets in a chunk, whose decays do not depend on them
+    c = Seqs([64], 1, 1, dk, 64, seed=31)
+    c.g[:48] = float("-inf")
+    out, _ = c.backward()
+    ref = D.delta_rule_grad(*c._seq(0)[1], f64(c.dO), f64(c.dS[0]), 1, 1, c.scale)
+    for k in ("dq", "dk", "dv"):
+        assert rel_fro(f64(out[k][48:]), rounded(ref[k][48:])) < flip(TOL_S), k
+    for k in ("dg", "dbeta"):
+        assert rel_fro(f64(out[k][48:]), ref[k][48:]) < 2 * TOL_S, k
+
+
 def test_states_and_gates_keep_what_is_stated():
     # dk = dv = 128: eight steps of 16 terms twice (leading and low parts) for each of a chunk's three products, each
     # step cutting off 2^-24 of the sum: 48 * 2^-24, and the operands' 3 * 2^-22 a product
