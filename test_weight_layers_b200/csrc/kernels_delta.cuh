@@ -404,9 +404,9 @@ __global__ void __launch_bounds__(128, 4) k_delta_prep(const PrepArgs a) {
     uint8_t* blk = a.blk + ((int64_t)ci * a.hv + h) * DR_BLK;
     float* vec = reinterpret_cast<float*>(blk + DR_VEC);
     // c in 64 bits: the exponents reach hundreds below zero, and only their differences count
-    // exp of less than -110 is zero in fp32: lower values (-inf: a reset) are taken as that, so that the sums of the
-    // tokens behind them keep their digits
-    double s = g_next < -110.f ? -110.0 : (double)g_next;
+    // lower values than -400 (-inf: a reset) are taken as that, so that the sums of the tokens behind them keep their
+    // digits: exp of it is zero in fp32 (below -104) even where gates behind it grow to fp32's largest (88)
+    double s = g_next < -400.f ? -400.0 : (double)g_next;
     const float b_now = b_next;
     if (tid < ch.len && hr + 1 < rep) {
       g_next = __ldg(a.g + gate0 + hr + 1);

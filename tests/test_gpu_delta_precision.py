@@ -131,6 +131,24 @@ def test_gradients_behind_many_resets(dk):
         assert rel_fro(f64(out[k][48:]), ref[k][48:]) < 2 * TOL_S, k
 
 
+@pytest.mark.parametrize("n", [40, 41, 64, 130])
+def test_a_reset_before_growth_leaves_nothing(n):
+    # g = -inf forgets the state whatever the gates behind it do with it
+    c = Seqs([n], 1, 1, 64, 64, seed=32)
+    c.beta[:] = 0
+    c.g[:] = 0
+    c.g[20] = float("-inf")
+    c.g[21:24] = 29.0
+    O, S, _ = c.forward()
+    assert torch.all(S == 0) and torch.all(O[20:] == 0) and torch.all(O[:20].abs().amax(-1) > 0)
+    c.dO[21:] = 0
+    out, _ = c.backward()
+    assert torch.all(out["dS0"].abs().amax() > 0)
+    c.dO[:20] = 0
+    out, _ = c.backward()
+    assert torch.all(out["dS0"] == 0)
+
+
 def test_states_and_gates_keep_what_is_stated():
     # dk = dv = 128: eight steps of 16 terms twice (leading and low parts) for each of a chunk's three products, each
     # step cutting off 2^-24 of the sum: 48 * 2^-24, and the operands' 3 * 2^-22 a product
