@@ -328,7 +328,7 @@ size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_
  *    (operands split in two fp16 parts; calls of up to 40 tokens on the CUDA
  *    cores); TTT_FP32: float Q, K, V, O, token by token on the CUDA cores (the
  *    precision check, and short sequences).
- *  - T up to 2^31 - 1. */
+ *  - T up to 2^31 - 65, n_seq up to 2^24 (TTT_ERR_UNSUPPORTED beyond). */
 int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
                       float* S, void* O, const int32_t* cu_seqlens, int n_seq, int64_t T, float scale,
                       ttt_delta_dims dims, const ttt_io_cfg* io, ttt_dtype dtype, void* ws, size_t ws_bytes,
@@ -340,8 +340,8 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
  * wanted) for the states before them.  Gradients of shared query/key heads are
  * summed over their value heads.  Stateless: the states are recomputed from the
  * inputs (workspace with backward = 1), nothing of the forward call is needed.
- * Rows outside the sequences are left as they are.  Deterministic.  TTT_BF16
- * only (TTT_FP32 returns TTT_ERR_UNSUPPORTED). */
+ * dO may be one of Q, K, V.  Rows outside the sequences are left as they are.
+ * Deterministic.  TTT_BF16 only (TTT_FP32 returns TTT_ERR_UNSUPPORTED). */
 int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, const float* g, const float* beta,
                                const float* S0, const void* dO, const float* dS, void* dQ, void* dK, void* dV,
                                float* dg, float* dbeta, float* dS0, const int32_t* cu_seqlens, int n_seq, int64_t T,

@@ -1,6 +1,7 @@
 // C ABI of the gated delta rule (see include/ttt.h for the contract): argument
 // checks, workspace carving and the launch sequences.
 #include <algorithm>
+#include <initializer_list>
 
 #include "host.cuh"
 #include "kernels_delta.cuh"
@@ -136,7 +137,7 @@ int check_rows(const void* p, int64_t ld, int64_t width, ttt_dtype dt) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Checks shared by the entry points; fills the row strides.
+// Checks shared by the entry points (O: the outputs' rows, or their gradient's); fills the row strides.
 int delta_check(const void* Q, const void* K, const void* V, const float* g, const float* beta, const void* O,
                 const ttt_delta_dims& d, const ttt_io_cfg* io, ttt_dtype dt, bool any_tokens, DeltaIo& out) {
   const int64_t nq = (int64_t)d.heads_qk * d.dk, nv = (int64_t)d.heads_v * d.dv;
@@ -151,8 +152,12 @@ int delta_check(const void* Q, const void* K, const void* V, const float* g, con
   TTT_TRY(check_rows(K, out.ldk, nq, dt));
   TTT_TRY(check_rows(V, out.ldv, nv, dt));
   TTT_TRY(check_rows(O, out.ldo, nv, dt));
-  if (!g || !beta || O == Q || O == K || O == V) return TTT_ERR_INVALID;
+  if (!g || !beta) return TTT_ERR_INVALID;
   return aligned4(g) && aligned4(beta) ? TTT_OK : TTT_ERR_ALIGN;
+}
+
+bool is_one_of(const void* out, std::initializer_list<const void*> in) {
+  return std::find(in.begin(), in.end(), out) != in.end();
 }
 
 // Opts kernel K in to all the shared memory a block can have, once per device.
@@ -386,7 +391,9 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
                       void* stream) {
   TTT_TRY(delta_check_call(dims, dtype, T, n_seq, cu_seqlens != nullptr, io, false, ws, ws_bytes));
   DeltaIo x;
-  TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, T > 0 && n_seq > 0, x));
+  const bool any = T > 0 && n_seq > 0;
+  TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, any, x));
+  if (any && is_one_of(O, {Q, K, V})) return TTT_ERR_INVALID;
   if ((S0 && !aligned16(S0)) || (S && !aligned16(S)) || !aligned4(cu_seqlens)) return TTT_ERR_ALIGN;
   if (n_seq == 0) return TTT_OK;
   cudaStream_t s = (cudaStream_t)stream;
@@ -433,7 +440,7 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
     TTT_TRY(check_rows(dV, x.ldv, (int64_t)dims.heads_v * dims.dv, dtype));
     if (!dg || !dbeta) return TTT_ERR_INVALID;
     for (const void* out : {(const void*)dQ, (const void*)dK, (const void*)dV})
-      if (out == Q || out == K || out == V || out == dO) return TTT_ERR_INVALID;
+      if (is_one_of(out, {Q, K, V, dO})) return TTT_ERR_INVALID;
   }
   if (n_seq == 0) return TTT_OK;
   cudaStream_t s = (cudaStream_t)stream;
@@ -496,6 +503,7 @@ int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, 
   DeltaIo x;
   TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, B > 0, x));
   if (B == 0) return TTT_OK;
+  if (is_one_of(O, {Q, K, V})) return TTT_ERR_INVALID;
   if (!S) return TTT_ERR_INVALID;
   if (!aligned16(S) || !aligned4(slots)) return TTT_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
