@@ -23,3 +23,20 @@ def test_the_outputs_gradient_may_be_the_values():
     out, ws = c.backward()
     assert T.ttt_poll_status(ws) == T.TTT_OK and all(torch.equal(out[k], want[k]) for k in out)
     c.check_backward(out)
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([70, 5], 1, 2, 64, 520), ([66], 1, 1, 40, 1024), ([30], 1, 1, 192, 1024),
+                                              ([900], 1, 1, 64, 520), ([100], 1, 1, 256, 544)])
+def test_many_value_channels(lens, hk, hv, dk, dv):
+    # more than 32 slices of 16 channels in the gates' sums
+    c = Seqs(lens, hk, hv, dk, dv, seed=dv)
+    c.check_forward(*c.forward()[:2])
+    c.check_backward(c.backward()[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_step_of_many_value_channels(dtype):
+    c = Seqs([1] * 3, 1, 1, 256, 1024, seed=41, dtype=dtype)
+    pool, O = c.S0.clone(), torch.zeros((3, 1024), dtype=dtype, device="cuda")
+    T.ttt_delta_step(c.Q, c.K, c.V, c.g, c.beta, pool, O, 3, c.dm, c.io, scale=c.scale)
+    c.check_forward(O, pool)
