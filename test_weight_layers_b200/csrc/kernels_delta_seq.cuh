@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
       x.fq = fminf(rsqrtf(p[1]), 1e12f);
     }
     x.fq *= a.scale;
-    x.kq = p[2];
+    // a row whose norm overflows has a factor of zero and counts as zero: its products may have overflowed too
+    x.kq = x.fk == 0.f || x.fq == 0.f ? 0.f : p[2];
     x.al = expf(x.g);
   };
   auto products = [&](const Token<E>& x, float* p) {  // S k and S q of this lane's columns
@@ -218,9 +219,10 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
       float out = 0.f;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        const float u = x.beta * (__shfl_sync(0xffffffffu, x.v, r) - x.al * (p[2 * r] * x.fk));
+        const float sk = x.fk == 0.f ? 0.f : p[2 * r] * x.fk;
+        const float u = x.beta * (__shfl_sync(0xffffffffu, x.v, r) - x.al * sk);
         const float uk = u * x.fk;
-        if (lane == r) out = x.fq * (x.al * p[2 * r + 1] + uk * x.kq);
+        if (lane == r) out = x.fq == 0.f ? 0.f : x.fq * (x.al * p[2 * r + 1] + uk * x.kq);
 #pragma unroll
         for (int i = 0; i < E; ++i) s[r][i] = x.al * s[r][i] + uk * x.k[i];
       }
@@ -267,9 +269,10 @@ __global__ void __launch_bounds__(128) k_delta_tokens(const SeqArgs<T> a) {
       factors(x, p + M);
       const float other = __shfl_xor_sync(0xffffffffu, p[0], LPI);
       const float sk = lane & LPI ? other : p[0], sq = lane & LPI ? p[0] : other;
-      const float uk = x.beta * (v - x.al * (sk * x.fk)) * x.fk;
+      const float uk = x.beta * (v - x.al * (x.fk == 0.f ? 0.f : sk * x.fk)) * x.fk;
       if (lane % (2 * LPI) == 0 && r0 + mine < a.dv)
-        store_one(a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + mine, x.fq * (x.al * sq + uk * x.kq));
+        store_one(a.O + tok * a.ldo + (int64_t)h * a.dv + r0 + mine,
+                  x.fq == 0.f ? 0.f : x.fq * (x.al * sq + uk * x.kq));
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         const float ur = __shfl_sync(0xffffffffu, uk, r * 2 * LPI);

@@ -40,3 +40,24 @@ def test_a_step_of_many_value_channels(dtype):
     pool, O = c.S0.clone(), torch.zeros((3, 1024), dtype=dtype, device="cuda")
     T.ttt_delta_step(c.Q, c.K, c.V, c.g, c.beta, pool, O, 3, c.dm, c.io, scale=c.scale)
     c.check_forward(O, pool)
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.bfloat16, 12), (torch.float32, 12), (torch.float32, 70)])
+@pytest.mark.parametrize("size", [1e25, 2e38])
+def test_rows_too_large_for_a_norm_count_as_zero(dtype, n, size):
+    # token by token the norms are summed in fp32: such keys write nothing, such queries read zero
+    c = Seqs([n], 1, 2, 64, 64, seed=42, dtype=dtype)
+    rows = torch.tensor([2, 3, 7], device="cuda"), torch.tensor([3, 5], device="cuda")
+    for t, at in ((c.K, rows[0]), (c.Q, rows[1])):
+        t[at] = (t[at].sign().float() * size).to(dtype)
+    O, S, _ = c.forward()
+    step_pool = c.S0.clone()
+    step_O = torch.zeros_like(O)
+    for t in range(n):
+        at = slice(t, t + 1)
+        T.ttt_delta_step(c.Q[at], c.K[at], c.V[at], c.g[at], c.beta[at], step_pool, step_O[at], 1, c.dm, c.io,
+                         scale=c.scale)
+    c.K[rows[0]] = 0
+    c.Q[rows[1]] = 0
+    c.check_forward(O, S)
+    c.check_forward(step_O, step_pool)
