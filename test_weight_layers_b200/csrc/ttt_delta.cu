@@ -504,6 +504,7 @@ int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, 
   TTT_TRY(delta_check(Q, K, V, g, beta, O, dims, io, dtype, B > 0, x));
   if (B == 0) return TTT_OK;
   if (is_one_of(O, {Q, K, V})) return TTT_ERR_INVALID;
+  if (n_slots == 0 && slots) return TTT_OK;  // every row is padding (and an empty pool may be NULL)
   if (!S) return TTT_ERR_INVALID;
   if (!aligned16(S) || !aligned4(slots)) return TTT_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;

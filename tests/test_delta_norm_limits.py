@@ -40,6 +40,14 @@ def test_outputs_on_inputs_are_refused(lib):
         assert lib.ttt_delta_step(*FAKE[:5], FAKE[6], 8, FAKE[10], FAKE[same], 4, 1.0, DM, io, T.TTT_BF16, None) == INV
 
 
+def test_an_empty_pool(lib):
+    # NULL is what an empty tensor has; every row is padding, so nothing is launched
+    step = lambda S, n, slots: lib.ttt_delta_step(  # noqa: E731
+        *FAKE[:5], S, n, slots, FAKE[7], 4, 1.0, DM, ctypes.byref(T.io_cfg()), T.TTT_BF16, None)
+    assert step(None, 0, FAKE[10]) == OK and step(FAKE[6], 0, FAKE[10]) == OK
+    assert step(None, 8, FAKE[10]) == INV and step(None, 0, None) == INV
+
+
 def test_the_largest_calls(lib):
     # the documented limits themselves are taken (stopped at Q's alignment), one more is not
     def fwd(t, n, cu=FAKE[10]):

@@ -61,3 +61,12 @@ def test_rows_too_large_for_a_norm_count_as_zero(dtype, n, size):
     c.Q[rows[1]] = 0
     c.check_forward(O, S)
     c.check_forward(step_O, step_pool)
+
+
+def test_a_pool_without_slots():
+    # every row is padding
+    c = Seqs([1] * 3, 1, 1, 64, 64, seed=43)
+    O = torch.full((3, 64), 77.0, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int32, device="cuda")
+    T.ttt_delta_step(c.Q, c.K, c.V, c.g, c.beta, c.S0[:0], O, 3, c.dm, c.io, slots=slots)
+    assert torch.all(O == 77)
