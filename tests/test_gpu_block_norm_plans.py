@@ -10,6 +10,7 @@ import torch
 
 from oracle import delta_oracle as D
 from test_gpu_block_norm import TOL, TOL_W, Rows
+from test_weight_layers_b200 import ttt as T
 
 from _gpu import f64, need_gpu, rel_fro
 
@@ -87,3 +88,82 @@ def test_rows_of_one_column():
             assert np.all(np.abs(out["dw_pre"] - ref["dw_pre"]) <= TOL_W * np.abs(dN).sum())
         else:
             assert np.all(out["dw_pre"] == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_groups_as_rows_with_a_residual(dtype):
+    # no second norm and no residual scale: the groups of strided rows are taken as rows of their own
+    c = Rows(601, 512, 128, dtype, pad=8, seed=12)
+    c.lam = c.w_pre = None
+    ref, _ = D.block_norm(f64(c.Y), *c.args())
+    Xo, _ = c.forward(n=False)
+    assert rel_fro(f64(Xo), ref) < TOL[dtype]
+    assert torch.all(Xo.as_strided((c.R - 1, c.pad), (c.W + c.pad, 1), Xo.storage_offset() + c.W) == 77)
+    X, Z, wp, lam, wn, group = c.args()
+    want = D.block_norm_grad(f64(c.Y), f64(c.dXo), None, X, Z, wp, lam, wn, group)
+    dy, dz, dx, dw = c.blank(), c.blank(), c.blank(), torch.zeros(128, device="cuda")
+    T.ttt_block_norm_backward(c.Y, c.dXo, dy, c.R, c.cfg, T.norm_workspace(c.R, c.cfg), X=c.X, Z=c.Z, w_post=c.w_post,
+                              dX=dx, dZ=dz, dw_post=dw)
+    for t, k in ((dy, "dy"), (dz, "dz"), (dx, "dx")):
+        assert rel_fro(f64(t), want[k]) < TOL[dtype], k
+    assert rel_fro(f64(dw), want["dw_post"]) < TOL_W
+
+
+@pytest.mark.parametrize("shape", [(650, 768, None), (650, 768, 192), (9, 2600, None), (650, 8192, None)])
+def test_every_output_on_an_input(shape):
+    c = Rows(*shape, dtype=torch.float32, seed=13)
+    Xo, N = c.forward()
+    y, z = c.Y.clone(), c.Z.clone()
+    T.ttt_block_norm(y, y, c.R, c.cfg, X=c.X, Z=z, w_post=c.w_post, res_scale=c.lam, w_pre=c.w_pre, N=z)
+    assert torch.equal(y, Xo) and torch.equal(z, N)
+    want = c.backward()
+    y, z, x = c.Y.clone(), c.Z.clone(), c.X.clone()
+    T.ttt_block_norm_backward(y, c.dXo, y, c.R, c.cfg, None, X=x, Z=z, w_post=c.w_post, res_scale=c.lam, w_pre=c.w_pre,
+                              dN=c.dN, dX=x, dZ=z)
+    assert torch.equal(y, want["dy"]) and torch.equal(z, want["dz"]) and torch.equal(x, want["dx"])
+
+
+def test_one_weight_gradient_at_a_time():
+    c = Rows(700, 768, None, seed=14)
+    want = c.backward()
+    ws = T.norm_workspace(c.R, c.cfg)
+    for arg, k in (("dw_post", "dw_post"), ("dres_scale", "dlam"), ("dw_pre", "dw_pre")):
+        out = torch.full((768,), 77.0, device="cuda")
+        T.ttt_block_norm_backward(c.Y, c.dXo, None, c.R, c.cfg, ws, X=c.X, Z=c.Z, w_post=c.w_post, res_scale=c.lam,
+                                  w_pre=c.w_pre, dN=c.dN, **{arg: out})
+        assert torch.equal(out, want[k]), k
+
+
+def test_two_gradients_at_once_and_in_two_graphs():
+    cs = [Rows(700, 768, None, seed=15), Rows(400, 2048, 256, seed=16)]
+    want = [c.backward() for c in cs]
+
+    def call(c, ws, out):
+        T.ttt_block_norm_backward(c.Y, c.dXo, out["dy"], c.R, c.cfg, ws, X=c.X, Z=c.Z, w_post=c.w_post,
+                                  res_scale=c.lam, w_pre=c.w_pre, dN=c.dN, dX=out["dx"], dZ=out["dz"],
+                                  dw_post=out["dw_post"], dres_scale=out["dlam"], dw_pre=out["dw_pre"])
+
+    wss = [T.norm_workspace(c.R, c.cfg) for c in cs]
+    outs = [{k: torch.zeros_like(t) for k, t in w.items()} for w in want]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, ws, out, st in zip(cs, wss, outs, streams):
+            with torch.cuda.stream(st):
+                call(c, ws, out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[k], w[k]) for o, w in zip(outs, want) for k in w)
+    graphs = []
+    for c, ws, out in zip(cs, wss, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c, ws, out)
+        for t in out.values():
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[k], w[k]) for o, w in zip(outs, want) for k in w)
