@@ -10,7 +10,10 @@
 // Scaling S by exp(g_t) at token t scales every later o and read error alike, so
 //     dg_t = <S~_t, dS~_t> = <S', dS'> + sum_{i >= t} (dO_i.O_i - dV_i.V_i)
 //     <S', dS'> = e^{c_C} <S, dS'> + sum_j U_j . e^{c_C - c_j} dS' k_j
-// with <S', dS'> taken at each chunk's end: no sum runs over more than a chunk.
+// with <S', dS'> taken at each chunk's end: no sum runs over more than a chunk.  Where dg is zero by itself (a token
+// that resets the state, or a chunk's first one behind a state of zeros) the sums of that chunk start there,
+//     dg_t = -sum_{a <= i < t} (...)_i for t >= a,   sum_{t <= i < a} (...)_i before it,
+// so that it is zero exactly and not a difference of sums.
 //
 // Passes: the chunk preparation and the state pass again (they keep S, E and
 // dO.O), the reverse pass over the chunks (dS in registers as the state pass
@@ -590,6 +593,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       for (int i = 0; i < 2; ++i)
         if (tid + i * 256 < TF_N * DR_C) tfs[tid + i * 256] = tf_in[i];
     float f[4][4], wm[4][4], sd = 0.f;  // F, W; this thread's part of <S, dS'>
+    uint32_t s_bits = 0;                // ... and what is set in its part of S
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -618,6 +622,7 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
         const int o = i / (DK / 4) * LDS + i % (DK / 4) * 4;
         const float4 x = *reinterpret_cast<const float4*>(Sm + o), y = *reinterpret_cast<const float4*>(Dm + o);
         sd += (x.x * y.x + x.y * y.y) + (x.z * y.z + x.w * y.w);
+        s_bits |= __float_as_uint(x.x) | __float_as_uint(x.y) | __float_as_uint(x.z) | __float_as_uint(x.w);
       }
 #pragma unroll
       for (int kk = 0; kk < GR_V; kk += 8) {
@@ -691,7 +696,8 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
         }
       }
     }
-    // <S, dS'> of the block, for the gates: dg_t = <S', dS'> + sum_{i >= t} w_i, dbeta = E.Z
+    // <S, dS'> of the block, for the gates: dg_t = <S', dS'> + sum_{i >= t} w_i (from the tokens where it is zero, if
+    // there are such), dbeta = E.Z
 #pragma unroll
     for (int m = 16; m; m >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, m);
     if (lane == 0) red[warp] = sd;
@@ -709,15 +715,33 @@ __global__ void __launch_bounds__(256, 1) k_delta_grad(const GradArgs a) {
       const float y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
-    if (tid < DR_C && lane == 31) red[8 + warp] = sum;
-    __syncthreads();
+    if (tid < DR_C) {
+      part[tid] = sum - w_sum;  // (of the warp's tokens before this one; this thread has read its sums there)
+      const float step = tid ? (vc[tid] - vc[tid - 1]) + (vc[4 * DR_C + tid] - vc[4 * DR_C + tid - 1]) : vc[0];
+      const uint32_t resets = __ballot_sync(0xffffffffu, expf(step) == 0.f);
+      if (lane == 31) red[8 + warp] = sum;
+      if (lane == 0) red[10 + warp] = __uint_as_float(resets);
+    }
+    const bool zero_state = !__syncthreads_or((s_bits << 1) != 0);
     if (tid < cu.len) {
-      float d = 0.f;
+      const float half = red[8];
+      auto before = [&](int t) { return part[t] + (t >= 32 ? half : 0.f); };
+      const unsigned long long zeros = __float_as_uint(red[10]) |
+                                       (unsigned long long)__float_as_uint(red[11]) << 32 | (zero_state ? 1ull : 0ull);
+      const unsigned long long upto = zeros & (~0ull >> (DR_C - 1 - tid));
+      float dg;
+      if (upto) {
+        dg = before(DR_C - 1 - __clzll(upto)) - before(tid);
+      } else if (zeros) {
+        dg = before(__ffsll(zeros) - 1) - before(tid);
+      } else {
+        float d = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d += red[i];
-      const float all = red[8] + red[9], before = (tid >= 32 ? red[8] : 0.f) + sum - w_sum;
+        for (int i = 0; i < 8; ++i) d += red[i];
+        dg = expf(vc[DR_C - 1]) * d + x_sum + ((half + red[9]) - before(tid));
+      }
       const int64_t at = (int64_t)(cu.tok + tid) * a.hv + h;
-      a.dg[at] = expf(vc[DR_C - 1]) * d + x_sum + (all - before);
+      a.dg[at] = dg;
       a.dbeta[at] = b_sum;
     }
     // dQ~ += F K~, dK~ += F^T Q~ - W K~ - W^T K~ with K~_j = f_k(j) K16_j, Q~_j = f_q(j) Q16_j

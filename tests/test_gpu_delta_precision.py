@@ -162,3 +162,34 @@ def test_states_and_gates_keep_what_is_stated():
     assert rel_fro(f64(out["dS0"]), np.stack([r["dS0"] for r in refs])) < tol
     for k in ("dg", "dbeta"):
         assert rel_fro(f64(out[k]), np.concatenate([r[k] for r in refs])) < 2 * tol, k
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (192, 40)])
+def test_gates_of_an_empty_state_have_no_gradient(dk, dv):
+    # dg_t is the product of the state before the token with its gradient: exactly zero without one
+    for s0 in (False, True):
+        c = Seqs([1, 1, 0, 1, 70], 1, 2, dk, dv, seed=34, s0=s0)
+        if s0:
+            c.S0.zero_()
+        out, _ = c.backward()
+        assert torch.all(out["dg"][:4] == 0) and torch.all(out["dg"][4:].abs().amax(-1) > 0)
+        c.check_backward(out)
+    c = Seqs([130], 1, 2, dk, dv, seed=35)
+    c.g[:] = float("-inf")
+    out, _ = c.backward()
+    assert torch.all(out["dg"] == 0)
+
+
+def test_gates_between_resets():
+    # resets at a chunk's first and last tokens, next to each other, on one of the heads only, and none
+    c = Seqs([260, 90], 1, 2, 64, 64, seed=36)
+    for t in (0, 20, 21, 63, 64, 100, 255, 259, 300):
+        c.g[t, 0] = float("-inf")
+    c.g[150] = -200.0
+    out, _ = c.backward()
+    c.check_backward(out)
+    assert torch.all(out["dg"][c.g < -104] == 0)
+    refs = [D.delta_rule_grad(*c._seq(i)[1], f64(c.dO[c._seq(i)[0]]), f64(c.dS[i]), 1, 2, c.scale) for i in range(2)]
+    ref = np.concatenate([r["dg"] for r in refs])
+    for h in range(2):
+        assert rel_fro(f64(out["dg"])[:, h], ref[:, h]) < 2 * TOL_S
