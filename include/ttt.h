@@ -341,7 +341,9 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
  * summed over their value heads.  Stateless: the states are recomputed from the
  * inputs (workspace with backward = 1), nothing of the forward call is needed.
  * dO may be one of Q, K, V.  Rows outside the sequences are left as they are.
- * Deterministic.  TTT_BF16 only (TTT_FP32 returns TTT_ERR_UNSUPPORTED). */
+ * Deterministic (as the forward call): the same call gives the same bits; a
+ * long sequence is cut into segments by the lengths of all sequences of a call,
+ * so that its last bits can depend on them.  TTT_BF16 only (TTT_FP32 returns TTT_ERR_UNSUPPORTED). */
 int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, const float* g, const float* beta,
                                const float* S0, const void* dO, const float* dS, void* dQ, void* dK, void* dV,
                                float* dg, float* dbeta, float* dS0, const int32_t* cu_seqlens, int n_seq, int64_t T,

@@ -48,9 +48,9 @@ constexpr int DR_P = DR_VEC + DR_NVEC * DR_C * 4;            // ... and of P
 constexpr int DR_BLK = DR_P + 2 * DR_TILE;
 
 // A sequence, or a segment of one: first token, tokens in it (-1: nothing to do), first chunk, the sequence's
-// number, the segment's number in it and how many it has.
+// number, the segment's number in it and how many it has, its number among the segments of cut sequences.
 struct DrSeq {
-  int tok, len, chunk0, id, seg, nseg, pad0, pad1;
+  int tok, len, chunk0, id, seg, nseg, cut, pad;
 };
 struct DrChunk {  // one chunk: first token, tokens in it (-1: unused entry)
   int tok, len;

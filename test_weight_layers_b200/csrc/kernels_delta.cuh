@@ -9,28 +9,62 @@ namespace ttt {
 
 // ---------------------------------------------------------------------------
 // Chunk table.  One block: checks the offsets (0 <= cu[i] <= cu[i+1] <= T), cuts
-// the sequences into segments of seg_chunks chunks (0: none is cut), and writes
-// the segments and each chunk's first token and length.  Refused offsets, or an
+// long sequences into segments (fill: sequences' passes that fit on the card; 0:
+// none is cut), and writes the segments, the two on each side of a cut once more by
+// themselves, and each chunk's first token and length.  Refused offsets, or an
 // error already recorded in the status word, mark every segment with length -1:
 // the kernels after it then write nothing.
-__global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu, int n_seq, int T, int seg_chunks,
-                                                     int max_segs, int max_chunks, DrSeq* __restrict__ seqs,
+//
+// Uncut, the passes take as long as the longest sequence.  Cut into segments of k
+// chunks they take about 3 k (the transitions are more rows than the states) and a
+// join for each, so the longest is cut where it is at least three times the card's
+// share of all chunks, k being that share; a join costs about as much as a chunk of
+// both passes, so neither many joins nor long segments: 2 k^2 >= chunks.
+constexpr int DR_CUT_CHUNKS = 12;  // shorter sequences are never cut
+__global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu, int n_seq, int T, int fill,
+                                                     int max_segs, int max_cuts, int max_chunks,
+                                                     DrSeq* __restrict__ seqs, DrSeq* __restrict__ cuts,
                                                      DrChunk* __restrict__ chunks, unsigned int* status) {
   __shared__ long long warp_sum[32];
+  __shared__ int warp_all[32], warp_max[32];
   __shared__ long long carry;
+  __shared__ int listed;
   __shared__ int order[1024], key[1024];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = *(volatile unsigned int*)status != DEV_OK;
   const int even = n_seq > 0 ? T / n_seq : 0;  // without offsets: sequences of equal length
-  if (cu)
+  int all = 0, most = 0;  // chunks of all sequences and of the longest one
+  if (cu) {
     for (int i = tid; i < n_seq; i += 1024) {
       const int a = cu[i], b = cu[i + 1];
       if (a < 0 || b < a || b > T) {
         bad = true;
         atomicCAS(status, (unsigned int)DEV_OK, (unsigned int)DEV_INVALID);
+      } else {
+        const int n = (b - a) / DR_C + ((b - a) % DR_C != 0);
+        all += n;
+        most = max(most, n);
       }
     }
+    all = __reduce_add_sync(0xffffffffu, all);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) warp_all[warp] = all, warp_max[warp] = most;
+  }
   bad = __syncthreads_or(bad);
+  int seg_chunks = 0;
+  if (fill) {
+    if (cu) {
+      all = __reduce_add_sync(0xffffffffu, warp_all[lane]);
+      most = __reduce_max_sync(0xffffffffu, warp_max[lane]);
+    } else {
+      most = (even + DR_C - 1) / DR_C;
+      all = most * n_seq;
+    }
+    if (most >= DR_CUT_CHUNKS && 3 * all <= (long long)fill * most) {
+      seg_chunks = (all + fill - 1) / fill;
+      while (2 * (long long)seg_chunks * seg_chunks < most) ++seg_chunks;
+    }
+  }
   // up to 1024 sequences are taken longest first, so that the passes' long blocks start early
   const bool sorted = cu && n_seq > 1 && n_seq <= 1024;
   if (sorted) {
@@ -55,7 +89,7 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
       }
     __syncthreads();
   }
-  if (tid == 0) carry = 0;
+  if (tid == 0) carry = listed = 0;
   __syncthreads();
   for (int i0 = 0; i0 < n_seq; i0 += 1024) {
     const int i = i0 + tid;
@@ -67,8 +101,9 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
     }
     const int n = len > 0 ? (len + DR_C - 1) / DR_C : 0;
     const int ns = i >= n_seq ? 0 : seg_chunks > 0 && n > 0 ? (n + seg_chunks - 1) / seg_chunks : 1;
-    const long long both = (long long)ns << 32 | n;  // segments and chunks, scanned together
-    long long sum = both;
+    // segments of cut sequences (up to 296), segments and chunks (each below 2^27), scanned together
+    const long long own = (long long)(ns > 1 ? ns : 0) << 54 | (long long)ns << 27 | n;
+    long long sum = own;
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
@@ -84,18 +119,25 @@ __global__ void __launch_bounds__(1024) k_delta_plan(const int* __restrict__ cu,
       warp_sum[lane] = w;
     }
     __syncthreads();
-    const long long first = carry + sum - both + (warp ? warp_sum[warp - 1] : 0);
+    const long long first = carry + sum - own + (warp ? warp_sum[warp - 1] : 0);
+    const int chunk0 = (int)(first & 0x7ffffff), seg0 = (int)(first >> 27 & 0x7ffffff), cut0 = (int)(first >> 54);
+    const int at = ns > 1 ? atomicAdd(&listed, ns - 1) : 0;  // (the list's order does not matter)
     for (int k = 0; k < ns; ++k) {
       const int c0 = k * seg_chunks;
       const int l = ns == 1 ? len : min(seg_chunks * DR_C, len - c0 * DR_C);
-      seqs[(int)(first >> 32) + k] = DrSeq{tok + c0 * DR_C, l, (int)first + c0, id, k, ns, 0, 0};
+      const DrSeq s{tok + c0 * DR_C, l, chunk0 + c0, id, k, ns, cut0 + k, 0};
+      seqs[seg0 + k] = s;
+      if (k < ns - 1) cuts[at + k] = s;
+      if (k > 0) cuts[max_cuts + at + k - 1] = s;
     }
     __syncthreads();
-    if (tid == 1023) carry = first + both;
+    if (tid == 1023) carry = first + own;
     __syncthreads();
   }
-  const int total = (int)carry, nsegs = (int)(carry >> 32);
+  const int total = (int)(carry & 0x7ffffff), nsegs = (int)(carry >> 27 & 0x7ffffff);
   for (int i = nsegs + tid; i < max_segs; i += 1024) seqs[i] = DrSeq{0, -1, 0, 0, 0, 1, 0, 0};
+  for (int i = listed + tid; i < max_cuts; i += 1024)
+    cuts[i] = cuts[max_cuts + i] = DrSeq{0, -1, 0, 0, 0, 1, 0, 0};
   __threadfence_block();
   __syncthreads();
   for (int c = tid; c < max_chunks; c += 1024) {
@@ -516,8 +558,9 @@ struct StateArgs {
   const uint8_t* kq;
   const uint8_t* blk;
   Guard guard;
-  // segments: [segment][hv][dv][dk] states at their starts and scan results, [segment][hv] transitions (fp16 hi
-  // and lo images [DK][DK], rows scaled) and their rows' inverse scales [segment][hv][DK]
+  // segments of cut sequences (the scan's seqs are those before a cut): [cut][hv][dv][dk] states at their starts and scan
+  // results, [cut][hv] transitions (fp16 hi and lo images [DK][DK], rows scaled) and their rows' inverse scales
+  // [cut][hv][DK]
   float *seg_s, *seg_n;
   uint8_t* phi;
   float* phi_scale;
@@ -715,8 +758,7 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
   const DrSeq sq = a.seqs[si];
   __syncthreads();
   if (sq.len < 0) return;
-  // a last segment's scan has no use, nor has a first one's transition (nor, with two segments, any)
-  if (SCAN && (sq.seg == sq.nseg - 1 || (phi && sq.seg == 0))) return;
+  if (phi && sq.seg == 0) return;  // a first segment's transition has no use (nor has a last one's scan)
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
   auto load_stage = [&](int n) {  // one thread: the chunk's shared operands
@@ -828,7 +870,7 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
   }
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)sq.cut * a.hv + h) * a.dv;
   // a first segment starts from S0 (which the scan keeps: S may be S0, and a last segment may end before the first one
   // starts), the others from the join's state, or in the scan from zero or the unit matrix
   const float* from = sq.nseg > 1 && !SCAN ? a.seg_s + grow * a.dk
@@ -1103,8 +1145,8 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
     }
     const int e0 = row_exp(quad_max(m0), DR_ROW_EXP), e1 = row_exp(quad_max(m1), DR_ROW_EXP);
     if (v0 < DK) {
-      uint8_t* img = a.phi + ((int64_t)si * a.hv + h) * (2 * DK * DK * 2);
-      float* sc = a.phi_scale + ((int64_t)si * a.hv + h) * DK;
+      uint8_t* img = a.phi + ((int64_t)sq.cut * a.hv + h) * (2 * DK * DK * 2);
+      float* sc = a.phi_scale + ((int64_t)sq.cut * a.hv + h) * DK;
       if (t == 0) {
         sc[v0 + g] = inv0 * pow2i(-e0);
         sc[v0 + g + 8] = inv1 * pow2i(-e1);
@@ -1138,9 +1180,9 @@ __global__ void __launch_bounds__(state_threads<DK, PASS>(), 1) k_delta_state(co
 // (of 64 columns of its transpose: the same bytes' rows hold them) through a ring of two stages, and what a
 // segment adds is copied in while its products run: nothing in a step waits for a load of its own.
 struct JoinArgs {
-  const DrSeq* seqs;
+  const DrSeq* seqs;   // the segments before a cut
   int hv, dk, dv;
-  float* seg_s;        // [segment][hv][dv][dk]: start states, or gradients at the ends
+  float* seg_s;        // [cut][hv][dv][dk]: start states, or gradients at the ends
   const float* seg_n;  // what each segment adds
   const uint8_t* phi;
   const float* phi_scale;
@@ -1176,7 +1218,7 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
   __syncthreads();
   if (sq.len < 0 || sq.seg != 0 || sq.nseg < 3) return;
   const int steps = sq.nseg - 2, total = steps * KB;  // segments 1 .. nseg - 2, in this order or from the last
-  auto seg_of = [&](int q) { return si + (REVERSE ? sq.nseg - 2 - q : 1 + q); };
+  auto seg_of = [&](int q) { return sq.cut + (REVERSE ? sq.nseg - 2 - q : 1 + q); };
   auto load = [&](int q) {  // one thread: 64 rows of Phi, hi and lo
     const uint8_t* img = a.phi + ((int64_t)seg_of(q / KB) * a.hv + h) * (2 * DK * DK * 2) + q % KB * BLK;
     uint8_t* st = smem + (q & 1) * 2 * BLK;
@@ -1204,7 +1246,7 @@ __global__ void __launch_bounds__(128, 1) k_delta_join(const JoinArgs a) {
         s[n][2 * p + 1] = v.y;
       }
   };
-  load_s(REVERSE ? si + sq.nseg - 2 : si + 1);
+  load_s(REVERSE ? sq.cut + sq.nseg - 2 : sq.cut + 1);
   if (tid == 0) load(0);
 #pragma unroll 1
   for (int q = 0; q < steps; ++q) {

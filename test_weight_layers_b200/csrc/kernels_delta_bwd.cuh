@@ -42,7 +42,7 @@ struct ReverseArgs {
   float* w_part;   // [chunk][hv][dv / 16][64]: dO.O in, dO.O - dV.V out
   float* b_part;   // [chunk][hv][dv / 16][64] E.Z
   float* x_part;   // [chunk][hv][dv / 16] sum_j U_j . e^{c_C - c_j} dS' k_j
-  // segments: [segment][hv][dv][dk] gradients at their ends (of the segments before the last) and scan results
+  // segments of cut sequences: [cut][hv][dv][dk] gradients at their ends (of the segments before the last) and scan results
   float *seg_ds, *seg_n;
 };
 
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
   const int si = blockIdx.x / (vblocks * a.hv);
   const DrSeq sq = a.seqs[si];
   __syncthreads();
-  if (sq.len < 0 || (SCAN && sq.seg == 0)) return;
+  if (sq.len < 0) return;
   const int nchunk = (sq.len + DR_C - 1) / DR_C;
 
   if (warp == nwarp) {  // the last warp brings the chunks, the last one first
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
   }
 
   float s[NT][4];
-  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)si * a.hv + h) * a.dv;
+  const int64_t srow = ((int64_t)sq.id * a.hv + h) * a.dv, grow = ((int64_t)sq.cut * a.hv + h) * a.dv;
   const float* from = sq.seg == sq.nseg - 1 ? (a.dS ? a.dS + srow * a.dk : nullptr) : SCAN ? nullptr
                                                                                          : a.seg_ds + grow * a.dk;
 #pragma unroll

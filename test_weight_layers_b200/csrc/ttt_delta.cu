@@ -20,7 +20,8 @@ struct DeltaWs {
   uint8_t* kq;
   uint8_t* blk;
   int64_t max_chunks;
-  int seg_chunks, max_segs;  // chunks of a segment (0: sequences are not cut)
+  DrSeq* cuts;  // [2][max_cuts] the segments before and behind each cut
+  int fill, max_segs, max_cuts;
   float *seg_s, *seg_n, *phi_scale;
   uint8_t* phi;
   // backward pass
@@ -46,43 +47,37 @@ bool delta_dims_supported(const ttt_delta_dims& d) {
 // Blocks of 4 warps (64 value channels) that the passes have for each sequence.
 int64_t pass_blocks(const ttt_delta_dims& d) { return (int64_t)d.heads_v * ((d.dv + 63) / 64); }
 
-// Segments.  Uncut, the passes have n_seq * pass_blocks blocks, each on its own SM for the length of a sequence.
-// Cut into k segments a sequence costs 2.6 times the products on k times the blocks, and a chain of k joins, so it is
-// cut where at least 3 segments fit on the card's 148 SMs and the sequences are long enough: 131,072 tokens, 4 heads
-// of 192: the passes take 10.1 ms uncut, 2.1 ms in 12 segments; 1,374 tokens: 117 us, and 78 us in 6.  Eight sequences
-// of 16 heads leave no SM idle and stay whole.  The length that goes into the rule is the mean one; the device cuts
-// each sequence by its own.
+// Segments.  Uncut, the passes have n_seq * pass_blocks blocks, each on its own SM for the length of a sequence; few
+// heads and a long sequence leave most SMs idle.  Such sequences are cut into segments (2.6 times the products, a scan
+// and a join; the rule, which needs the lengths, is k_delta_plan's): 131,072 tokens, 4 heads of 192, take 10.7 ms
+// uncut, 2.56 ms in 12 segments, 1,374 tokens 138 us, and 101 us in 6; 32,768 tokens beside four prompts of 100 take
+// 2.71 ms uncut, 0.76 in 12 segments; 16 heads of 128, 32,768 tokens and 100: 2.1 ms, 1.49 in 4.  Where no sequence
+// is cut after all, the scan and the join end at once (4 and 3 us of packed prompts' 388).
 constexpr int kDeltaSms = 148;
-int seg_chunks(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
-  if (dt != TTT_BF16 || n_seq < 1) return 0;
-  const int64_t blocks = pass_blocks(d) * n_seq, chunks = (T / n_seq + DR_C - 1) / DR_C;
-  const int64_t most = kDeltaSms / blocks;
-  if (most < 3 || chunks < 12) return 0;
-  // short sequences: a join costs about as much as a chunk of both passes, so neither many joins nor long segments
-  int64_t k = (chunks + most - 1) / most;
-  while (k * k * 2 < chunks) ++k;
-  return (int)k;
+
+struct SegRoom {
+  int fill = 0;   // pass_blocks that fit on the card (0: no sequence can be cut)
+  int cuts = 0;   // cuts, at most
+  int segs = 0;   // segments of cut sequences, at most
+};
+
+// With k chunks to a segment, k >= chunks of all sequences / fill and 2 k^2 >= those of the longest: a sequence of n
+// chunks has at most n / k segments beyond the first, so all have `fill` at most, and each sqrt(2 n); fewer than
+// `fill` sequences are longer than k.
+SegRoom seg_room(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
+  SegRoom r;
+  const int64_t fill = dt == TTT_BF16 ? kDeltaSms / pass_blocks(d) : 0;
+  if (fill < 3 || T <= (DR_CUT_CHUNKS - 1) * DR_C) return r;
+  const int64_t chunks = (T + DR_C - 1) / DR_C, some = std::min<int64_t>(n_seq, fill);
+  int64_t root = 1;
+  while (root < fill && root * root < 2 * chunks) ++root;
+  r.fill = (int)fill;
+  r.cuts = (int)std::min(fill, some * root);
+  r.segs = (int)some + r.cuts;
+  return r;
 }
 
-// The most segments of any call with up to T tokens in up to n_seq sequences: a workspace for (T, n_seq) serves fewer
-// and shorter sequences too, and few sequences are cut where many are not.  With k chunks to a segment, n sequences have
-// at most n + (T / 64 + n) / k segments; k >= chunks / most, 2 k^2 >= chunks and chunks >= 12 bound that by
-// n + 13/12 n min(most, sqrt(2 chunks)).
-int64_t seg_cap(const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt) {
-  int64_t cap = 0;
-  for (int64_t n = 1; dt == TTT_BF16 && n <= n_seq; ++n) {
-    const int64_t most = kDeltaSms / (pass_blocks(d) * n), chunks = (T / n + DR_C - 1) / DR_C;
-    if (most < 3 || chunks < 12) break;
-    int64_t root = 1;
-    while (root < most && root * root < 2 * chunks) ++root;
-    cap = std::max(cap, n + n * root * 13 / 12 + 1);
-  }
-  return cap;
-}
-
-// `cap`: room for so many segments (the workspace query), else for this call's.
-DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward,
-                    int64_t cap = -1) {
+DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, ttt_dtype dt, bool backward) {
   DeltaWs w{};
   uint8_t* b = static_cast<uint8_t*>(base);
   size_t off = 0;
@@ -92,18 +87,20 @@ DeltaWs delta_carve(void* base, const ttt_delta_dims& d, int64_t T, int n_seq, t
     return p;
   };
   w.max_chunks = T / DR_C + n_seq;
-  w.seg_chunks = seg_chunks(d, T, n_seq, dt);
-  w.max_segs = n_seq + (w.seg_chunks ? (int)(w.max_chunks / w.seg_chunks) : 0);
+  const SegRoom room = seg_room(d, T, n_seq, dt);
+  w.fill = room.fill;
+  w.max_segs = n_seq + room.cuts;
+  w.max_cuts = room.cuts;
   w.status = reinterpret_cast<unsigned int*>(take(256));
-  const size_t segs_room = cap >= 0 ? cap : w.seg_chunks ? w.max_segs : 0;
-  w.seqs = reinterpret_cast<DrSeq*>(take((n_seq + segs_room + 1) * sizeof(DrSeq)));
+  w.seqs = reinterpret_cast<DrSeq*>(take(((size_t)w.max_segs + 2 * w.max_cuts) * sizeof(DrSeq)));
+  w.cuts = w.seqs + w.max_segs;
   w.chunks = reinterpret_cast<DrChunk*>(take((size_t)std::max<int64_t>(w.max_chunks, 1) * sizeof(DrChunk)));
   if (dt == TTT_BF16) {
     w.kq = take((size_t)w.max_chunks * d.heads_qk * 2 * DR_C * dk_pad(d.dk) * 2);
     w.blk = take((size_t)w.max_chunks * d.heads_v * DR_BLK);
   }
-  if (segs_room) {
-    const size_t segs = segs_room * d.heads_v, dkp = dk_pad(d.dk);
+  if (w.max_cuts) {
+    const size_t segs = (size_t)room.segs * d.heads_v, dkp = dk_pad(d.dk);
     w.seg_s = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
     w.seg_n = reinterpret_cast<float*>(take(segs * d.dv * d.dk * 4));
     w.phi = take(segs * 2 * dkp * dkp * 2);
@@ -173,9 +170,16 @@ int smem_opt_in() {
   return TTT_OK;
 }
 
+// Sequences of equal length need not be looked at to see that none is cut.
+void even_cuts(DeltaWs& w, int64_t T, int n_seq) {
+  if (!w.fill || ((T / n_seq + DR_C - 1) / DR_C >= DR_CUT_CHUNKS && 3ll * n_seq <= w.fill)) return;
+  w.fill = w.max_cuts = 0;
+  w.max_segs = n_seq;
+}
+
 int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaStream_t s) {
-  k_delta_plan<<<1, 1024, 0, s>>>(cu, n_seq, (int)T, w.seg_chunks, w.max_segs, (int)w.max_chunks, w.seqs, w.chunks,
-                                  w.status);
+  k_delta_plan<<<1, 1024, 0, s>>>(cu, n_seq, (int)T, w.fill, w.max_segs, w.max_cuts, (int)w.max_chunks, w.seqs, w.cuts,
+                                  w.chunks, w.status);
   TTT_LAUNCHED();
   return TTT_OK;
 }
@@ -204,16 +208,17 @@ int64_t blocks_of(int rows, int warps) { return (rows + 16 * warps - 1) / (16 * 
 
 template <int DK, bool REVERSE>
 int launch_join(const StateArgs& sa, float* seg_s, const DeltaWs& w, cudaStream_t s) {
-  JoinArgs ja{sa.seqs, sa.hv, sa.dk, sa.dv, seg_s, w.seg_n, w.phi, w.phi_scale, sa.guard};
-  return launch_pass<k_delta_join<DK, REVERSE>>(ja, w.max_segs, (sa.dv + 63) / 64, 4, join_smem<DK>(), s);
+  JoinArgs ja{w.cuts, sa.hv, sa.dk, sa.dv, seg_s, w.seg_n, w.phi, w.phi_scale, sa.guard};
+  return launch_pass<k_delta_join<DK, REVERSE>>(ja, w.max_cuts, (sa.dv + 63) / 64, 4, join_smem<DK>(), s);
 }
 
-// The states at the segments' starts (nothing to do for uncut sequences).
+// The states at the starts of cut sequences' segments.
 template <int DK>
-int run_scan(const StateArgs& sa, const DeltaWs& w, cudaStream_t s) {
-  if (!w.seg_chunks) return TTT_OK;
+int run_scan(StateArgs sa, const DeltaWs& w, cudaStream_t s) {
+  if (!w.max_cuts) return TTT_OK;
   const int warps = pass_warps<DK>(false);
-  TTT_TRY((launch_pass<k_delta_state<DK, PASS_SCAN>>(sa, w.max_segs, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
+  sa.seqs = w.cuts;
+  TTT_TRY((launch_pass<k_delta_state<DK, PASS_SCAN>>(sa, w.max_cuts, blocks_of(sa.dv, warps) + blocks_of(DK, warps),
                                                    warps + 1, state_smem<DK, PASS_SCAN>(warps), s)));
   return launch_join<DK, false>(sa, w.seg_s, w, s);
 }
@@ -244,8 +249,10 @@ int run_delta_bwd(const PrepArgs& pa, const StateArgs& sa, const ReverseArgs& ra
   const int warps = pass_warps_for(pass_warps<DK>(true), sa.dv), smem = state_smem<DK, PASS_BACK>(warps, true);
   const int64_t blocks = blocks_of(sa.dv, warps);
   TTT_TRY((launch_pass<k_delta_state<DK, PASS_BACK>>(sa, w.max_segs, blocks, warps + 1, smem, s)));
-  if (w.seg_chunks) {  // the transitions are the state pass's, transposed
-    TTT_TRY((launch_pass<k_delta_reverse<DK, true>>(ra, w.max_segs, blocks, warps + 1, smem, s)));
+  if (w.max_cuts) {  // the transitions are the state pass's, transposed
+    ReverseArgs scan = ra;
+    scan.seqs = w.cuts + w.max_cuts;
+    TTT_TRY((launch_pass<k_delta_reverse<DK, true>>(scan, w.max_cuts, blocks, warps + 1, smem, s)));
     TTT_TRY((launch_join<DK, true>(sa, w.seg_s, w, s)));
   }
   TTT_TRY((launch_pass<k_delta_reverse<DK, false>>(ra, w.max_segs, blocks, warps + 1, smem, s)));
@@ -382,7 +389,7 @@ size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_
   if ((dtype != TTT_FP32 && dtype != TTT_BF16) || !delta_dims_ok(dims) || !delta_dims_supported(dims) || T < 0 ||
       T > INT32_MAX - DR_C || n_seq < 0 || n_seq > kDeltaMaxSeqs)
     return 0;
-  return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0, seg_cap(dims, T, n_seq, dtype)).total;
+  return delta_carve(nullptr, dims, T, n_seq, dtype, backward != 0).total;
 }
 
 int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
@@ -397,7 +404,8 @@ int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* 
   if ((S0 && !aligned16(S0)) || (S && !aligned16(S)) || !aligned4(cu_seqlens)) return TTT_ERR_ALIGN;
   if (n_seq == 0) return TTT_OK;
   cudaStream_t s = (cudaStream_t)stream;
-  const DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, false);
+  DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, false);
+  if (!cu_seqlens) even_cuts(w, T, n_seq);
   ProfScope ps(TTT_PROF_DELTA, s);
   TTT_TRY(launch_plan(cu_seqlens, n_seq, T, w, s));
   if (dtype == TTT_FP32 || T <= kTokensMost) {
@@ -444,7 +452,8 @@ int ttt_delta_chunked_backward(const void* Q, const void* K, const void* V, cons
   }
   if (n_seq == 0) return TTT_OK;
   cudaStream_t s = (cudaStream_t)stream;
-  const DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, true);
+  DeltaWs w = delta_carve(ws, dims, T, n_seq, dtype, true);
+  if (!cu_seqlens) even_cuts(w, T, n_seq);
   ProfScope ps(TTT_PROF_DELTA, s);
   TTT_TRY(launch_plan(cu_seqlens, n_seq, T, w, s));
   const PrepArgs pa = prep_args(Q, K, g, beta, scale, dims, x, w);

@@ -136,3 +136,55 @@ def test_a_nan_stays_in_its_sequence_on_the_way_back():
             rows = slice(c.starts[i], c.starts[i + 1])
             assert all(torch.equal(out[k][rows], clean[k][rows]) for k in ("dq", "dk", "dv", "dg", "dbeta"))
             assert torch.equal(out["dS0"][i], clean["dS0"][i])
+
+
+def test_short_neighbours_leave_a_long_sequence_cut():
+    # whether a sequence is cut goes by the lengths themselves: with and without a few tokens beside it, a long one
+    # runs in segments of the same size, to the last bit
+    # (the gates hold the state over several segments, so that uncut sums differ from joined ones)
+    alone = Seqs([32000], 4, 4, 192, 192, seed=48, decay=1e-4)
+    c = Seqs([1, 32000, 0, 1, 1, 1], 4, 4, 192, 192, seed=49)
+    for name in ("Q", "K", "V", "g", "beta", "dO"):
+        getattr(c, name)[1:32001] = getattr(alone, name)
+    for name in ("S0", "dS"):
+        getattr(c, name)[1] = getattr(alone, name)[0]
+    O, S, _ = alone.forward()
+    O2, S2, ws = c.forward()
+    assert T.ttt_poll_status(ws) == T.TTT_OK and torch.equal(O2[1:32001], O) and torch.equal(S2[1], S[0])
+    out, _ = alone.backward()
+    out2, ws = c.backward()
+    assert T.ttt_poll_status(ws) == T.TTT_OK and torch.equal(out2["dS0"][1], out["dS0"][0])
+    assert all(torch.equal(out2[k][1:32001], out[k]) for k in ("dq", "dk", "dv", "dg", "dbeta"))
+
+
+@pytest.mark.parametrize("lens,hk,hv,dk,dv", [([3000, 1, 0, 64, 100, 2999], 1, 1, 64, 64),
+                                              ([20, 65, 1500, 64, 0, 129], 1, 2, 192, 64),
+                                              ([0, 0, 800, 0, 0, 0, 0, 0], 1, 3, 128, 128),
+                                              ([768] * 5 + [2500], 1, 1, 40, 16),
+                                              ([900, 30], 1, 1, 256, 200)])
+def test_ragged_batches_in_segments(lens, hk, hv, dk, dv):
+    for s0 in (False, True):
+        c = Seqs(lens, hk, hv, dk, dv, seed=50 + dk, s0=s0, lead=2, tail=3, decay=0.003)
+        O, S, ws = c.forward()
+        assert T.ttt_poll_status(ws) == T.TTT_OK and torch.all(O[:2] == 77) and torch.all(O[-3:] == 77)
+        c.check_forward(O, S)
+        out, ws = c.backward()
+        assert T.ttt_poll_status(ws) == T.TTT_OK
+        c.check_backward(out)
+    state = c.S0.clone()  # in place
+    O2, _, _ = c.forward(S=state, S0=state)
+    assert torch.equal(O, O2) and torch.equal(S, state)
+
+
+def test_equal_sequences_without_offsets_in_segments():
+    # two sequences are cut, forty fill the card as they are; without offsets that is known before the launch
+    for n, length in ((2, 900), (40, 900), (3, 130)):
+        c = Seqs([length] * n, 1, 2, 64, 64, seed=51)
+        O, S, _ = c.forward()
+        O2, S2, ws = c.forward(cu=None)
+        assert T.ttt_poll_status(ws) == T.TTT_OK and torch.equal(O, O2) and torch.equal(S, S2)
+        out, _ = c.backward()
+        cu, c.cu = c.cu, None
+        out2, ws = c.backward()
+        c.cu = cu
+        assert T.ttt_poll_status(ws) == T.TTT_OK and all(torch.equal(out[k], out2[k]) for k in out)
