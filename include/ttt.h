@@ -299,9 +299,10 @@ int ttt_layer_host(ttt_weights W, const void* hQ, const void* hK, const void* hV
  *  - Token by token (ttt_delta_step, TTT_FP32, bf16 calls of up to 40 tokens) the
  *    L2 norms are summed in fp32: rows of norm above 1.8e19 count as zero there.
  *    The chunked bf16 form scales each row first and takes any finite one.
- *  - A non-finite token, gate (other than g = -inf) or state makes undefined the outputs of its chunk
- *    of 64 tokens (earlier tokens of that chunk too) and of all later tokens of
- *    its sequence and head; other sequences are not touched by it.
+ *  - A non-finite token, gate (other than g = -inf) or state makes undefined the
+ *    outputs of its chunk of 64 tokens (earlier tokens of that chunk too) and of
+ *    all later tokens of its sequence and head, and all gradients of that sequence
+ *    and head; other sequences are not touched by it.
  *  - Outputs may not overlap inputs or each other, except that S may be S0.
  *  - All buffers are on the current device. */
 typedef struct { int heads_qk, heads_v, dk, dv; } ttt_delta_dims;
@@ -311,7 +312,10 @@ typedef struct { int heads_qk, heads_v, dk, dv; } ttt_delta_dims;
  * n_seq sequences; 256-byte aligned, its status word cleared once
  * (ttt_reset_status) before the first call and read with ttt_poll_status.
  * Calls that can overlap, and captured graphs that can replay at the same
- * time, need a workspace each.  Returns 0 for invalid dims. */
+ * time, need a workspace each.  Returns 0 for invalid dims.  The gradient keeps
+ * two float states and two float rows of errors for every 64 tokens of each value
+ * head: 8 query/key and 16 value heads of 128, 131,072 tokens: 1.7 GB forward,
+ * 8.3 GB with backward; 4 heads of 192, 32,768 tokens: 0.2 and 1.0 GB. */
 size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_dtype dtype, int backward);
 
 /* The rule over n_seq packed sequences, in chunks of 64 tokens.
@@ -325,8 +329,8 @@ size_t ttt_delta_workspace_bytes(ttt_delta_dims dims, int64_t T, int n_seq, ttt_
  *    S: state after each (a sequence of length 0 keeps S0), may be S0 itself
  *    or NULL.  Passing S as the next call's S0 resumes the sequences.
  *  - TTT_BF16: bf16 Q, K, V, O on the tensor cores, with fp32-precise products
- *    (operands split in two fp16 parts; calls of up to 40 tokens on the CUDA
- *    cores); TTT_FP32: float Q, K, V, O, token by token on the CUDA cores (the
+ *    (operands in two fp16 parts, for dQ and dK of the gradient in two TF32 parts:
+ *    2^-21 of each term; calls of up to 40 tokens on the CUDA cores); TTT_FP32: float Q, K, V, O, token by token on the CUDA cores (the
  *    precision check, and short sequences).
  *  - T up to 2^31 - 65, n_seq up to 2^24 (TTT_ERR_UNSUPPORTED beyond). */
 int ttt_delta_chunked(const void* Q, const void* K, const void* V, const float* g, const float* beta, const float* S0,
@@ -376,7 +380,9 @@ int ttt_delta_step(const void* Q, const void* K, const void* V, const float* g, 
  *    cfg (elements; 0 means D).  Any alignment of the element type works;
  *    16-byte aligned rows and D, group multiples of 8 run with 16-byte accesses.
  *  - An output may be one of the inputs (same pointer and stride), else they may
- *    not overlap.  Arithmetic is fp32, each output rounded once.
+ *    not overlap.  Arithmetic is fp32, each output rounded once; SiLU of bf16 rows
+ *    by the hardware's exponential and reciprocal (2^-21 of it for |z| below 8,
+ *    2^-17 where it vanishes).
  *  - D <= 8192; group divides D and is D or a multiple of 8. */
 typedef struct { int D, group; float eps; int64_t ld_x, ld_y, ld_z, ld_xout, ld_n; } ttt_norm_cfg;
 

@@ -9,8 +9,19 @@
 //     dz = dp y r_y w_post s'(z);   u = dp w_post s;   dy = r_y (u - y r_y mean(u y r_y))
 //     dw_pre = sum dn x' r;  dlambda = sum D_x' p;  dw_post = sum dp y r_y s
 // The row stays in registers between its reductions, so each tensor crosses
-// HBM once: the kernels are bound by those bytes.  All arithmetic is fp32, rounded
-// once on the way out.
+// HBM once.  All arithmetic is fp32, rounded once on the way out.
+//
+// Share of the copy rate (6.46 TB/s) with all operands, bf16 | fp32:
+//                         forward       gradient
+//     131,072 x   768   0.89 | 0.68   0.62 | 0.58
+//      65,536 x 2,048   0.83 | 0.97   0.79 | 0.51
+//      16,384 x 8,192   0.57 | 0.61   0.25 | 0.21
+// The bf16 forward and the bf16 gradient at 2,048 columns are bound by those bytes.
+// What is far below spills registers in its row loop: the fp32 gradient (224 to 524
+// bytes a thread), the gradient of more than 4,096 columns, whose 512 threads have
+// 128 registers for two chunks each (976 to 1,592), and the fp32 forward with three
+// chunks to a thread, as for 768 columns (148 to 392, under the bound of four blocks
+// an SM); the bf16 gradient with one chunk to a thread spills 24 to 156.
 #pragma once
 
 #include "common.cuh"
@@ -223,8 +234,9 @@ struct RowAt {
   }
 };
 
-// The logistic function.  bf16 rows take the hardware's exponential and reciprocal (2^-21, far below the outputs'
-// rounding): the exact ones are a third of the instructions of a pass that is otherwise bound by HBM.
+// The logistic function.  bf16 rows take the hardware's exponential and reciprocal (2^-21 for |z| below 8, 2^-17 at -88
+// where it vanishes: far below the outputs' rounding, and what the weights' gradients take from it is that of single
+// rows): the exact ones are a third of the instructions of a pass that is otherwise bound by HBM.
 template <typename T>
 __device__ __forceinline__ float sigmoid_f(float z) {
   if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
@@ -232,7 +244,7 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 }
 
 // TPR threads to a row, NV chunks of 8 columns to a thread; GROUPS: several means of y to a row.
-// Measured (131,072 x 768, bf16, all operands): 175 us, 5.75 TB/s; without the loads ahead 208 us.
+// Measured (131,072 x 768, bf16, all operands): 176 us, 5.73 TB/s; without the loads ahead 208 us.
 template <typename T, int TPR, int NV, bool GROUPS, bool VEC>
 __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, NV <= 3 ? 4 * 128 / (TPR > 128 ? TPR : 128) : 1) k_block_norm(const NormArgs<T> a) {
   constexpr int BLOCK = TPR > 128 ? TPR : 128;

@@ -29,8 +29,8 @@ struct DeltaWs {
   size_t total;
 };
 
-// bf16 calls of so few tokens run token by token: one short kernel instead of the chunks' three (4 heads of 192:
-// 16 us against 26 us for 32 tokens, 28 against 26 for 64; 16 heads of 128: 17 against 27, 29 against 27).
+// bf16 calls of so few tokens run token by token: one short kernel instead of the chunks' three (4 heads of 192: 19 us
+// against 33 us for 32 tokens, 33 and 33 for 64; 16 heads of 128: 19 against 27, 31 and 27).
 constexpr int64_t kTokensMost = 40;
 constexpr int kDeltaMaxSeqs = 1 << 24;
 
@@ -185,9 +185,9 @@ int launch_plan(const int32_t* cu, int n_seq, int64_t T, const DeltaWs& w, cudaS
 }
 
 // Row warps of a pass block (16 value channels each): four, one to a sub-partition of the SM.  A warp's chain of
-// products is bound by its own latency, so eight on an SM run at 0.6 of the speed each (state pass of packed prompts
-// of 16 heads: 435 us with 8, 260 with 4; with 2, which share a staged copy of the operands with fewer, 353); two where
-// shared memory holds no more (dk = 256 on the way back).
+// products is bound by its own latency, so eight on an SM ran at 0.6 of the speed each (state pass of packed prompts
+// of 16 heads, taken with the row warps making the outputs as well: 435 us with 8, 260 with 4; with 2, which share a
+// staged copy of the operands with fewer, 353); two where shared memory holds no more (dk = 256 on the way back).
 template <int DK>
 constexpr int pass_warps(bool back) {
   return back && DK > 192 ? 2 : 4;
