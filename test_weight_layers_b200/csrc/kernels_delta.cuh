@@ -10,8 +10,8 @@ namespace ttt {
 // ---------------------------------------------------------------------------
 // Chunk table.  One block: checks the offsets (0 <= cu[i] <= cu[i+1] <= T), cuts
 // long sequences into segments (fill: sequences' passes that fit on the card; 0:
-// none is cut), and writes the segments, the two on each side of a cut once more by
-// themselves, and each chunk's first token and length.  Refused offsets, or an
+// none is cut), and writes the segments, those before and those behind a cut once
+// more by themselves, and each chunk's first token and length.  Refused offsets, or an
 // error already recorded in the status word, mark every segment with length -1:
 // the kernels after it then write nothing.
 //

@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(160, 1) k_delta_reverse(const ReverseArgs a) {
 // documents 279 us instead of 440), but keeps 2^-11 of the terms where they
 // cancel, as behind a key that is written again.  32 value channels at a time
 // are copied in while the 32 before are multiplied.
-// Bound by the tensor cores and one block's phases on an SM (252 registers):
-// 56% tensor pipe, 0.31 issue slots.
+// Bound by the tensor cores and one block's phases on an SM (255 registers):
+// 55% tensor pipe, 0.31 issue slots.
 struct GradArgs {
   const __nv_bfloat16 *dO;
   int64_t ldo, ldq, ldk;

@@ -51,8 +51,9 @@ int64_t pass_blocks(const ttt_delta_dims& d) { return (int64_t)d.heads_v * ((d.d
 // heads and a long sequence leave most SMs idle.  Such sequences are cut into segments (2.6 times the products, a scan
 // and a join; the rule, which needs the lengths, is k_delta_plan's): 131,072 tokens, 4 heads of 192, take 10.7 ms
 // uncut, 2.56 ms in 12 segments, 1,374 tokens 138 us, and 101 us in 6; 32,768 tokens beside four prompts of 100 take
-// 2.71 ms uncut, 0.76 in 12 segments; 16 heads of 128, 32,768 tokens and 100: 2.1 ms, 1.49 in 4.  Where no sequence
-// is cut after all, the scan and the join end at once (4 and 3 us of packed prompts' 388).
+// 2.71 ms uncut, 0.76 in 12 segments; 16 heads of 128, 32,768 tokens and 100: 2.29 ms, 1.49 in 4.  Where no sequence
+// is cut after all, the scan and the join end at once (4 and 3 us of packed prompts' 388; four prompts of 700 tokens, 4
+// heads of 192: 86 us without them, 92 with).
 constexpr int kDeltaSms = 148;
 
 struct SegRoom {
